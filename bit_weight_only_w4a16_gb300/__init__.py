@@ -27,7 +27,8 @@ STATUS_NAMES = {0: "W4_OK", 1: "W4_ERR_INVALID_ARG", 2: "W4_ERR_UNSUPPORTED",
 EXPORTS = ("w4_status_string", "w4_last_cuda_error", "w4_init", "w4_device_error", "w4a16_gemv", "w4a16_gemm",
            "w4a16_gemv_argmax", "w4a16_gemv_argmax_noalloc", "w4_embed_gather", "hbm_read_probe",
            "w4_attn_decode", "w4a16_gemv_hadamard", "w4_selftest_wait_timeout", "w4_attn_decode_devpos",
-           "w4_kv_append", "w4a16_gemv_argmax_forced", "w4_decode_prologue")
+           "w4_kv_append", "w4a16_gemv_argmax_forced", "w4_decode_prologue", "w4_attn_prompt", "w4_attn_tree",
+           "w4_logprobs", "w4_kv_commit")
 
 
 class W4Error(RuntimeError):
@@ -76,6 +77,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_gemv_argmax_forced.restype = I
     lib.w4_decode_prologue.argtypes = [P, P, P, P, P, P, I, I, I, I, P, P]
     lib.w4_decode_prologue.restype = I
+    L, F = ctypes.c_longlong, ctypes.c_float
+    lib.w4_attn_prompt.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, L, L, L, L, I, F, P]
+    lib.w4_attn_prompt.restype = I
+    lib.w4_attn_tree.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P]
+    lib.w4_attn_tree.restype = I
+    lib.w4_logprobs.argtypes = [P, P, P, P, P, P, I, I, L, I, P, P]
+    lib.w4_logprobs.restype = I
+    lib.w4_kv_commit.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P]
+    lib.w4_kv_commit.restype = I
     return lib
 
 
@@ -314,3 +324,120 @@ def w4_decode_prologue(token, pos, qtable, scales, group: int = 32, x_next=None,
     _check(_lib.w4_decode_prologue(_ptr(o), _ptr(tokens), _ptr(pos), _ptr(token), _ptr(qtable), _ptr(scales), V, K,
                                    group, cap, _ptr(status), _stream(stream)), "w4_decode_prologue")
     return o
+
+
+def _rows16(t, name, heads=None, D=None):
+    """A bf16 [rows][heads][D] tensor whose rows may be strided (a view of a wider
+    projection); returns the elements between rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"{name} must be bf16 (or its raw 16-bit bits)")
+    if t.dim() != 3 or (D is not None and t.shape[2] != D) or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows][heads][D]")
+    s = t.stride()
+    if (t.shape[2] > 1 and s[2] != 1) or (t.shape[1] > 1 and s[1] != t.shape[2]):
+        raise ValueError(f"{name}: heads and D must be contiguous")
+    return s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * t.shape[2])
+
+
+def _i32(t, name, n):
+    _cuda(t, name)
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{name} must be int32 with {n} elements")
+    return t
+
+
+def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0, out=None, stream=None):
+    """bf16 [total_q][Hq][D]: causal attention of packed prompts (or chunks of them).
+
+    q bf16 [total_q][Hq][D]; k, v bf16 [total_k][Hkv][D] (rows may be strided);
+    cu_q, cu_k int32 [B + 1]: the sequences' first rows (cu_k None: as cu_q). A
+    sequence's queries are the last of its keys' positions; window 0 = no window.
+    """
+    ldq = _rows16(q, "q")
+    Sq, Hq, D = q.shape
+    ldk = _rows16(k, "k", D=D)
+    Sk, Hkv, _ = k.shape
+    ldv = _rows16(v, "v", Hkv, D)
+    if v.shape[0] != Sk:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}")
+    B = cu_q.numel() - 1
+    _i32(cu_q, "cu_q", B + 1)
+    if cu_k is not None:
+        _i32(cu_k, "cu_k", B + 1)
+    o = torch.empty((Sq, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    ldo = _rows16(o, "out", Hq, D)
+    if o.shape[0] != Sq:
+        raise ValueError(f"out must be [{Sq}][{Hq}][{D}]")
+    _check(_lib.w4_attn_prompt(_ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), B, Sq, Sk, Hq, Hkv, D,
+                               ldq, ldk, ldv, ldo, int(window), float(scale), _stream(stream)), "w4_attn_prompt")
+    return o
+
+
+def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int = 0, scale: float = 1.0, out=None,
+                 stream=None):
+    """bf16 [B][N][Hq][D]: attention of a tree of N <= 64 drafted tokens per sequence
+    over the cache k, v bf16 [B][T][Hkv][D] and the tree's own k_tree, v_tree
+    [B][N][Hkv][D].
+
+    parents int32 [B][N] (-1 = first level, -2 = absent); pos int32 [B]: the first
+    level's position (cached positions below it are kept); kpos int32 [B][T]
+    recorded positions of a ring, or None (slot t holds position t).
+    """
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_tree, "k_tree"), (v_tree, "v_tree")):
+        _bits16(t, n)
+    B, N, Hq, D = q.shape
+    T, Hkv = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (B, T, Hkv, D) or v.shape != k.shape or tuple(k_tree.shape) != (B, N, Hkv, D) or \
+            v_tree.shape != k_tree.shape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
+                         f"k_tree {tuple(k_tree.shape)}, v_tree {tuple(v_tree.shape)}")
+    _i32(parents, "parents", B * N)
+    _i32(pos, "pos", B)
+    if kpos is not None:
+        _i32(kpos, "kpos", B * T)
+    o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else _bits16(out, "out")
+    if tuple(o.shape) != (B, N, Hq, D):
+        raise ValueError(f"out must be [{B}][{N}][{Hq}][{D}]")
+    _check(_lib.w4_attn_tree(_ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(kpos), _ptr(k_tree), _ptr(v_tree),
+                             _ptr(parents), _ptr(pos), B, N, T, Hq, Hkv, D, int(window), float(scale),
+                             _stream(stream)), "w4_attn_tree")
+    return o
+
+
+def w4_logprobs(logits, targets=None, topk: int = 0, status=None, stream=None):
+    """(logprob [M] or None, entropy [M], top_logprob [M][topk], top_id [M][topk]) of
+    fp32 logits [M][V] (rows may be strided) and int32 targets [M]."""
+    if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
+    M, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("a row of logits must be contiguous")
+    ld = logits.stride(0) if M > 1 else max(logits.stride(0), V)
+    if targets is not None:
+        _i32(targets, "targets", M)
+    k = int(topk)
+    dev = logits.device
+    f = torch.empty((2 + max(k, 0), M), dtype=torch.float32, device=dev)
+    lp, ent, top = (f[0] if targets is not None else None), f[1], f[2:].view(M, max(k, 0))
+    ids = torch.empty((M, max(k, 0)), dtype=torch.int32, device=dev)
+    _check(_lib.w4_logprobs(_ptr(lp), _ptr(ent), _ptr(top) if k > 0 else None, _ptr(ids) if k > 0 else None,
+                            _ptr(logits), _ptr(targets), M, V, ld, k, _ptr(status), _stream(stream)), "w4_logprobs")
+    return lp, ent, top, ids
+
+
+def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, status=None, stream=None):
+    """Store the accepted tokens: rows path[b][j] (j < count[b]) of the trees k_tree,
+    v_tree bf16 [L][B][N][W] become position pos[b] + j of the caches [L][B][T][W]
+    (a ring when kpos int32 [B][T] is given: it records the positions)."""
+    _bits16(k_cache, "k_cache"); _bits16(v_cache, "v_cache"); _bits16(k_tree, "k_tree"); _bits16(v_tree, "v_tree")
+    L, B, T, W = k_cache.shape
+    N = k_tree.shape[2]
+    if v_cache.shape != k_cache.shape or tuple(k_tree.shape) != (L, B, N, W) or v_tree.shape != k_tree.shape:
+        raise ValueError("cache / tree shape mismatch")
+    _i32(path, "path", B * N); _i32(count, "count", B); _i32(pos, "pos", B)
+    if kpos is not None:
+        _i32(kpos, "kpos", B * T)
+    _check(_lib.w4_kv_commit(_ptr(k_cache), _ptr(v_cache), _ptr(kpos), _ptr(k_tree), _ptr(v_tree), _ptr(path),
+                             _ptr(count), _ptr(pos), L, B, N, T, W, _ptr(status), _stream(stream)), "w4_kv_commit")

@@ -17,6 +17,13 @@ constexpr int kMaxDevices = 64;
 constexpr size_t kKeyCapacity = 8u * 65536u;
 // Prefill split-K scratch: 8 Mi fp32 partials (32 MiB).
 constexpr size_t kWsFloats = 8u << 20;
+// The same allocation is the scratch of the tiled attention (two partial row
+// tiles per SM, about 39 MiB) and of the log probabilities.
+size_t ws_capacity(int num_sms)
+{
+    const size_t n = w4::attn_ws_floats(num_sms);
+    return n > kWsFloats ? n : kWsFloats;
+}
 
 struct DeviceState {
     // Set (release) once the fields below are written; read (acquire) first.
@@ -24,7 +31,7 @@ struct DeviceState {
     int num_sms = 0;
     unsigned long long *keys = nullptr;
     int *err = nullptr; // device error word written by kernels whose bounded waits ran out
-    float *ws = nullptr; // prefill split-K partials
+    float *ws = nullptr; // prefill split-K and attention partials, ws_capacity(num_sms) floats
 };
 
 DeviceState g_dev[kMaxDevices];
@@ -76,7 +83,7 @@ int device_state(DeviceState **out)
         if (e != cudaSuccess)
             return cuda_fail(e);
         void *w = nullptr;
-        e = cudaMalloc(&w, kWsFloats * sizeof(float));
+        e = cudaMalloc(&w, ws_capacity(sms) * sizeof(float));
         if (e != cudaSuccess)
             return cuda_fail(e);
         st.ws = static_cast<float *>(w);
@@ -107,6 +114,18 @@ int check_attn_args(const float *out, const uint16_t *q, const uint16_t *k, cons
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 4) ||
         (kpos && !aligned(kpos, 4)))
         return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+// Head layout, width, window and scale of the tiled attention calls.
+int check_heads(int Hq, int Hkv, int D, int window, float scale)
+{
+    if (Hq < 1 || Hkv < 1 || D < 1 || window < 0 || !(scale > 0.f) || !(scale <= 3.4e38f))
+        return W4_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0)
+        return W4_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || !(D == 64 || D == 128 || D == 256 || D == 384 || D == 512))
+        return W4_ERR_UNSUPPORTED;
     return W4_OK;
 }
 
@@ -488,6 +507,157 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
     cudaError_t e = w4::run_decode_prologue(x_next, tokens, pos, token, qtable, scales, V, K,
                                             w4::group_shift(group), tokens ? cap : 0, status,
                                             static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                   const int32_t *cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int D, long long ldq,
+                   long long ldk, long long ldv, long long ldo, int window, float scale, void *stream)
+{
+    if (!out || !q || !k || !v || !cu_q)
+        return W4_ERR_INVALID_ARG;
+    if (B < 1 || total_q < 1 || total_k < 1)
+        return W4_ERR_INVALID_ARG;
+    int rc = check_heads(Hq, Hkv, D, window, scale);
+    if (rc != W4_OK)
+        return rc;
+    if (B > 4096)
+        return W4_ERR_UNSUPPORTED;
+    const long long wq = (long long)Hq * D, wk = (long long)Hkv * D, most = (1ll << 31) - 1;
+    if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || ldq > most || ldk > most || ldv > most || ldo > most)
+        return W4_ERR_INVALID_ARG;
+    if (ldq % 8 != 0 || ldk % 8 != 0 || ldv % 8 != 0 || ldo % 8 != 0)
+        return W4_ERR_MISALIGNED;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_q, 4) ||
+        (cu_k && !aligned(cu_k, 4)))
+        return W4_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st)) != W4_OK)
+        return rc;
+    w4::AttnPromptArgs p = {};
+    p.out = out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k ? cu_k : cu_q;
+    p.B = B;
+    p.total_q = total_q;
+    p.total_k = total_k;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.ldo = ldo;
+    p.window = window;
+    p.scale = scale;
+    cudaError_t e = w4::run_attn_prompt(p, st->ws, st->err, st->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kpos,
+                 const uint16_t *k_tree, const uint16_t *v_tree, const int32_t *parents, const int32_t *pos, int B,
+                 int N, int T, int Hq, int Hkv, int D, int window, float scale, void *stream)
+{
+    if (!out || !q || !k || !v || !k_tree || !v_tree || !parents || !pos)
+        return W4_ERR_INVALID_ARG;
+    if (B < 1 || N < 1 || T < 1)
+        return W4_ERR_INVALID_ARG;
+    int rc = check_heads(Hq, Hkv, D, window, scale);
+    if (rc != W4_OK)
+        return rc;
+    if (B > 4096 || N > 64)
+        return W4_ERR_UNSUPPORTED;
+    if ((long long)B * T >= (1ll << 31) || (long long)Hq * D >= (1ll << 31))
+        return W4_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_tree, 16) ||
+        !aligned(v_tree, 16) || !aligned(parents, 4) || !aligned(pos, 4) || (kpos && !aligned(kpos, 4)))
+        return W4_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st)) != W4_OK)
+        return rc;
+    w4::AttnTreeArgs p = {};
+    p.out = out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.kpos = kpos;
+    p.k_tree = k_tree;
+    p.v_tree = v_tree;
+    p.parents = parents;
+    p.pos = pos;
+    p.B = B;
+    p.N = N;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.window = window;
+    p.scale = scale;
+    cudaError_t e = w4::run_attn_tree(p, st->ws, st->err, st->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top_id, const float *logits,
+                const int32_t *targets, int M, int V, long long ld, int topk, int32_t *status, void *stream)
+{
+    if (!logits || (logprob && !targets))
+        return W4_ERR_INVALID_ARG;
+    if (M < 1 || V < 1 || ld < V || topk < 0)
+        return W4_ERR_INVALID_ARG;
+    if (topk > 32)
+        return W4_ERR_UNSUPPORTED;
+    if (!aligned(logits, 4) || (targets && !aligned(targets, 4)) || (logprob && !aligned(logprob, 4)) ||
+        (entropy && !aligned(entropy, 4)) || (top_logprob && !aligned(top_logprob, 4)) ||
+        (top_id && !aligned(top_id, 4)) || (status && !aligned(status, 4)))
+        return W4_ERR_MISALIGNED;
+    if (!logprob && !entropy && (topk == 0 || (!top_logprob && !top_id)))
+        return W4_ERR_INVALID_ARG; // nothing to compute
+    DeviceState *st = nullptr;
+    int rc = device_state(&st);
+    if (rc != W4_OK)
+        return rc;
+    w4::LogprobsArgs p = {};
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.top_logprob = top_logprob;
+    p.top_id = top_id;
+    p.logits = logits;
+    p.targets = targets;
+    p.M = M;
+    p.V = V;
+    p.ld = ld;
+    p.k = top_logprob || top_id ? topk : 0;
+    p.status = status;
+    cudaError_t e = w4::run_logprobs(p, st->ws, ws_capacity(st->num_sms), st->num_sms,
+                                     static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported)
+        return W4_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint16_t *k_tree,
+                 const uint16_t *v_tree, const int32_t *path, const int32_t *count, const int32_t *pos, int L, int B,
+                 int N, int T, int W, int32_t *status, void *stream)
+{
+    if (!k_cache || !v_cache || !k_tree || !v_tree || !path || !count || !pos)
+        return W4_ERR_INVALID_ARG;
+    if (L < 1 || B < 1 || N < 1 || T < 1 || W < 8 || W % 8 != 0 || (long long)L * B >= (1ll << 31))
+        return W4_ERR_INVALID_ARG;
+    if (N > 64)
+        return W4_ERR_UNSUPPORTED;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_tree, 16) || !aligned(v_tree, 16) ||
+        !aligned(path, 4) || !aligned(count, 4) || !aligned(pos, 4) || (kpos && !aligned(kpos, 4)) ||
+        (status && !aligned(status, 4)))
+        return W4_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    int rc = device_state(&st);
+    if (rc != W4_OK)
+        return rc;
+    const w4::KvCommitArgs a = {k_cache, v_cache, kpos, k_tree, v_tree, path, count, pos, L, B, N, T, W, status};
+    cudaError_t e = w4::run_kv_commit(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? W4_OK : cuda_fail(e);
 }
 

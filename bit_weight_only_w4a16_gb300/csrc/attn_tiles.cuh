@@ -1,0 +1,1135 @@
+// Tiled attention on the 5th-generation tensor cores: the kernel behind the
+// prompt attention and the tree attention (which differ in what a query row may
+// see, not in the arithmetic).
+//
+// Mathematics. For a row (query token, query head) with kept keys t:
+//   s_t = c q.k_t (c = scale * log2 e),  out = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m)
+// for any m; one pass keeps m near the running maximum. m moves only when the
+// maximum has grown by more than 2^8 (a weight is then at most 256, which bf16
+// holds with the same relative error), so the accumulator in tensor memory is
+// rarely rescaled. Weights are rounded to bf16 (relative 2^-9) for the tensor
+// core's value product: the output is bf16, whose own rounding is as large. The
+// sum of the weights, m and the accumulator are fp32.
+//
+// Rows. The G query heads of one key/value head share its keys, so a tile's 128
+// rows are (token, head) pairs, 128 / G tokens with all their heads: each key
+// tile serves all of them, a causal tile wastes at most 128 / G tokens of
+// diagonal, and a few tokens still fill the rows.
+//
+// Work. A unit is one 128-key tile of one row tile. All units of a call, in
+// order, are cut into equal runs, one per CTA (one CTA per SM): a CTA finishes
+// the row tile its predecessor began, does whole ones, and begins another. A row
+// tile that was cut leaves partial sums (accumulator, m, sum) in the scratch,
+// which a second kernel merges in key order (deterministic).
+//
+//   warp 0    tensor copies: the Q tile, then K and V chunks (16 KiB) through a ring
+//   warp 1    issues tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
+//             read from tensor memory
+//   warp 2    repairs V chunks of edge tiles in shared memory: the rows that no
+//             query row keeps become zeros (0 * NaN would poison the product)
+//   warps 4+  softmax: one thread per row, scores from tensor memory, P back
+//             over them; at the end of a row tile the same threads read O
+//
+// Value rows that some rows of a tile keep and others do not (the diagonal, a
+// window's start, siblings in a tree) are searched for NaN and infinities as
+// well: such elements become zero for the product and are added, in the
+// epilogue, to exactly the rows that keep them.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+#include <cuda.h>
+
+namespace w4 {
+namespace attn {
+
+constexpr int kKeys = 128;      // keys per tile
+constexpr int kRowsQ = 128;     // rows of one MMA tile
+constexpr int kChunk = 16384;   // ring slot
+constexpr int kSmemChunks = 14; // Q tiles and ring together
+constexpr int kWaitLimit = 1 << 15;
+constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
+
+template <int D>
+struct Shape {
+    static constexpr int NV = D > 256 ? 2 : 1;       // slices of the value width (tensor memory holds 256 columns of O)
+    static constexpr int DV = D / NV;                // width of a slice
+    static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
+    static constexpr int KC = D / 64;                // key chunks per tile: 128 keys x 64 dims
+    static constexpr int VKEYS = DV == 64 ? 128 : (DV == 128 ? 64 : 32); // keys per value chunk
+    static constexpr int VC = kKeys / VKEYS;
+    static constexpr int VBYTES = VKEYS * DV * 2;
+    static constexpr int QCHUNKS = TQ * KC;
+    static constexpr int NS = kSmemChunks - QCHUNKS; // ring slots
+    static constexpr int ROWS = TQ * kRowsQ;
+    static constexpr int THREADS = 128 + TQ * 128;
+    static constexpr size_t SMEM = (size_t)kSmemChunks * kChunk + 1024;
+    static_assert(VBYTES <= kChunk, "value chunk");
+    static_assert(NS >= 6, "ring");
+};
+
+// Scratch of a call with `grid` CTAs (floats): accumulators, (m, sum) per row,
+// then the integer tables.
+constexpr size_t kSlotFloats = 32768; // ROWS * DV at most
+inline size_t ws_need(int grid)
+{
+    return (size_t)2 * grid * kSlotFloats + (size_t)2 * grid * 256 * 2 + (size_t)8 * grid + 64;
+}
+
+struct Args {
+    uint16_t *out;
+    long long ldo; // elements between tokens
+    const int32_t *cu_q, *cu_k;    // prompt: [B + 1] first query / key row of each sequence
+    const int32_t *parents, *pos;  // tree: [B][N], [B]
+    const int32_t *kpos;           // tree: [B][T] or null
+    const uint16_t *v, *vt;        // value rows (only for the NaN / infinity path)
+    long long ldv;
+    float *ws_o, *ws_ml;
+    int32_t *rec;   // [grid][2]: the continued row tile (0 = none, 1 = goes on, 3 = ends here); 1 = begins one
+    int32_t *where; // [grid][4]: token row, tokens, key/value head, slice of the tile whose first partial CTA c holds
+    int *err;
+    int B, N, T; // sequences; tree: nodes, slots
+    int total_q, total_k;
+    int Hq, Hkv, G, D;
+    int tpt; // tokens per MMA row tile: 128 / G
+    int window;
+    float c; // scale * log2(e)
+    int gmin; // units a CTA gets at least
+};
+
+struct Maps {
+    CUtensorMap q, k, v, kt, vt;
+};
+
+// ------------------------------------------------------------------ PTX ----
+
+__device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr)
+{
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(1024 >> 4) << 32; // 8 rows x 128 B
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61; // 128-byte swizzle
+    return d;
+}
+
+// The same swizzle with the other dimension contiguous: 64 dims per 128-byte
+// row, `group` bytes between blocks of 64 dims, 1024 between blocks of 8 keys.
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t group)
+{
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(group >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+constexpr uint32_t idesc_bf16(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kRowsQ >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define W4_R32(v, o)                                                                                             \
+    "=r"(v[o + 0]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]),              \
+        "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]),        \
+        "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15]), "=r"(v[o + 16]), "=r"(v[o + 17]),    \
+        "=r"(v[o + 18]), "=r"(v[o + 19]), "=r"(v[o + 20]), "=r"(v[o + 21]), "=r"(v[o + 22]), "=r"(v[o + 23]),    \
+        "=r"(v[o + 24]), "=r"(v[o + 25]), "=r"(v[o + 26]), "=r"(v[o + 27]), "=r"(v[o + 28]), "=r"(v[o + 29]),    \
+        "=r"(v[o + 30]), "=r"(v[o + 31])
+#define W4_I32(v, o)                                                                                             \
+    "r"(v[o + 0]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]),     \
+        "r"(v[o + 7]), "r"(v[o + 8]), "r"(v[o + 9]), "r"(v[o + 10]), "r"(v[o + 11]), "r"(v[o + 12]),             \
+        "r"(v[o + 13]), "r"(v[o + 14]), "r"(v[o + 15]), "r"(v[o + 16]), "r"(v[o + 17]), "r"(v[o + 18]),          \
+        "r"(v[o + 19]), "r"(v[o + 20]), "r"(v[o + 21]), "r"(v[o + 22]), "r"(v[o + 23]), "r"(v[o + 24]),          \
+        "r"(v[o + 25]), "r"(v[o + 26]), "r"(v[o + 27]), "r"(v[o + 28]), "r"(v[o + 29]), "r"(v[o + 30]),          \
+        "r"(v[o + 31])
+
+// 32 consecutive columns of this thread's tensor-memory lane; the wait belongs to
+// the same statement, so that no use of the registers can move before it.
+#define W4_TLD32(v, addr)                                                                                        \
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "                                                       \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"                                       \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"                  \
+                 "tcgen05.wait::ld.sync.aligned;"                                                                \
+                 : W4_R32(v, 0)                                                                                  \
+                 : "r"(addr)                                                                                     \
+                 : "memory")
+// 128 columns, as four loads and one wait.
+#define W4_TLD128(v, addr) \
+    asm volatile(\
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15," \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t" \
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47," \
+                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t" \
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79," \
+                 "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t" \
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111," \
+                 "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t" \
+                 "tcgen05.wait::ld.sync.aligned;" \
+                 : W4_R32(v, 0), W4_R32(v, 32), W4_R32(v, 64), W4_R32(v, 96) \
+                 : "r"(addr), "r"((addr) + 32u), "r"((addr) + 64u), "r"((addr) + 96u) \
+                 : "memory")
+// 16 columns.
+#define W4_TST16(v, o, addr) \
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], " \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[o + 0]), "r"(v[o + 1]), \
+                 "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7]), \
+                 "r"(v[o + 8]), "r"(v[o + 9]), "r"(v[o + 10]), "r"(v[o + 11]), "r"(v[o + 12]), "r"(v[o + 13]), \
+                 "r"(v[o + 14]), "r"(v[o + 15]), "r"(addr) \
+                 : "memory")
+#define W4_TST32(v, o, addr)                                                                                     \
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "                                                \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"                                       \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::W4_I32(v, o),             \
+                 "r"(addr)                                                                                       \
+                 : "memory")
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// Two fp32 rounded to bf16 (nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ------------------------------------------------------------ the work ----
+
+// A sequence as the kernel sees it: its query rows, its key rows, and for a row
+// tile the range of keys that any of its rows keeps.
+struct Seq {
+    int q0, lq; // first query row, query rows
+    int k0, lk; // first key row (cache row), keys (prompt: the sequence's; tree: min(pos, T))
+    int off;    // prompt: position of query row 0; tree: position of depth 0
+};
+
+template <bool TREE>
+__device__ __forceinline__ Seq load_seq(const Args &a, int s)
+{
+    Seq q;
+    if (TREE) {
+        q.q0 = s * a.N;
+        q.lq = a.N;
+        q.k0 = s * a.T;
+        q.off = max(__ldg(a.pos + s), 0);
+        q.lk = min(q.off, a.T);
+    } else {
+        q.q0 = __ldg(a.cu_q + s);
+        q.lq = q.q0 < 0 ? 0 : max(0, min(__ldg(a.cu_q + s + 1), a.total_q) - q.q0);
+        q.k0 = max(0, __ldg(a.cu_k + s));
+        q.lk = max(0, min(__ldg(a.cu_k + s + 1), a.total_k) - q.k0);
+        q.off = q.lk - q.lq;
+    }
+    return q;
+}
+
+// First key and one past the last that any of the tokens [t0, t0 + nt) keeps.
+template <bool TREE>
+__device__ __forceinline__ void key_range(const Args &a, const Seq &q, int t0, int nt, int &lo, int &hi)
+{
+    if (TREE) {
+        lo = a.window > 0 ? max(0, q.off - a.window + 1) : 0; // depth 0 sees furthest back
+        hi = q.lk;
+        if (a.kpos) { // any slot may hold any position
+            lo = 0;
+            hi = a.T;
+        }
+    } else {
+        lo = a.window > 0 ? max(0, q.off + t0 - a.window + 1) : 0;
+        hi = min(q.lk, q.off + t0 + nt);
+    }
+    if (hi <= lo) {
+        lo = 0;
+        hi = 0;
+    }
+}
+
+// Units of a row tile: its key tiles, and in a tree call one more for the tree's
+// own keys; at least one, so that rows without keys are written.
+template <bool TREE>
+__device__ __forceinline__ int tile_units(int lo, int hi)
+{
+    const int n = hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
+    return TREE ? n + 1 : max(n, 1);
+}
+
+// One CTA's run of units, as pieces of row tiles.
+template <int D, bool TREE>
+struct Walk {
+    using S = Shape<D>;
+    int hs;        // key/value head * NV + slice
+    int s, i;      // sequence, row tile within it
+    int u;         // first unit of the piece within the row tile
+    long long left; // units of the run from here
+    Seq q;
+    // the piece
+    int t0, nt, lo, hi, n; // first token, tokens, keys, units of the row tile
+    int u1;                // one past the piece's last unit
+
+    __device__ __forceinline__ void describe(const Args &a)
+    {
+        const int tt = a.tpt * S::TQ;
+        t0 = i * tt;
+        nt = min(tt, q.lq - t0);
+        key_range<TREE>(a, q, t0, nt, lo, hi);
+        n = tile_units<TREE>(lo, hi);
+        u1 = (int)min((long long)n, u + left);
+    }
+    __device__ __forceinline__ void begin(const Args &a, int hs_, int s_, int i_, int u_, long long left_)
+    {
+        hs = hs_;
+        s = s_;
+        i = i_;
+        u = u_;
+        left = left_;
+        if (left > 0) {
+            q = load_seq<TREE>(a, s);
+            describe(a);
+        }
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const Args &a)
+    {
+        left -= u1 - u;
+        if (left <= 0)
+            return;
+        u = 0;
+        ++i;
+        const int tt = a.tpt * S::TQ;
+        while (i * tt >= q.lq) { // ends: units are left, so a later sequence (or head) has row tiles
+            i = 0;
+            if (++s == a.B) {
+                s = 0;
+                if (++hs == a.Hkv * S::NV) {
+                    left = 0;
+                    return;
+                }
+            }
+            q = load_seq<TREE>(a, s);
+        }
+        describe(a);
+    }
+    __device__ __forceinline__ int units() const { return u1 - u; }
+    __device__ __forceinline__ bool whole() const { return u == 0 && u1 == n; }
+    // Key tile of unit x of the row tile; the tree's own keys follow the cache's.
+    __device__ __forceinline__ bool tree_unit(int x) const { return TREE && x == n - 1; }
+    __device__ __forceinline__ int key0(int x) const { return (lo / kKeys + x) * kKeys; }
+    // MMA row tiles of the piece that hold any token.
+    __device__ __forceinline__ int nq(const Args &a) const { return S::TQ == 1 ? 1 : (nt > a.tpt ? 2 : 1); }
+    // A unit whose value rows need repair: keys outside [lo, hi), keys that only
+    // some rows keep, recorded positions, the tree's own keys.
+    __device__ __forceinline__ bool edge(const Args &a, int x) const
+    {
+        if (TREE) {
+            if (tree_unit(x) || a.kpos)
+                return true;
+            const int k = key0(x);
+            return k + kKeys > hi || k < lo || (a.window > 0 && k < lo + 64);
+        }
+        const int k = key0(x);
+        if (k + kKeys > q.off + t0 + 1 || k + kKeys > hi || k < lo) // past the first row's last key
+            return true;
+        return a.window > 0 && k < q.off + t0 + nt - a.window; // before the last row's first key
+    }
+};
+
+// A value row's part in the product: 0 = kept by every row, 1 = by some, 2 = by none.
+template <int D, bool TREE>
+__device__ __forceinline__ int key_class(const Args &a, const Walk<D, TREE> &w, int x, int j)
+{
+    if (TREE) {
+        if (w.tree_unit(x))
+            return j < a.N ? 1 : 2;
+        const int k = w.key0(x) + j;
+        if (k >= a.T)
+            return 2;
+        const int p = a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
+        if (p < 0 || p >= w.q.off)
+            return 2;
+        if (a.window > 0) {
+            if ((long long)p <= (long long)w.q.off - a.window)
+                return 2;
+            if ((long long)p <= (long long)w.q.off + (a.N - 1) - a.window)
+                return 1;
+        }
+        return 0;
+    }
+    const int k = w.key0(x) + j;
+    if (k >= w.hi || k < w.lo)
+        return 2;
+    if (k > w.q.off + w.t0)
+        return 1;
+    if (a.window > 0 && k <= w.q.off + w.t0 + w.nt - 1 - a.window)
+        return 1;
+    return 0;
+}
+
+// What one row keeps.
+struct RowMask {
+    bool live;                // a row of the output
+    int lo, hi;               // kept keys (positions) [lo, hi)
+    unsigned long long nodes; // tree: ancestors or self within the window
+};
+
+template <int D, bool TREE>
+__device__ __forceinline__ RowMask row_mask(const Args &a, const Walk<D, TREE> &w, int tok, bool live)
+{
+    RowMask m;
+    m.live = live;
+    m.lo = m.hi = 0;
+    m.nodes = 0;
+    if (!live)
+        return m;
+    if (TREE) {
+        const int32_t *par = a.parents + (size_t)w.s * a.N;
+        int j = w.t0 + tok, d = 0, p = __ldg(par + j);
+        if (p == -2) // an absent node
+            return m;
+        for (;; ++d) {
+            if (a.window <= 0 || d < a.window)
+                m.nodes |= 1ull << j;
+            if (p < 0 || p >= j)
+                break;
+            j = p;
+            p = __ldg(par + j);
+        }
+        m.hi = a.kpos ? w.q.off : w.q.lk;
+        m.lo = a.window > 0 ? (int)max(0ll, (long long)w.q.off + d - a.window + 1) : 0;
+    } else {
+        const int at = w.q.off + w.t0 + tok;
+        m.hi = min(at + 1, w.q.lk);
+        m.lo = a.window > 0 ? max(0, at - a.window + 1) : 0;
+    }
+    return m;
+}
+
+// Adds to a stored output row (or partial) the NaN and infinite values of the
+// keys that warp 2 took out of the product and that this row keeps.
+template <int D, bool TREE, typename Add>
+__device__ __forceinline__ void add_specials(const Args &a, const Walk<D, TREE> &w, const RowMask &m, int kvh,
+                                             int dv0, Add add)
+{
+#pragma unroll 1
+    for (int x = w.u; x < w.u1; ++x) {
+        if (!w.edge(a, x))
+            continue;
+        const bool tree = w.tree_unit(x);
+#pragma unroll 1
+        for (int j = 0; j < kKeys; ++j) {
+            if (key_class(a, w, x, j) != 1)
+                continue;
+            const int k = w.key0(x) + j;
+            bool kept;
+            const uint16_t *row;
+            if (tree) {
+                kept = (m.nodes >> j) & 1;
+                row = a.vt + ((size_t)(w.s * (long long)a.N + j) * a.Hkv + kvh) * D;
+            } else {
+                const int p = TREE && a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
+                kept = p >= m.lo && p < m.hi;
+                row = a.v + (size_t)((long long)w.q.k0 + k) * a.ldv + (size_t)kvh * D;
+            }
+            if (!kept)
+                continue;
+#pragma unroll 1
+            for (int d = 0; d < Shape<D>::DV; ++d) {
+                const uint32_t b = row[dv0 + d];
+                if ((b & 0x7F80u) == 0x7F80u)
+                    add(d, __uint_as_float(b << 16));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- kernel ----
+
+struct Bars {
+    unsigned long long full[12], efull[12], empty[12];
+    unsigned long long q_full, q_empty;
+    unsigned long long s_full[2], p_full[2], o_done[2], o_free[2], drain;
+};
+
+template <int THREADS>
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
+{
+    // Inclusive sum over the block; `total` is the sum of all.
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d)
+            x += y;
+    }
+    __syncthreads();
+    if (lane == 31)
+        warp_sums[w] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        const int t = warp_sums[i];
+        before += i < w ? t : 0;
+        all += t;
+    }
+    total = all;
+    return x + before;
+}
+
+template <int D, bool TREE>
+__global__ void __launch_bounds__(Shape<D>::THREADS, 1)
+attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
+{
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ __align__(8) Bars bars;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int s_abort;
+    __shared__ int s_special[4];
+    __shared__ int s_start[4];
+    __shared__ int warp_sums[12];
+
+    unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t q_base = smem_addr(smem);
+    const uint32_t ring = q_base + S::QCHUNKS * kChunk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::NS; ++i) {
+            mbar_init(smem_addr(&bars.full[i]), 1);
+            mbar_init(smem_addr(&bars.efull[i]), 1);
+            mbar_init(smem_addr(&bars.empty[i]), 1);
+        }
+        mbar_init(smem_addr(&bars.q_full), 1);
+        mbar_init(smem_addr(&bars.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&bars.s_full[i]), 1);
+            mbar_init(smem_addr(&bars.p_full[i]), 4);
+            mbar_init(smem_addr(&bars.o_done[i]), 1);
+            mbar_init(smem_addr(&bars.o_free[i]), 4);
+        }
+        mbar_init(smem_addr(&bars.drain), 1);
+        s_abort = 0;
+        for (int i = 0; i < 4; ++i)
+            s_special[i] = -1;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&tmem_base)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // -------------------------------------------------- this CTA's run
+    Walk<D, TREE> w0;
+    {
+        const int tt = a.tpt * S::TQ;
+        int *sbase = reinterpret_cast<int *>(smem); // first row tile of each sequence
+        int R = 0;
+        for (int s0 = 0; s0 < a.B; s0 += S::THREADS) {
+            const int s = s0 + (int)threadIdx.x;
+            const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
+            int total;
+            const int incl = block_scan<S::THREADS>(nt, warp_sums, total);
+            if (s < a.B)
+                sbase[s] = R + incl - nt;
+            R += total;
+        }
+        __syncthreads();
+        auto seq_of = [&](int r) { // the last sequence that begins at or before r and is not empty there
+            int x = 0, y = a.B - 1;
+            while (x < y) {
+                const int m = (x + y + 1) >> 1;
+                if (sbase[m] <= r)
+                    x = m;
+                else
+                    y = m - 1;
+            }
+            return x;
+        };
+        auto units_of = [&](int r, int &s) {
+            s = seq_of(r);
+            const Seq q = load_seq<TREE>(a, s);
+            const int t0 = (r - sbase[s]) * tt;
+            int lo, hi;
+            key_range<TREE>(a, q, t0, min(tt, q.lq - t0), lo, hi);
+            return tile_units<TREE>(lo, hi);
+        };
+        long long W = 0;
+        for (int r0 = 0; r0 < R; r0 += S::THREADS) {
+            const int r = r0 + (int)threadIdx.x;
+            int total, s;
+            block_scan<S::THREADS>(r < R ? units_of(r, s) : 0, warp_sums, total);
+            W += total;
+        }
+        const long long all = W * a.Hkv * S::NV;
+        const long long ctas = max(1ll, min((long long)gridDim.x, all / a.gmin));
+        const long long c = blockIdx.x;
+        const long long u0 = c < ctas ? all * c / ctas : all, u1 = c < ctas ? all * (c + 1) / ctas : all;
+        const int hs = W > 0 ? (int)(u0 / W) : 0;
+        const long long at = u0 - hs * W;
+        long long before = 0;
+        for (int r0 = 0; r0 < R && u1 > u0; r0 += S::THREADS) {
+            const int r = r0 + (int)threadIdx.x;
+            int total, s = 0;
+            const int n = r < R ? units_of(r, s) : 0;
+            const int incl = block_scan<S::THREADS>(n, warp_sums, total);
+            const long long p = before + incl - n;
+            if (n > 0 && at >= p && at < p + n) {
+                s_start[0] = s;
+                s_start[1] = r - sbase[s];
+                s_start[2] = (int)(at - p);
+            }
+            before += total;
+            if (at < before)
+                break;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // sbase reads before the ring's copies
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        w0.begin(a, hs, s_start[0], s_start[1], s_start[2], u1 - u0);
+    }
+    const uint32_t tmem = tmem_base;
+    // S (and P over it) in columns [128 b, 128 b + 128), O_t from 256 + t * DV.
+    auto s_col = [&](int b) { return tmem + 128u * (uint32_t)b; };
+    auto o_col = [&](int t) { return tmem + 256u + (uint32_t)(t * S::DV); };
+
+    auto wait = [&](unsigned long long &bar, uint32_t parity) -> bool {
+        const uint32_t b = smem_addr(&bar);
+        for (int i = 0; i < kWaitLimit; ++i) {
+            if (mbar_try_wait(b, parity, 20000u))
+                return true;
+            if (s_abort)
+                return false;
+        }
+        s_abort = 1;
+        atomicOr(a.err, 8);
+        return false;
+    };
+
+    // 384 threads: 168 registers each at launch (64512 in all). The softmax threads
+    // hold a row of 128 scores: 208, and 80 for the first four warps (63488 in all).
+    if (S::TQ == 2) {
+        if (warp < 4)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    }
+
+    if (warp == 0) {
+        // ---------------------------------------------------- copies
+        if (lane == 0) {
+            uint32_t g = 0, piece = 0;
+            uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
+            bool ok = true;
+            Walk<D, TREE> w = w0;
+            for (; ok && w.more(); w.next(a), ++piece) {
+                const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
+                if (piece > 0 && !wait(bars.q_empty, (piece - 1) & 1)) {
+                    ok = false;
+                    break; // the Q copies waited for below are the previous piece's
+                }
+                const int nq = w.nq(a), units = w.units();
+                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(nq * S::KC * a.tpt * a.G * 128));
+                for (int t = 0; t < nq; ++t)
+                    for (int c = 0; c < S::KC; ++c)
+                        tma_3d(q_base + (t * S::KC + c) * kChunk, &maps.q, 64 * c, kvh * a.G,
+                               w.q.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
+                auto slot_wait = [&]() {
+                    const uint32_t u = g / S::NS;
+                    return u == 0 || wait(bars.empty[g % S::NS], (u - 1) & 1);
+                };
+                auto keys = [&](int j) {
+                    const int x = w.u + j;
+                    const bool tr = w.tree_unit(x);
+                    const CUtensorMap *m = tr ? &maps.kt : &maps.k;
+                    const int row = tr ? w.s * a.N : w.q.k0 + w.key0(x);
+                    for (int c = 0; c < S::KC; ++c, ++g) {
+                        if (!slot_wait())
+                            return false;
+                        const uint32_t slot = g % S::NS, bar = smem_addr(&bars.full[slot]);
+                        onedge &= ~(1u << slot);
+                        mbar_arrive_expect_tx(bar, kChunk);
+                        tma_3d(ring + slot * kChunk, m, 64 * c, kvh, row, bar);
+                    }
+                    return true;
+                };
+                auto values = [&](int j) {
+                    const int x = w.u + j;
+                    const bool tr = w.tree_unit(x), edge = w.edge(a, x);
+                    const CUtensorMap *m = tr ? &maps.vt : &maps.v;
+                    const int row = tr ? w.s * a.N : w.q.k0 + w.key0(x);
+                    for (int c = 0; c < S::VC; ++c, ++g) {
+                        if (!slot_wait())
+                            return false;
+                        const uint32_t slot = g % S::NS;
+                        const uint32_t bar = smem_addr(edge ? &bars.efull[slot] : &bars.full[slot]);
+                        onedge = edge ? onedge | (1u << slot) : onedge & ~(1u << slot);
+                        par ^= edge ? 1u << slot : 0u;
+                        mbar_arrive_expect_tx(bar, S::VBYTES);
+#pragma unroll
+                        for (int b = 0; b < S::DV / 64; ++b)
+                            tma_3d(ring + slot * kChunk + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
+                                   row + c * S::VKEYS, bar);
+                    }
+                    return true;
+                };
+                ok = keys(0);
+                for (int j = 0; ok && j < units; ++j) {
+                    if (S::TQ == 1) {
+                        ok = (j + 1 >= units || keys(j + 1)) && values(j);
+                    } else {
+                        ok = values(j) && (j + 1 >= units || keys(j + 1));
+                    }
+                }
+            }
+            if (!ok) {
+                // Copies in flight write this CTA's shared memory: let them land.
+                for (int i = 0; i < S::NS; ++i) {
+                    const uint32_t uses = (g + S::NS - 1 - i) / S::NS;
+                    if ((onedge >> i) & 1)
+                        mbar_wait_bounded(smem_addr(&bars.efull[i]), ((par >> i) & 1) ^ 1, 64);
+                    else if (uses > 0)
+                        mbar_wait_bounded(smem_addr(&bars.full[i]), (uses - 1) & 1, 64);
+                }
+                if (piece > 0)
+                    mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
+            uint32_t g = 0, piece = 0, it = 0; // chunks, pieces, units so far
+            bool ok = true;
+            Walk<D, TREE> w = w0;
+            // S_b = Q_t K^T from chunks gk ..; `last` frees them.
+            auto scores = [&](int t, int b, uint32_t gk, bool first, bool last) {
+                for (int c = 0; c < S::KC; ++c) {
+                    const uint32_t gg = gk + c, slot = gg % S::NS;
+                    if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::KC + c) * kChunk);
+                    const uint64_t bd = sdesc_kmajor(ring + slot * kChunk);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(s_col(b), ad + 2u * k, bd + 2u * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                    if (last)
+                        mma_commit(smem_addr(&bars.empty[slot]));
+                }
+                mma_commit(smem_addr(&bars.s_full[b]));
+                return true;
+            };
+            auto product = [&](int t, int b, uint32_t gv, bool acc, bool first, bool last) {
+                for (int c = 0; c < S::VC; ++c) {
+                    const uint32_t gg = gv + c, slot = gg % S::NS;
+                    if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t bd = sdesc_mnmajor(ring + slot * kChunk, S::VKEYS * 128);
+#pragma unroll
+                    for (int k = 0; k < S::VKEYS / 16; ++k)
+                        mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
+                               (acc || c > 0 || k > 0) ? 1u : 0u);
+                    if (last)
+                        mma_commit(smem_addr(&bars.empty[slot]));
+                }
+                mma_commit(smem_addr(&bars.o_done[t]));
+                return true;
+            };
+            uint32_t itq[2] = {0, 0}, pcq[2] = {0, 0}; // units and pieces of each row tile (TQ == 2)
+            for (; ok && w.more(); w.next(a), ++piece) {
+                const int units = w.units(), nq = w.nq(a);
+                ok = wait(bars.q_full, piece & 1);
+                if (!ok)
+                    break;
+                if (S::TQ == 1) {
+                    ok = scores(0, it & 1, g, true, true);
+                    g += S::KC;
+                    for (int j = 0; ok && j < units; ++j, ++it) {
+                        if (j + 1 < units) {
+                            ok = scores(0, (it + 1) & 1, g, true, true);
+                            g += S::KC;
+                        }
+                        if (ok && (j + 2 == units || units == 1))
+                            mma_commit(smem_addr(&bars.q_empty));
+                        ok = ok && wait(bars.p_full[it & 1], (it >> 1) & 1) &&
+                             (j > 0 || piece == 0 || wait(bars.o_free[0], (piece - 1) & 1));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        ok = product(0, it & 1, g, j > 0, true, true);
+                        g += S::VC;
+                    }
+                } else {
+                    for (int t = 0; ok && t < nq; ++t)
+                        ok = scores(t, t, g, t == 0, t == nq - 1);
+                    g += S::KC;
+                    if (units == 1)
+                        mma_commit(smem_addr(&bars.q_empty));
+                    for (int j = 0; ok && j < units; ++j) {
+                        for (int t = 0; ok && t < nq; ++t) {
+                            ok = wait(bars.p_full[t], itq[t] & 1) &&
+                                 (j > 0 || pcq[t] == 0 || wait(bars.o_free[t], (pcq[t] - 1) & 1));
+                            if (!ok)
+                                break;
+                            ++itq[t];
+                            tc_fence_after();
+                            ok = product(t, t, g, j > 0, t == 0, t == nq - 1);
+                            if (ok && j + 1 < units)
+                                ok = scores(t, t, g + S::VC, t == 0, t == nq - 1);
+                        }
+                        g += S::VC + (j + 1 < units ? S::KC : 0);
+                        if (j + 2 == units)
+                            mma_commit(smem_addr(&bars.q_empty));
+                    }
+                    for (int t = 0; t < nq; ++t)
+                        ++pcq[t];
+                }
+            }
+            // Every MMA has finished before tensor memory is freed.
+            mma_commit(smem_addr(&bars.drain));
+            mbar_wait_bounded(smem_addr(&bars.drain), 0, 1024);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------- value rows of edge tiles
+        uint32_t base = 0, par = 0; // chunks before the piece; phase of each slot's edge barrier
+        int piece = 0;
+        bool ok = true;
+        Walk<D, TREE> w = w0;
+        for (; ok && w.more(); w.next(a), ++piece) {
+            const int units = w.units();
+            for (int j = 0; ok && j < units; ++j) {
+                const int x = w.u + j;
+                if (!w.edge(a, x))
+                    continue;
+                const uint32_t gv = base + (uint32_t)(j * (S::KC + S::VC) + S::KC) +
+                                    (S::TQ == 1 && j + 1 < units ? S::KC : 0);
+                for (int c = 0; ok && c < S::VC; ++c) {
+                    const uint32_t slot = (gv + c) % S::NS;
+                    // Classes of this chunk's keys: key c * VKEYS + 32 h + lane in bits 2h, 2h + 1.
+                    uint32_t cls = 0;
+#pragma unroll
+                    for (int h = 0; h < S::VKEYS / 32; ++h)
+                        cls |= (uint32_t)key_class(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
+                    ok = __all_sync(0xFFFFFFFFu, wait(bars.efull[slot], (par >> slot) & 1));
+                    if (!ok)
+                        break;
+                    par ^= 1u << slot;
+                    const uint32_t vb = ring + slot * kChunk;
+                    bool found = false;
+#pragma unroll
+                    for (int h = 0; h < S::VKEYS / 32; ++h) {
+                        const uint32_t mine = (cls >> (2 * h)) & 3u;
+                        uint32_t todo = __ballot_sync(0xFFFFFFFFu, mine != 0);
+                        const uint32_t none = __ballot_sync(0xFFFFFFFFu, mine == 2);
+                        // Four rows at a time, eight lanes of 16 bytes each per 64 dims.
+                        for (int r4 = 0; r4 < 32; r4 += 4) {
+                            if (!((todo >> r4) & 0xFu))
+                                continue;
+                            const int rr = r4 + (lane >> 3);
+                            if ((todo >> rr) & 1u) {
+                                for (int b = 0; b < S::DV / 64; ++b) {
+                                    const uint32_t p = vb + b * (S::VKEYS * 128) + (32 * h + rr) * 128 + (lane & 7) * 16;
+                                    uint4 v = make_uint4(0, 0, 0, 0);
+                                    if (!((none >> rr) & 1u)) {
+                                        v = lds128(p);
+                                        uint32_t *e = reinterpret_cast<uint32_t *>(&v);
+                                        bool bad = false;
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            if ((e[i] & 0x7F80u) == 0x7F80u) {
+                                                e[i] &= 0xFFFF0000u;
+                                                bad = true;
+                                            }
+                                            if ((e[i] & 0x7F800000u) == 0x7F800000u) {
+                                                e[i] &= 0x0000FFFFu;
+                                                bad = true;
+                                            }
+                                        }
+                                        if (!bad)
+                                            continue;
+                                        found = true;
+                                    }
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x),
+                                                 "r"(v.y), "r"(v.z), "r"(v.w)
+                                                 : "memory");
+                                }
+                            }
+                        }
+                    }
+                    if (found)
+                        s_special[piece & 3] = piece;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&bars.full[slot]));
+                }
+            }
+            base += (uint32_t)(units * (S::KC + S::VC));
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------ softmax
+        const int t = (warp - 4) >> 2;  // MMA row tile
+        const int wq = warp & 3;        // tensor-memory lanes 32 wq ..
+        const int row = 32 * wq + lane; // row of the MMA tile
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const int tok_in = row / a.G, head = row - tok_in * a.G;
+        uint32_t it = 0, piece = 0; // units of this row tile; pieces of the run
+        bool ok = true;
+        Walk<D, TREE> w = w0;
+        for (; ok && w.more(); w.next(a), ++piece) {
+            const int units = w.units(), kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
+            if (t >= w.nq(a))
+                continue;
+            const int tok = t * a.tpt + tok_in;
+            const RowMask rm = row_mask(a, w, tok, tok_in < a.tpt && tok < w.nt);
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; ok && j < units; ++j, ++it) {
+                const int x = w.u + j, key0 = w.key0(x);
+                const bool tr = w.tree_unit(x);
+                const uint32_t b = S::TQ == 1 ? (it & 1) : (uint32_t)t;
+                const uint32_t ph = S::TQ == 1 ? (it >> 1) & 1 : it & 1;
+                // Kept keys of this row, one bit each; `all`: the warp keeps every key.
+                uint32_t km[4];
+                bool all = false;
+                if (TREE && tr) {
+                    km[0] = (uint32_t)rm.nodes;
+                    km[1] = (uint32_t)(rm.nodes >> 32);
+                    km[2] = km[3] = 0;
+                } else if (TREE && a.kpos) {
+                    // Recorded positions: lane i holds keys i, 32 + i, ... A key is kept by
+                    // all rows, by none, or by those whose window reaches back to it.
+                    const int lo = rm.hi > 0 ? rm.lo : 0x7FFFFFFF; // rm.hi = 0: an absent node
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int k = key0 + 32 * h + lane;
+                        const int p = k < a.T ? __ldg(a.kpos + (size_t)w.s * a.T + k) : -1;
+                        const bool in = p >= 0 && p < w.q.off;
+                        const bool every = in && (a.window <= 0 || (long long)p + a.window > (long long)w.q.off + a.N);
+                        uint32_t some = __ballot_sync(0xFFFFFFFFu, in && !every);
+                        km[h] = __ballot_sync(0xFFFFFFFFu, every);
+                        if (lo == 0x7FFFFFFF)
+                            km[h] = 0;
+                        while (some) {
+                            const int i = __ffs(some) - 1;
+                            some &= some - 1;
+                            if (__shfl_sync(0xFFFFFFFFu, p, i) >= lo)
+                                km[h] |= 1u << i;
+                        }
+                    }
+                } else {
+                    const int lo = rm.lo - key0, hi = rm.hi - key0;
+                    all = __all_sync(0xFFFFFFFFu, !rm.live || (lo <= 0 && hi >= kKeys));
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        km[h] = below(hi - 32 * h) & ~below(lo - 32 * h);
+                }
+                ok = __all_sync(0xFFFFFFFFu, wait(bars.s_full[b], ph));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                uint32_t v[128];
+                const uint32_t sa = s_col(b) + lanes;
+                W4_TLD128(v, sa);
+                constexpr uint32_t kNegInf = 0xFF800000u;
+                if (!all) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (!((km[i >> 5] >> (i & 31)) & 1u))
+                            v[i] = kNegInf;
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mx[q] = __uint_as_float(v[q]);
+#pragma unroll
+                for (int i = 4; i < 128; ++i)
+                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                float alpha = 1.f;
+                if (rm.live && mt > m + 8.f) { // also the first kept key (m = -inf)
+                    alpha = ex2(m - mt);
+                    l *= alpha;
+                    m = mt;
+                }
+                if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+                    // O holds the units before this one: wait for their product.
+                    ok = __all_sync(0xFFFFFFFFu, wait(bars.o_done[t], (it - 1) & 1));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                        uint32_t o[32];
+                        W4_TLD32(o, o_col(t) + lanes + c0);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        W4_TST32(o, 0, o_col(t) + lanes + c0);
+                    }
+                }
+                const float mm = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i]), a.c, -mm));
+                        const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i + 1]), a.c, -mm));
+                        sum[i & 3] += p0 + p1;
+                        pk[i] = pack2(p0, p1);
+                    }
+                    W4_TST16(pk, 0, sa + 16u * c);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bars.p_full[b]));
+            }
+            if (!ok)
+                break;
+            // ------------------------------------------------- epilogue
+            // With two score buffers the last scores say nothing of the product before
+            // last, and a parity wait tells only neighbouring phases apart.
+            ok = __all_sync(0xFFFFFFFFu, (S::TQ == 2 || units < 2 || wait(bars.o_done[t], it & 1)) &&
+                                             wait(bars.o_done[t], (it - 1) & 1));
+            if (!ok)
+                break;
+            tc_fence_after();
+            const bool whole = w.whole(), special = s_special[piece & 3] == (int)piece;
+            uint16_t *orow = a.out + (size_t)((long long)w.q.q0 + w.t0 + tok) * a.ldo +
+                             (size_t)(kvh * a.G + head) * D + dv0;
+            const int slot = 2 * (int)blockIdx.x + (w.u == 0 ? 1 : 0);
+            // Partial accumulators: [slot][DV / 4][ROWS] float4.
+            float4 *prow = reinterpret_cast<float4 *>(a.ws_o + (size_t)slot * kSlotFloats) + t * kRowsQ + row;
+            const float f = l == 0.f ? 0.f : 1.f / l; // nothing kept: zeros
+#pragma unroll 1
+            for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                uint32_t o[32];
+                W4_TLD32(o, o_col(t) + lanes + c0);
+                if (rm.live && whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 y;
+                        y.x = pack2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f);
+                        y.y = pack2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
+                        y.z = pack2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f);
+                        y.w = pack2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f);
+                        *reinterpret_cast<uint4 *>(orow + c0 + i) = y;
+                    }
+                } else if (rm.live) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        prow[(size_t)((c0 + i) / 4) * S::ROWS] =
+                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                        __uint_as_float(o[i + 3]));
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&bars.o_free[t]));
+            if (!whole && rm.live) {
+                float *ml = a.ws_ml + ((size_t)slot * 256 + t * kRowsQ + row) * 2;
+                ml[0] = m;
+                ml[1] = l;
+            }
+            if (special && rm.live)
+                add_specials(a, w, rm, kvh, dv0, [&](int d, float f) {
+                    if (whole) {
+                        const float o = __uint_as_float((uint32_t)orow[d] << 16) + f;
+                        orow[d] = (uint16_t)(pack2(o, 0.f) & 0xFFFFu);
+                    } else {
+                        reinterpret_cast<float *>(prow + (size_t)(d / 4) * S::ROWS)[d & 3] += f;
+                    }
+                });
+        }
+    } else if (lane == 0) {
+        // warp 3: what the merge needs to know about this CTA's partials.
+        int cont = 0, begins = 0;
+        Walk<D, TREE> w = w0;
+        for (; w.more(); w.next(a)) {
+            if (w.u > 0)
+                cont = 1 | (w.u1 == w.n ? 2 : 0);
+            else if (!w.whole()) {
+                begins = 1;
+                int32_t *p = a.where + 4 * blockIdx.x;
+                p[0] = w.q.q0 + w.t0;
+                p[1] = w.nt;
+                p[2] = w.hs / S::NV;
+                p[3] = w.hs % S::NV;
+            }
+        }
+        a.rec[2 * blockIdx.x] = cont;
+        a.rec[2 * blockIdx.x + 1] = begins;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+} // namespace attn
+} // namespace w4

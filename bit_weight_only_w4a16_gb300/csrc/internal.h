@@ -161,4 +161,60 @@ cudaError_t run_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos,
                                 const uint32_t *qt, const uint16_t *sc, int V, int K, int lg, int cap,
                                 int32_t *status, cudaStream_t s);
 
+// Tiled attention (attn_tiles.cuh): scratch floats for a device with num_sms SMs.
+size_t attn_ws_floats(int num_sms);
+
+// Causal attention of B packed sequences: query rows cu_q[b] .. cu_q[b + 1) are
+// the last ones of the positions that key rows cu_k[b] .. cu_k[b + 1) hold.
+// D in {64, 128, 256, 384, 512}. ld*: elements between rows.
+struct AttnPromptArgs {
+    uint16_t *out;
+    const uint16_t *q, *k, *v;
+    const int32_t *cu_q, *cu_k;
+    int B, total_q, total_k, Hq, Hkv, D;
+    long long ldq, ldk, ldv, ldo;
+    int window;
+    float scale;
+};
+cudaError_t run_attn_prompt(const AttnPromptArgs &p, float *ws, int *err, int num_sms, cudaStream_t s);
+
+// Attention of B trees of N <= 64 drafted tokens over caches of T slots and over
+// the tokens' own keys and values.
+struct AttnTreeArgs {
+    uint16_t *out;
+    const uint16_t *q, *k, *v;
+    const int32_t *kpos;
+    const uint16_t *k_tree, *v_tree;
+    const int32_t *parents, *pos;
+    int B, N, T, Hq, Hkv, D, window;
+    float scale;
+};
+cudaError_t run_attn_tree(const AttnTreeArgs &p, float *ws, int *err, int num_sms, cudaStream_t s);
+
+// Log probability of targets[m], entropy and the k <= 32 largest logits of M rows
+// of V fp32 logits, ld elements apart. Any output may be null.
+struct LogprobsArgs {
+    float *logprob, *entropy, *top_logprob;
+    int32_t *top_id;
+    const float *logits;
+    const int32_t *targets;
+    int M, V;
+    long long ld;
+    int k;
+    int32_t *status;
+};
+cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s);
+
+// Rows path[b][0 .. count[b]) of the trees' keys and values [L][B][N][W] into the
+// slots of positions pos[b], pos[b] + 1, ... of caches [L][B][T][W].
+struct KvCommitArgs {
+    uint16_t *k_cache, *v_cache;
+    int32_t *kpos;
+    const uint16_t *k_tree, *v_tree;
+    const int32_t *path, *count, *pos;
+    int L, B, N, T, W;
+    int32_t *status;
+};
+cudaError_t run_kv_commit(const KvCommitArgs &a, cudaStream_t s);
+
 } // namespace w4

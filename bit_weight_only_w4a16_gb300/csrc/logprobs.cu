@@ -1,0 +1,389 @@
+// Log probabilities of given tokens, entropy and the most likely alternatives
+// from rows of fp32 logits (the vocabulary projection's output).
+//
+// Source: "Gemma 4 E2B on a 4 GB GPU with pure PyTorch" - Step 2 (the logits of
+// 262144 tokens come from the 4-bit embedding). The pages pick greedily; judging
+// drafted tokens needs the probabilities themselves.
+//
+// Mathematics, one pass: with m the running maximum of a warp,
+//   s = sum e^(x - m),  u = sum e^(x - m) (x - m)
+// and when m grows to m': s' = f s, u' = f (u + (m - m') s), f = e^(m - m').
+//   log p(t) = (x_t - m) - log s,   entropy = log s - u / s
+// (u in terms of x - m keeps the entropy's two parts small).
+//
+// The k largest logits need no second pass over the row: the streaming kernel
+// keeps the maximum of every 256 logits. In the order (value descending, index
+// ascending) the k largest logits lie in the k chunks whose maxima are first in
+// that order, because an element of any other chunk has k chunk maxima before
+// it. The second kernel picks those chunks and looks at them alone.
+//
+// Bound by the read of the logits: 4 V bytes a row.
+#include "common.cuh"
+#include "internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kChunk = 256; // logits per chunk: two float4 per lane
+constexpr int kWarps = 8;
+constexpr int kBatch = 4; // chunks in flight per warp
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct LogprobArgs {
+    const float *x;
+    long long ld;
+    int V, nc, S; // logits per row, chunks per row, blocks per row
+    float *cmax;  // [rows][nc]
+    float *part;  // [rows][S][4]: m, s, u
+    const int32_t *targets;
+    float *logprob, *entropy, *top_logprob;
+    int32_t *top_id;
+    int k;
+    int32_t *status;
+};
+
+// Chunk c of a row covers logits [256 c - mis, 256 c - mis + 256), where mis is
+// the row's distance (in floats) from a 16-byte boundary: every interior float4
+// is aligned whatever the row stride.
+__device__ __forceinline__ int row_mis(const float *row)
+{
+    return (int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3);
+}
+
+// This lane's eight logits of chunk c: elements e0 .. e0 + 3 and e0 + 128 .. e0 + 131.
+__device__ __forceinline__ void load_chunk(const float *row, int mis, int V, int c, int lane, float v[8])
+{
+    const long long e0 = (long long)c * kChunk - mis + 4 * lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long e = e0 + 128 * h;
+        if (e >= 0 && e + 4 <= V) {
+            const float4 f = __ldcs(reinterpret_cast<const float4 *>(row + e));
+            v[4 * h] = f.x;
+            v[4 * h + 1] = f.y;
+            v[4 * h + 2] = f.z;
+            v[4 * h + 3] = f.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * h + i] = e + i >= 0 && e + i < V ? __ldcs(row + e + i) : -INFINITY;
+        }
+    }
+}
+
+__device__ __forceinline__ float ex2f(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (m, s, u) += (m2, s2, u2).
+__device__ __forceinline__ void merge_stats(float &m, float &s, float &u, float m2, float s2, float u2)
+{
+    const float M = fmaxf(m, m2);
+    if (m == -INFINITY) { // nothing yet (s = u = 0, or NaN)
+        s += s2;
+        u += u2;
+        m = m2;
+        return;
+    }
+    if (m2 == -INFINITY) {
+        s += s2;
+        u += u2;
+        return;
+    }
+    const float d = m - M, d2 = m2 - M;
+    const float f = ex2f(d * kLog2e), f2 = ex2f(d2 * kLog2e);
+    u = f * fmaf(d, s, u) + f2 * fmaf(d2, s2, u2);
+    s = f * s + f2 * s2;
+    m = M;
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+logprob_stream_kernel(const LogprobArgs a)
+{
+    __shared__ float sm[kWarps], ss[kWarps], su[kWarps];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const float *row = a.x + (size_t)blockIdx.y * a.ld;
+    const int mis = row_mis(row);
+    const int c0 = (int)((long long)blockIdx.x * a.nc / a.S), c1 = (int)((long long)(blockIdx.x + 1) * a.nc / a.S);
+    float *cmax = a.cmax + (size_t)blockIdx.y * a.nc;
+
+    float m = -INFINITY, s = 0.f, u = 0.f; // m is the same in all lanes
+    for (int cb = c0 + w; cb < c1; cb += kBatch * kWarps) {
+        float v[kBatch][8];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int c = cb + b * kWarps;
+            if (c < c1) {
+                load_chunk(row, mis, a.V, c, lane, v[b]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[b][i] = -INFINITY;
+            }
+        }
+        float bm = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            float cm = v[b][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                cm = fmaxf(cm, v[b][i]);
+            if (cm != cm)
+                cm = -INFINITY; // eight NaNs: the row's sums are NaN all the same
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, d));
+            if (a.k > 0 && lane == 0 && cb + b * kWarps < c1)
+                cmax[cb + b * kWarps] = cm;
+            bm = fmaxf(bm, cm);
+        }
+        if (bm > m) {
+            if (m != -INFINITY) {
+                const float d = m - bm, f = ex2f(d * kLog2e);
+                u = f * fmaf(d, s, u);
+                s *= f;
+            }
+            m = bm;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = v[b][i] - ref;
+                const float e = ex2f(d * kLog2e);
+                s += e;
+                u = fmaf(e, fmaxf(d, -1e30f), u); // a masked logit (-inf) adds 0
+            }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        u += __shfl_xor_sync(0xFFFFFFFFu, u, d);
+    }
+    if (lane == 0) {
+        sm[w] = m;
+        ss[w] = s;
+        su[w] = u;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kWarps; ++i)
+            merge_stats(m, s, u, sm[i], ss[i], su[i]);
+        *reinterpret_cast<float4 *>(a.part + ((size_t)blockIdx.y * a.S + blockIdx.x) * 4) = make_float4(m, s, u, 0.f);
+    }
+}
+
+// --------------------------------------------------- lists of the largest ----
+
+// A key orders (value descending, index ascending): larger keys come first.
+// Zeros of either sign are equal. 0 is below every key.
+__device__ __forceinline__ unsigned long long make_key(float x, uint32_t index)
+{
+    const uint32_t b = __float_as_uint(x + 0.f);
+    const uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    return ((unsigned long long)o << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(unsigned long long k)
+{
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint32_t key_index(unsigned long long k) { return ~(uint32_t)k; }
+
+__device__ __forceinline__ unsigned long long cmp_xchg(unsigned long long k, int d, bool keep_max)
+{
+    const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, k, d);
+    return keep_max == (k > o) ? k : o;
+}
+
+// 32 keys, one per lane, into descending order by lane.
+__device__ __forceinline__ unsigned long long sort32(unsigned long long k, int lane)
+{
+#pragma unroll
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+        for (int d = n >> 1; d; d >>= 1)
+            k = cmp_xchg(k, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
+    return k;
+}
+
+// The 32 largest of two descending lists, in descending order.
+__device__ __forceinline__ unsigned long long merge32(unsigned long long list, unsigned long long other, int lane)
+{
+    const unsigned long long r = __shfl_sync(0xFFFFFFFFu, other, 31 - lane);
+    unsigned long long k = list > r ? list : r;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        k = cmp_xchg(k, d, (lane & d) == 0);
+    return k;
+}
+
+// Adds 32 keys (one per lane) to a warp's descending list, of which `k` matter.
+__device__ __forceinline__ void push32(unsigned long long &list, unsigned long long key, int k, int lane)
+{
+    const unsigned long long least = __shfl_sync(0xFFFFFFFFu, list, k - 1);
+    if (__any_sync(0xFFFFFFFFu, key > least))
+        list = merge32(list, sort32(key, lane), lane);
+}
+
+// The block's lists into one, held by every warp.
+__device__ __forceinline__ unsigned long long merge_block(unsigned long long list, unsigned long long (*sl)[32],
+                                                          int lane, int w)
+{
+    __syncthreads();
+    sl[w][lane] = list;
+    __syncthreads();
+    unsigned long long r = sl[0][lane];
+    for (int i = 1; i < kWarps; ++i)
+        r = merge32(r, sl[i][lane], lane);
+    return r;
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+logprob_finish_kernel(const LogprobArgs a)
+{
+    __shared__ unsigned long long sl[kWarps][32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const size_t r = blockIdx.x;
+    const float *row = a.x + r * a.ld;
+    const int mis = row_mis(row);
+
+    // Sums: every warp merges all blocks' parts (lane i: parts i, i + 32, ...) in the same order.
+    float m = -INFINITY, s = 0.f, u = 0.f;
+    for (int i = lane; i < a.S; i += 32) {
+        const float4 p = *reinterpret_cast<const float4 *>(a.part + (r * a.S + i) * 4);
+        merge_stats(m, s, u, p.x, p.y, p.z);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d),
+                    u2 = __shfl_xor_sync(0xFFFFFFFFu, u, d);
+        // the lower lane's part first: both lanes form the same sums
+        if (lane & d) {
+            float mm = m2, s1 = s2, u1 = u2;
+            merge_stats(mm, s1, u1, m, s, u);
+            m = mm;
+            s = s1;
+            u = u1;
+        } else {
+            merge_stats(m, s, u, m2, s2, u2);
+        }
+    }
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    const bool bad = s != s;            // a NaN or +inf among the logits
+    const bool none = m == -INFINITY;   // every logit is -inf
+    const float logs = bad ? nan : logf(s);
+    if (threadIdx.x == 0) {
+        if (a.entropy)
+            a.entropy[r] = bad ? nan : (none ? 0.f : logs - u / s);
+        if (a.logprob) {
+            const int t = a.targets[r];
+            float y = 0.f;
+            if (t < 0 || t >= a.V) {
+                if (a.status)
+                    *a.status = 1;
+            } else {
+                const float x = row[t];
+                y = bad ? nan : (x == -INFINITY ? -INFINITY : (x - m) - logs);
+            }
+            a.logprob[r] = y;
+        }
+    }
+    if (a.k == 0)
+        return;
+
+    // The k first chunks by (maximum, index).
+    const float *cmax = a.cmax + r * a.nc;
+    unsigned long long list = 0;
+    for (int c0 = w * 32; c0 < a.nc; c0 += kWarps * 32) {
+        const int c = c0 + lane;
+        push32(list, c < a.nc ? make_key(cmax[c], c) : 0ull, a.k, lane);
+    }
+    const unsigned long long chunks = merge_block(list, sl, lane, w);
+    // Their logits: chunk i goes to warp i % kWarps.
+    list = 0;
+    for (int i = w; i < a.k; i += kWarps) {
+        const unsigned long long ck = __shfl_sync(0xFFFFFFFFu, chunks, i);
+        if (ck == 0)
+            break;
+        const int c = (int)key_index(ck);
+        float v[8];
+        load_chunk(row, mis, a.V, c, lane, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long e = (long long)c * kChunk - mis + 4 * lane + (j >> 2) * 128 + (j & 3);
+            push32(list, e >= 0 && e < a.V ? make_key(v[j], (uint32_t)e) : 0ull, a.k, lane);
+        }
+    }
+    const unsigned long long best = merge_block(list, sl, lane, w);
+    if (w == 0 && lane < a.k) {
+        const float x = key_value(best);
+        const size_t o = r * a.k + lane;
+        if (a.top_id)
+            a.top_id[o] = bad || best == 0 ? -1 : (int32_t)key_index(best);
+        if (a.top_logprob)
+            a.top_logprob[o] = bad ? nan : (best == 0 || x == -INFINITY ? -INFINITY : (x - m) - logs);
+    }
+}
+
+} // namespace
+
+cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s)
+{
+    LogprobArgs a = {};
+    a.ld = p.ld;
+    a.V = p.V;
+    a.nc = (p.V + 3 + kChunk - 1) / kChunk; // a row may begin three floats past a boundary
+    a.k = p.k;
+    a.status = p.status;
+    // Four blocks of eight warps per SM, each warp with at least a batch of chunks.
+    int S = (4 * num_sms + p.M - 1) / p.M;
+    const int most = (a.nc + kWarps - 1) / kWarps;
+    S = S < most ? S : most;
+    S = S < 1 ? 1 : S;
+    a.S = S;
+    const size_t per_row = (size_t)a.nc + (size_t)S * 4;
+    long long rows = (long long)((ws_floats - 4) / per_row); // rows of one pass
+    if (rows < 1)
+        return cudaErrorNotSupported;
+    rows = rows < 65535 ? rows : 65535;
+
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    for (long long r0 = 0; r0 < p.M; r0 += rows) {
+        const int n = (int)(p.M - r0 < rows ? p.M - r0 : rows);
+        a.x = p.logits + (size_t)r0 * p.ld;
+        a.part = ws;
+        a.cmax = ws + (size_t)n * S * 4;
+        a.targets = p.targets ? p.targets + r0 : nullptr;
+        a.logprob = p.logprob ? p.logprob + r0 : nullptr;
+        a.entropy = p.entropy ? p.entropy + r0 : nullptr;
+        a.top_logprob = p.top_logprob ? p.top_logprob + (size_t)r0 * p.k : nullptr;
+        a.top_id = p.top_id ? p.top_id + (size_t)r0 * p.k : nullptr;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(S, n);
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_stream_kernel, a);
+        if (e != cudaSuccess)
+            return e;
+        cfg.gridDim = dim3(n);
+        e = cudaLaunchKernelEx(&cfg, logprob_finish_kernel, a);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+} // namespace w4

@@ -291,6 +291,108 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
                        const uint32_t *qtable, const uint16_t *scales, int V, int K, int group, int cap,
                        int32_t *status, void *stream);
 
+/*
+ * Prompt attention: causal attention of B prompts, or chunks of prompts, packed
+ * one after another (source: "Gemma 4 E2B on a 4 GB GPU with pure PyTorch", the
+ * prompt-read paragraph: a prompt is read in chunks; the cache paragraph: full
+ * and sliding layers, eight query heads on one key/value head).
+ *
+ *   out[i][h] = sum_t w_t v[t][h / G],  w = softmax over the kept keys t of
+ *               scale * sum_d q[i][h][d] * k[t][h / G][d],   G = Hq / Hkv
+ *
+ *   Sequence b has query rows cu_q[b] .. cu_q[b+1] and key rows cu_k[b] ..
+ *   cu_k[b+1], whose positions are 0, 1, ...; its queries are the last of those
+ *   positions (a chunk that follows cached tokens has more keys than queries).
+ *   Query position p keeps key positions t <= p and, when window > 0, t > p - window.
+ *   A row that keeps no key (more queries than keys) gives zeros. A row of out
+ *   that belongs to no sequence is not written.
+ *
+ *   out, q  bf16 [total_q][Hq][D], ldo / ldq elements between rows
+ *   k, v    bf16 [total_k][Hkv][D], ldk / ldv elements between rows
+ *   cu_q    int32 [B + 1] device, ascending; cu_k the same, or NULL: cu_q
+ *   16-byte aligned pointers, cu_* 4-byte; ld* multiples of 8, at least heads * D.
+ *   B in 1..4096, Hq / Hkv a whole number in 1..128, D in {64, 128, 256, 384,
+ *   512}, scale > 0 and finite; rows and ld* below 2^31.
+ * Scores and sums fp32; weights bf16 (relative 2^-9) in the value product, out
+ * rounded once. What a row does not keep never reaches it, NaN and infinities
+ * included. Lengths are read when the kernels run: one captured call serves
+ * every batch with the same total_q and total_k. Uses the library's split
+ * scratch (like w4a16_gemm).
+ */
+int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                   const int32_t *cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int D, long long ldq,
+                   long long ldk, long long ldv, long long ldo, int window, float scale, void *stream);
+
+/*
+ * Attention of a tree of drafted tokens over a cache and the tree itself (the
+ * same article's decode-attention and cache paragraphs, for several tokens per
+ * step). The drafted tokens' keys and values are given beside the cache;
+ * w4_kv_commit stores those that are accepted.
+ *
+ *   Node i of sequence b has parent parents[b][i] in [0, i), or -1 at the tree's
+ *   first level, or -2: absent (its rows of out are zeros). Its position is
+ *   pos[b] + depth (first level: depth 0), its keys are
+ *     cache slots with recorded position p (kpos[b][t], or t when kpos is NULL),
+ *       0 <= p < pos[b], and p > position - window when window > 0;
+ *     itself and its ancestors in the tree, under the same window.
+ *   A parent outside [-2, i) counts as -1. A row that keeps no key gives zeros.
+ *
+ *   out, q          bf16 [B][N][Hq][D]
+ *   k, v            bf16 [B][T][Hkv][D]
+ *   k_tree, v_tree  bf16 [B][N][Hkv][D]
+ *   kpos            int32 [B][T] (-1 = empty slot) or NULL; parents int32 [B][N]; pos int32 [B]
+ *   16-byte aligned pointers, the int32 ones 4-byte. N in 1..64, B in 1..4096,
+ *   B * T and B * N below 2^31; Hq / Hkv, D, scale, precision, masked values and
+ *   scratch as w4_attn_prompt. pos, parents and kpos are read when the kernels
+ *   run. N = 1 is decode attention for any number of key/value heads.
+ */
+int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kpos,
+                 const uint16_t *k_tree, const uint16_t *v_tree, const int32_t *parents, const int32_t *pos, int B,
+                 int N, int T, int Hq, int Hkv, int D, int window, float scale, void *stream);
+
+/*
+ * Log probabilities of given tokens, entropy and the most likely alternatives of
+ * M rows of logits (the output of w4a16_gemv or w4a16_gemm with the vocabulary
+ * projection; source: Step 2, the tied 4-bit embedding as the output layer).
+ *
+ *   lse = log sum_n exp(logits[m][n])
+ *   logprob[m] = logits[m][targets[m]] - lse
+ *   entropy[m] = lse - sum_n p_n logits[m][n],  p_n = exp(logits[m][n] - lse)
+ *   top_id[m][j], top_logprob[m][j]: the j-th largest logit's index (the lowest
+ *     of equal ones; -0 and +0 are equal) and its logit - lse, j < topk
+ *
+ *   logits fp32 [M][V], ld >= V floats between rows, 4-byte aligned (-inf: a
+ *   token that a constrained decoder masks, probability 0); targets int32 [M];
+ *   logprob, entropy fp32 [M]; top_logprob fp32 [M][topk]; top_id int32 [M][topk].
+ *   Any output may be NULL (targets too when logprob is); topk in 0..32.
+ *   A target outside [0, V) gives logprob 0 and, if status is not NULL, stores 1
+ *   to *status. Entries past V are -1 and -inf. A row of -inf alone has entropy 0
+ *   and log probabilities -inf; a row with a NaN or +inf gives NaN and ids -1.
+ * Sums in fp32. Uses the library's split scratch (like w4a16_gemm).
+ */
+int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top_id, const float *logits,
+                const int32_t *targets, int M, int V, long long ld, int topk, int32_t *status, void *stream);
+
+/*
+ * Stores the accepted tokens of a drafted tree: w4_kv_append for a path of
+ * tokens, and for all layers of one kind (the same article's cache paragraph).
+ *
+ *   for j < count[b]: p = pos[b] + j, slot = p mod T (kpos != NULL) or p,
+ *     k_cache[l][b][slot] = k_tree[l][b][path[b][j]] for every layer l, v alike;
+ *     kpos[b][slot] = p (one table for all L layers)
+ *
+ *   k_cache, v_cache  bf16 [L][B][T][W]; k_tree, v_tree bf16 [L][B][N][W] (W =
+ *   key/value heads * head width, a multiple of 8); path int32 [B][N], count and
+ *   pos int32 [B], kpos int32 [B][T] or NULL; 16-byte aligned, int32 4-byte.
+ *   N in 1..64, L * B < 2^31. count is taken into [0, N]. A node outside [0, N),
+ *   a negative position or one outside a full cache is not stored and sets
+ *   *status = 1 (status may be NULL). Of tokens that share a slot of a short ring
+ *   the last is stored. pos is not changed. The caches do not overlap the trees.
+ */
+int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint16_t *k_tree,
+                 const uint16_t *v_tree, const int32_t *path, const int32_t *count, const int32_t *pos, int L, int B,
+                 int N, int T, int W, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
