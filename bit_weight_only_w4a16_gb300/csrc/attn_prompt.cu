@@ -29,7 +29,6 @@ cudaError_t run_attn_prompt(const AttnPromptArgs &p, float *ws, int *err, int nu
     a.tpt = attn::kRowsQ / a.G;
     a.window = p.window;
     a.c = p.scale * 1.4426950408889634f;
-    a.gmin = 1;
     const attn::Rows q = {p.q, p.total_q, p.ldq}, k = {p.k, p.total_k, p.ldk}, v = {p.v, p.total_k, p.ldv};
     auto run = [&](auto shape) {
         using S = decltype(shape);

@@ -48,6 +48,12 @@ constexpr int kKeys = 128;      // keys per tile
 constexpr int kRowsQ = 128;     // rows of one MMA tile
 constexpr int kChunk = 16384;   // ring slot
 constexpr int kSmemChunks = 14; // Q tiles and ring together
+constexpr int kPieces = 4;      // pieces in flight between the warps
+// Cutting the work, a row tile counts as its units and this many more (copying
+// Q, the first scores without a product beside them, reading the accumulator)
+// when there are as many row tiles as CTAs: a run is then at least 1 + kTileCost
+// long and holds a unit. With fewer row tiles the units alone are cut.
+constexpr int kTileCost = 2;
 constexpr int kWaitLimit = 1 << 15;
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
@@ -95,7 +101,6 @@ struct Args {
     int tpt; // tokens per MMA row tile: 128 / G
     int window;
     float c; // scale * log2(e)
-    int gmin; // units a CTA gets at least
 };
 
 struct Maps {
@@ -191,20 +196,16 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
                  : W4_R32(v, 0)                                                                                  \
                  : "r"(addr)                                                                                     \
                  : "memory")
-// 128 columns, as four loads and one wait.
-#define W4_TLD128(v, addr) \
+// 64 columns, as two loads and one wait.
+#define W4_TLD64(v, addr) \
     asm volatile(\
                  "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15," \
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t" \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t" \
                  "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47," \
-                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t" \
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79," \
-                 "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t" \
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111," \
-                 "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t" \
+                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t" \
                  "tcgen05.wait::ld.sync.aligned;" \
-                 : W4_R32(v, 0), W4_R32(v, 32), W4_R32(v, 64), W4_R32(v, 96) \
-                 : "r"(addr), "r"((addr) + 32u), "r"((addr) + 64u), "r"((addr) + 96u) \
+                 : W4_R32(v, 0), W4_R32(v, 32) \
+                 : "r"(addr), "r"((addr) + 32u) \
                  : "memory")
 // 16 columns.
 #define W4_TST16(v, o, addr) \
@@ -302,113 +303,73 @@ __device__ __forceinline__ int tile_units(int lo, int hi)
     return TREE ? n + 1 : max(n, 1);
 }
 
-// One CTA's run of units, as pieces of row tiles.
-template <int D, bool TREE>
-struct Walk {
-    using S = Shape<D>;
-    int hs;        // key/value head * NV + slice
-    int s, i;      // sequence, row tile within it
-    int u;         // first unit of the piece within the row tile
-    long long left; // units of the run from here
-    Seq q;
-    // the piece
-    int t0, nt, lo, hi, n; // first token, tokens, keys, units of the row tile
-    int u1;                // one past the piece's last unit
+// A piece: units [u, u1) of one row tile, as all warps see it.
+struct Piece {
+    int units;         // u1 - u; 0 ends the run
+    int hs;            // key/value head * NV + slice of the value width
+    int s;             // sequence
+    int t0, nt;        // first token within the sequence, tokens
+    int lo, hi;        // keys that any row keeps lie in [lo, hi)
+    int n, u, u1;      // units of the row tile, of the piece
+    int q0, k0;        // the sequence's first query row, first key row
+    int lk, off;       // its keys; position of query row 0 (tree: of depth 0)
+    int nq;            // MMA row tiles that hold any token
 
-    __device__ __forceinline__ void describe(const Args &a)
-    {
-        const int tt = a.tpt * S::TQ;
-        t0 = i * tt;
-        nt = min(tt, q.lq - t0);
-        key_range<TREE>(a, q, t0, nt, lo, hi);
-        n = tile_units<TREE>(lo, hi);
-        u1 = (int)min((long long)n, u + left);
-    }
-    __device__ __forceinline__ void begin(const Args &a, int hs_, int s_, int i_, int u_, long long left_)
-    {
-        hs = hs_;
-        s = s_;
-        i = i_;
-        u = u_;
-        left = left_;
-        if (left > 0) {
-            q = load_seq<TREE>(a, s);
-            describe(a);
-        }
-    }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next(const Args &a)
-    {
-        left -= u1 - u;
-        if (left <= 0)
-            return;
-        u = 0;
-        ++i;
-        const int tt = a.tpt * S::TQ;
-        while (i * tt >= q.lq) { // ends: units are left, so a later sequence (or head) has row tiles
-            i = 0;
-            if (++s == a.B) {
-                s = 0;
-                if (++hs == a.Hkv * S::NV) {
-                    left = 0;
-                    return;
-                }
-            }
-            q = load_seq<TREE>(a, s);
-        }
-        describe(a);
-    }
-    __device__ __forceinline__ int units() const { return u1 - u; }
     __device__ __forceinline__ bool whole() const { return u == 0 && u1 == n; }
-    // Key tile of unit x of the row tile; the tree's own keys follow the cache's.
-    __device__ __forceinline__ bool tree_unit(int x) const { return TREE && x == n - 1; }
-    __device__ __forceinline__ int key0(int x) const { return (lo / kKeys + x) * kKeys; }
-    // MMA row tiles of the piece that hold any token.
-    __device__ __forceinline__ int nq(const Args &a) const { return S::TQ == 1 ? 1 : (nt > a.tpt ? 2 : 1); }
-    // A unit whose value rows need repair: keys outside [lo, hi), keys that only
-    // some rows keep, recorded positions, the tree's own keys.
-    __device__ __forceinline__ bool edge(const Args &a, int x) const
-    {
-        if (TREE) {
-            if (tree_unit(x) || a.kpos)
-                return true;
-            const int k = key0(x);
-            return k + kKeys > hi || k < lo || (a.window > 0 && k < lo + 64);
-        }
-        const int k = key0(x);
-        if (k + kKeys > q.off + t0 + 1 || k + kKeys > hi || k < lo) // past the first row's last key
-            return true;
-        return a.window > 0 && k < q.off + t0 + nt - a.window; // before the last row's first key
-    }
 };
 
+// Key tile of unit x of the row tile; in a tree call the tree's own keys follow
+// the cache's.
+template <bool TREE>
+__device__ __forceinline__ bool tree_unit(const Piece &w, int x)
+{
+    return TREE && x == w.n - 1;
+}
+__device__ __forceinline__ int key0(const Piece &w, int x) { return (w.lo / kKeys + x) * kKeys; }
+
+// A unit whose value rows need repair: keys outside [lo, hi), keys that only
+// some rows keep, recorded positions, the tree's own keys.
+template <bool TREE>
+__device__ __forceinline__ bool edge_unit(const Args &a, const Piece &w, int x)
+{
+    const int k = key0(w, x);
+    if (TREE) {
+        if (tree_unit<TREE>(w, x) || a.kpos)
+            return true;
+        return k + kKeys > w.hi || k < w.lo || (a.window > 0 && k < w.lo + 64);
+    }
+    if (k + kKeys > w.off + w.t0 + 1 || k + kKeys > w.hi || k < w.lo) // past the first row's last key
+        return true;
+    return a.window > 0 && k < w.off + w.t0 + w.nt - a.window; // before the last row's first key
+}
+
 // A value row's part in the product: 0 = kept by every row, 1 = by some, 2 = by none.
-template <int D, bool TREE>
-__device__ __forceinline__ int key_class(const Args &a, const Walk<D, TREE> &w, int x, int j)
+template <bool TREE>
+__device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, int j)
 {
     if (TREE) {
-        if (w.tree_unit(x))
+        if (tree_unit<TREE>(w, x))
             return j < a.N ? 1 : 2;
-        const int k = w.key0(x) + j;
+        const int k = key0(w, x) + j;
         if (k >= a.T)
             return 2;
         const int p = a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
-        if (p < 0 || p >= w.q.off)
+        if (p < 0 || p >= w.off)
             return 2;
         if (a.window > 0) {
-            if ((long long)p <= (long long)w.q.off - a.window)
+            if ((long long)p <= (long long)w.off - a.window)
                 return 2;
-            if ((long long)p <= (long long)w.q.off + (a.N - 1) - a.window)
+            if ((long long)p <= (long long)w.off + (a.N - 1) - a.window)
                 return 1;
         }
         return 0;
     }
-    const int k = w.key0(x) + j;
+    const int k = key0(w, x) + j;
     if (k >= w.hi || k < w.lo)
         return 2;
-    if (k > w.q.off + w.t0)
+    if (k > w.off + w.t0)
         return 1;
-    if (a.window > 0 && k <= w.q.off + w.t0 + w.nt - 1 - a.window)
+    if (a.window > 0 && k <= w.off + w.t0 + w.nt - 1 - a.window)
         return 1;
     return 0;
 }
@@ -420,8 +381,8 @@ struct RowMask {
     unsigned long long nodes; // tree: ancestors or self within the window
 };
 
-template <int D, bool TREE>
-__device__ __forceinline__ RowMask row_mask(const Args &a, const Walk<D, TREE> &w, int tok, bool live)
+template <bool TREE>
+__device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int tok, bool live)
 {
     RowMask m;
     m.live = live;
@@ -442,11 +403,11 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Walk<D, TREE> &
             j = p;
             p = __ldg(par + j);
         }
-        m.hi = a.kpos ? w.q.off : w.q.lk;
-        m.lo = a.window > 0 ? (int)max(0ll, (long long)w.q.off + d - a.window + 1) : 0;
+        m.hi = a.kpos ? w.off : w.lk;
+        m.lo = a.window > 0 ? (int)max(0ll, (long long)w.off + d - a.window + 1) : 0;
     } else {
-        const int at = w.q.off + w.t0 + tok;
-        m.hi = min(at + 1, w.q.lk);
+        const int at = w.off + w.t0 + tok;
+        m.hi = min(at + 1, w.lk);
         m.lo = a.window > 0 ? max(0, at - a.window + 1) : 0;
     }
     return m;
@@ -455,19 +416,19 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Walk<D, TREE> &
 // Adds to a stored output row (or partial) the NaN and infinite values of the
 // keys that warp 2 took out of the product and that this row keeps.
 template <int D, bool TREE, typename Add>
-__device__ __forceinline__ void add_specials(const Args &a, const Walk<D, TREE> &w, const RowMask &m, int kvh,
+__device__ __forceinline__ void add_specials(const Args &a, const Piece &w, const RowMask &m, int kvh,
                                              int dv0, Add add)
 {
 #pragma unroll 1
     for (int x = w.u; x < w.u1; ++x) {
-        if (!w.edge(a, x))
+        if (!edge_unit<TREE>(a, w, x))
             continue;
-        const bool tree = w.tree_unit(x);
+        const bool tree = tree_unit<TREE>(w, x);
 #pragma unroll 1
         for (int j = 0; j < kKeys; ++j) {
-            if (key_class(a, w, x, j) != 1)
+            if (key_class<TREE>(a, w, x, j) != 1)
                 continue;
-            const int k = w.key0(x) + j;
+            const int k = key0(w, x) + j;
             bool kept;
             const uint16_t *row;
             if (tree) {
@@ -476,7 +437,7 @@ __device__ __forceinline__ void add_specials(const Args &a, const Walk<D, TREE> 
             } else {
                 const int p = TREE && a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
                 kept = p >= m.lo && p < m.hi;
-                row = a.v + (size_t)((long long)w.q.k0 + k) * a.ldv + (size_t)kvh * D;
+                row = a.v + (size_t)((long long)w.k0 + k) * a.ldv + (size_t)kvh * D;
             }
             if (!kept)
                 continue;
@@ -496,7 +457,23 @@ struct Bars {
     unsigned long long full[12], efull[12], empty[12];
     unsigned long long q_full, q_empty;
     unsigned long long s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    unsigned long long pc_full[kPieces], pc_empty[kPieces];
 };
+
+// Lanes that differ in bit d of their number swap: the lower one's b for the
+// upper one's a.
+__device__ __forceinline__ void swap4(uint4 &a, uint4 &b, int d, bool upper)
+{
+    uint4 t = upper ? a : b;
+    t.x = __shfl_xor_sync(0xFFFFFFFFu, t.x, d);
+    t.y = __shfl_xor_sync(0xFFFFFFFFu, t.y, d);
+    t.z = __shfl_xor_sync(0xFFFFFFFFu, t.z, d);
+    t.w = __shfl_xor_sync(0xFFFFFFFFu, t.w, d);
+    if (upper)
+        a = t;
+    else
+        b = t;
+}
 
 template <int THREADS>
 __device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
@@ -535,7 +512,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     __shared__ uint32_t tmem_base;
     __shared__ volatile int s_abort;
     __shared__ int s_special[4];
-    __shared__ int s_start[4];
+    __shared__ int s_cut[2][4], s_tiles;
+    __shared__ Piece s_piece[kPieces];
     __shared__ int warp_sums[12];
 
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -558,6 +536,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             mbar_init(smem_addr(&bars.o_free[i]), 4);
         }
         mbar_init(smem_addr(&bars.drain), 1);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_addr(&bars.pc_full[i]), 1);
+            mbar_init(smem_addr(&bars.pc_empty[i]), 3 + 4 * S::TQ);
+        }
         s_abort = 0;
         for (int i = 0; i < 4; ++i)
             s_special[i] = -1;
@@ -573,9 +555,12 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     pdl_wait();
 
     // -------------------------------------------------- this CTA's run
-    Walk<D, TREE> w0;
+    // Row tiles in order of (head and slice, sequence, token), with their units
+    // and kTileCost each, cut at equal costs: s_cut[e] is where the run begins
+    // (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within
+    // the sequence, unit.
     {
-        const int tt = a.tpt * S::TQ;
+        const int tt = a.tpt * S::TQ, HS = a.Hkv * S::NV;
         int *sbase = reinterpret_cast<int *>(smem); // first row tile of each sequence
         int R = 0;
         for (int s0 = 0; s0 < a.B; s0 += S::THREADS) {
@@ -588,7 +573,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             R += total;
         }
         __syncthreads();
-        auto seq_of = [&](int r) { // the last sequence that begins at or before r and is not empty there
+        const int extra = (long long)R * HS >= (long long)gridDim.x ? kTileCost : 0;
+        auto units_of = [&](int r, int &s) {
+            // The last sequence that begins at or before r (empty ones begin where the next does).
             int x = 0, y = a.B - 1;
             while (x < y) {
                 const int m = (x + y + 1) >> 1;
@@ -597,10 +584,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 else
                     y = m - 1;
             }
-            return x;
-        };
-        auto units_of = [&](int r, int &s) {
-            s = seq_of(r);
+            s = x;
             const Seq q = load_seq<TREE>(a, s);
             const int t0 = (r - sbase[s]) * tt;
             int lo, hi;
@@ -611,36 +595,49 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         for (int r0 = 0; r0 < R; r0 += S::THREADS) {
             const int r = r0 + (int)threadIdx.x;
             int total, s;
-            block_scan<S::THREADS>(r < R ? units_of(r, s) : 0, warp_sums, total);
+            block_scan<S::THREADS>(r < R ? units_of(r, s) + extra : 0, warp_sums, total);
             W += total;
         }
-        const long long all = W * a.Hkv * S::NV;
-        const long long ctas = max(1ll, min((long long)gridDim.x, all / a.gmin));
-        const long long c = blockIdx.x;
-        const long long u0 = c < ctas ? all * c / ctas : all, u1 = c < ctas ? all * (c + 1) / ctas : all;
-        const int hs = W > 0 ? (int)(u0 / W) : 0;
-        const long long at = u0 - hs * W;
+        const long long all = W * HS;
+        long long at[2];
+        int hs[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long ctas = max(1ll, min((long long)gridDim.x, all)); // a unit each at least
+            const long long x = all * min((long long)blockIdx.x + e, ctas) / ctas;
+            hs[e] = W > 0 ? (int)(x / W) : 0;
+            at[e] = x - hs[e] * W;
+        }
+        if (threadIdx.x < 2) { // the end of the last run, until a tile claims the place
+            s_cut[threadIdx.x][0] = HS * R;
+            s_cut[threadIdx.x][3] = 0;
+        }
         long long before = 0;
-        for (int r0 = 0; r0 < R && u1 > u0; r0 += S::THREADS) {
+        for (int r0 = 0; r0 < R; r0 += S::THREADS) {
             const int r = r0 + (int)threadIdx.x;
             int total, s = 0;
             const int n = r < R ? units_of(r, s) : 0;
-            const int incl = block_scan<S::THREADS>(n, warp_sums, total);
-            const long long p = before + incl - n;
-            if (n > 0 && at >= p && at < p + n) {
-                s_start[0] = s;
-                s_start[1] = r - sbase[s];
-                s_start[2] = (int)(at - p);
-            }
+            const int cost = n > 0 ? n + extra : 0;
+            const int incl = block_scan<S::THREADS>(cost, warp_sums, total);
+            const long long p = before + incl - cost;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (cost > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost) {
+                    s_cut[e][0] = hs[e] * R + r;
+                    s_cut[e][1] = s;
+                    s_cut[e][2] = r - sbase[s];
+                    s_cut[e][3] = (int)max(0ll, at[e] - p - extra);
+                }
             before += total;
-            if (at < before)
+            if (max(at[0], at[1]) < before)
                 break;
         }
+        if (threadIdx.x == 0)
+            s_tiles = R;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // sbase reads before the ring's copies
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        w0.begin(a, hs, s_start[0], s_start[1], s_start[2], u1 - u0);
     }
     const uint32_t tmem = tmem_base;
     // S (and P over it) in columns [128 b, 128 b + 128), O_t from 256 + t * DV.
@@ -660,14 +657,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         return false;
     };
 
-    // 384 threads: 168 registers each at launch (64512 in all). The softmax threads
-    // hold a row of 128 scores: 208, and 80 for the first four warps (63488 in all).
-    if (S::TQ == 2) {
-        if (warp < 4)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    }
+    // Piece p is in s_piece[p % kPieces] between these two.
+    auto take = [&](uint32_t p) { return wait(bars.pc_full[p % kPieces], (p / kPieces) & 1); };
+    auto done = [&](uint32_t p) { mbar_arrive(smem_addr(&bars.pc_empty[p % kPieces])); };
 
     if (warp == 0) {
         // ---------------------------------------------------- copies
@@ -675,28 +667,35 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             uint32_t g = 0, piece = 0;
             uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
             bool ok = true;
-            Walk<D, TREE> w = w0;
-            for (; ok && w.more(); w.next(a), ++piece) {
+            for (; ok; ++piece) {
+                if (!take(piece)) {
+                    ok = false;
+                    break;
+                }
+                const Piece w = s_piece[piece % kPieces];
+                done(piece);
+                if (w.units == 0)
+                    break;
                 const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
                 if (piece > 0 && !wait(bars.q_empty, (piece - 1) & 1)) {
                     ok = false;
                     break; // the Q copies waited for below are the previous piece's
                 }
-                const int nq = w.nq(a), units = w.units();
+                const int nq = w.nq, units = w.units;
                 mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(nq * S::KC * a.tpt * a.G * 128));
                 for (int t = 0; t < nq; ++t)
                     for (int c = 0; c < S::KC; ++c)
                         tma_3d(q_base + (t * S::KC + c) * kChunk, &maps.q, 64 * c, kvh * a.G,
-                               w.q.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
+                               w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
                 auto slot_wait = [&]() {
                     const uint32_t u = g / S::NS;
                     return u == 0 || wait(bars.empty[g % S::NS], (u - 1) & 1);
                 };
                 auto keys = [&](int j) {
                     const int x = w.u + j;
-                    const bool tr = w.tree_unit(x);
+                    const bool tr = tree_unit<TREE>(w, x);
                     const CUtensorMap *m = tr ? &maps.kt : &maps.k;
-                    const int row = tr ? w.s * a.N : w.q.k0 + w.key0(x);
+                    const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::KC; ++c, ++g) {
                         if (!slot_wait())
                             return false;
@@ -709,9 +708,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 };
                 auto values = [&](int j) {
                     const int x = w.u + j;
-                    const bool tr = w.tree_unit(x), edge = w.edge(a, x);
+                    const bool tr = tree_unit<TREE>(w, x), edge = edge_unit<TREE>(a, w, x);
                     const CUtensorMap *m = tr ? &maps.vt : &maps.v;
-                    const int row = tr ? w.s * a.N : w.q.k0 + w.key0(x);
+                    const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::VC; ++c, ++g) {
                         if (!slot_wait())
                             return false;
@@ -755,7 +754,6 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
             uint32_t g = 0, piece = 0, it = 0; // chunks, pieces, units so far
             bool ok = true;
-            Walk<D, TREE> w = w0;
             // S_b = Q_t K^T from chunks gk ..; `last` frees them.
             auto scores = [&](int t, int b, uint32_t gk, bool first, bool last) {
                 for (int c = 0; c < S::KC; ++c) {
@@ -792,10 +790,12 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 return true;
             };
             uint32_t itq[2] = {0, 0}, pcq[2] = {0, 0}; // units and pieces of each row tile (TQ == 2)
-            for (; ok && w.more(); w.next(a), ++piece) {
-                const int units = w.units(), nq = w.nq(a);
-                ok = wait(bars.q_full, piece & 1);
-                if (!ok)
+            for (; ok; ++piece) {
+                if (!(ok = take(piece)))
+                    break;
+                const int units = s_piece[piece % kPieces].units, nq = s_piece[piece % kPieces].nq;
+                done(piece);
+                if (units == 0 || !(ok = wait(bars.q_full, piece & 1)))
                     break;
                 if (S::TQ == 1) {
                     ok = scores(0, it & 1, g, true, true);
@@ -850,12 +850,20 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         uint32_t base = 0, par = 0; // chunks before the piece; phase of each slot's edge barrier
         int piece = 0;
         bool ok = true;
-        Walk<D, TREE> w = w0;
-        for (; ok && w.more(); w.next(a), ++piece) {
-            const int units = w.units();
+        for (; ok; ++piece) {
+            ok = __all_sync(0xFFFFFFFFu, take(piece));
+            if (!ok)
+                break;
+            const Piece w = s_piece[piece % kPieces];
+            __syncwarp();
+            if (lane == 0)
+                done(piece);
+            const int units = w.units;
+            if (units == 0)
+                break;
             for (int j = 0; ok && j < units; ++j) {
                 const int x = w.u + j;
-                if (!w.edge(a, x))
+                if (!edge_unit<TREE>(a, w, x))
                     continue;
                 const uint32_t gv = base + (uint32_t)(j * (S::KC + S::VC) + S::KC) +
                                     (S::TQ == 1 && j + 1 < units ? S::KC : 0);
@@ -865,7 +873,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     uint32_t cls = 0;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
-                        cls |= (uint32_t)key_class(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
+                        cls |= (uint32_t)key_class<TREE>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
                     ok = __all_sync(0xFFFFFFFFu, wait(bars.efull[slot], (par >> slot) & 1));
                     if (!ok)
                         break;
@@ -931,17 +939,26 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         const int tok_in = row / a.G, head = row - tok_in * a.G;
         uint32_t it = 0, piece = 0; // units of this row tile; pieces of the run
         bool ok = true;
-        Walk<D, TREE> w = w0;
-        for (; ok && w.more(); w.next(a), ++piece) {
-            const int units = w.units(), kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
-            if (t >= w.nq(a))
+        for (; ok; ++piece) {
+            ok = __all_sync(0xFFFFFFFFu, take(piece));
+            if (!ok)
+                break;
+            const Piece &w = s_piece[piece % kPieces];
+            const int units = w.units;
+            if (units == 0)
+                break;
+            if (t >= w.nq) {
+                __syncwarp();
+                if (lane == 0)
+                    done(piece);
                 continue;
+            }
             const int tok = t * a.tpt + tok_in;
-            const RowMask rm = row_mask(a, w, tok, tok_in < a.tpt && tok < w.nt);
+            const RowMask rm = row_mask<TREE>(a, w, tok, tok_in < a.tpt && tok < w.nt);
             float m = -INFINITY, l = 0.f;
             for (int j = 0; ok && j < units; ++j, ++it) {
-                const int x = w.u + j, key0 = w.key0(x);
-                const bool tr = w.tree_unit(x);
+                const int x = w.u + j, kb = key0(w, x);
+                const bool tr = tree_unit<TREE>(w, x);
                 const uint32_t b = S::TQ == 1 ? (it & 1) : (uint32_t)t;
                 const uint32_t ph = S::TQ == 1 ? (it >> 1) & 1 : it & 1;
                 // Kept keys of this row, one bit each; `all`: the warp keeps every key.
@@ -957,10 +974,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     const int lo = rm.hi > 0 ? rm.lo : 0x7FFFFFFF; // rm.hi = 0: an absent node
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        const int k = key0 + 32 * h + lane;
+                        const int k = kb + 32 * h + lane;
                         const int p = k < a.T ? __ldg(a.kpos + (size_t)w.s * a.T + k) : -1;
-                        const bool in = p >= 0 && p < w.q.off;
-                        const bool every = in && (a.window <= 0 || (long long)p + a.window > (long long)w.q.off + a.N);
+                        const bool in = p >= 0 && p < w.off;
+                        const bool every = in && (a.window <= 0 || (long long)p + a.window > (long long)w.off + a.N);
                         uint32_t some = __ballot_sync(0xFFFFFFFFu, in && !every);
                         km[h] = __ballot_sync(0xFFFFFFFFu, every);
                         if (lo == 0x7FFFFFFF)
@@ -973,7 +990,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         }
                     }
                 } else {
-                    const int lo = rm.lo - key0, hi = rm.hi - key0;
+                    const int lo = rm.lo - kb, hi = rm.hi - kb;
                     all = __all_sync(0xFFFFFFFFu, !rm.live || (lo <= 0 && hi >= kKeys));
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
@@ -983,24 +1000,37 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 if (!ok)
                     break;
                 tc_fence_after();
-                uint32_t v[128];
+                // The row's 128 scores in two halves of 64 registers: the upper half is
+                // read for the maximum, the lower half for the maximum and its weights,
+                // then the upper half again (P goes over columns that were read).
                 const uint32_t sa = s_col(b) + lanes;
-                W4_TLD128(v, sa);
-                constexpr uint32_t kNegInf = 0xFF800000u;
-                if (!all) {
+                uint32_t v[64];
+                auto mask = [&](int h0) {
+                    if (!all) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (!((km[i >> 5] >> (i & 31)) & 1u))
-                            v[i] = kNegInf;
-                }
-                float mx[4];
+                        for (int i = 0; i < 64; ++i)
+                            if (!((km[h0 + (i >> 5)] >> (i & 31)) & 1u))
+                                v[i] = 0xFF800000u;
+                    }
+                };
+                auto most = [&]() {
+                    float mx[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    mx[q] = __uint_as_float(v[q]);
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = fmaxf(__uint_as_float(v[q]), __uint_as_float(v[q + 4]));
 #pragma unroll
-                for (int i = 4; i < 128; ++i)
-                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                    for (int i = 8; i < 64; i += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[i + q]), __uint_as_float(v[i + q + 4])));
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                W4_TLD64(v, sa + 64u);
+                mask(2);
+                float mt = most();
+                W4_TLD64(v, sa);
+                mask(0);
+                mt = fmaxf(mt, most()) * a.c;
                 float alpha = 1.f;
                 if (rm.live && mt > m + 8.f) { // also the first kept key (m = -inf)
                     alpha = ex2(m - mt);
@@ -1025,18 +1055,24 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 }
                 const float mm = m == -INFINITY ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                auto weights = [&](uint32_t to) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i]), a.c, -mm));
-                        const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i + 1]), a.c, -mm));
-                        sum[i & 3] += p0 + p1;
-                        pk[i] = pack2(p0, p1);
+                        for (int i = 0; i < 16; ++i) {
+                            const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i]), a.c, -mm));
+                            const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i + 1]), a.c, -mm));
+                            sum[i & 3] += p0 + p1;
+                            pk[i] = pack2(p0, p1);
+                        }
+                        W4_TST16(pk, 0, to + 16u * c);
                     }
-                    W4_TST16(pk, 0, sa + 16u * c);
-                }
+                };
+                weights(sa);
+                W4_TLD64(v, sa + 64u);
+                mask(2);
+                weights(sa + 32u);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc_wait_st();
                 tc_fence_before();
@@ -1055,34 +1091,62 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 break;
             tc_fence_after();
             const bool whole = w.whole(), special = s_special[piece & 3] == (int)piece;
-            uint16_t *orow = a.out + (size_t)((long long)w.q.q0 + w.t0 + tok) * a.ldo +
+            const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
+            uint16_t *orow = a.out + (size_t)((long long)w.q0 + w.t0 + tok) * a.ldo +
                              (size_t)(kvh * a.G + head) * D + dv0;
             const int slot = 2 * (int)blockIdx.x + (w.u == 0 ? 1 : 0);
             // Partial accumulators: [slot][DV / 4][ROWS] float4.
             float4 *prow = reinterpret_cast<float4 *>(a.ws_o + (size_t)slot * kSlotFloats) + t * kRowsQ + row;
             const float f = l == 0.f ? 0.f : 1.f / l; // nothing kept: zeros
-#pragma unroll 1
-            for (int c0 = 0; c0 < S::DV; c0 += 32) {
-                uint32_t o[32];
-                W4_TLD32(o, o_col(t) + lanes + c0);
-                if (rm.live && whole) {
+            if (whole) {
+                // Four lanes exchange their rows' 16-byte parts, so that a store writes
+                // 64 contiguous bytes of a row (rows 4 g + i of lanes 4 g .. 4 g + 3).
+                uint16_t *to[4];
+                bool live[4];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 y;
-                        y.x = pack2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f);
-                        y.y = pack2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
-                        y.z = pack2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f);
-                        y.w = pack2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f);
-                        *reinterpret_cast<uint4 *>(orow + c0 + i) = y;
-                    }
-                } else if (rm.live) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        prow[(size_t)((c0 + i) / 4) * S::ROWS] =
-                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                        __uint_as_float(o[i + 3]));
+                for (int i = 0; i < 4; ++i) {
+                    const int src = (lane & 28) + i;
+                    to[i] = reinterpret_cast<uint16_t *>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)orow, src)) +
+                            8 * (lane & 3);
+                    live[i] = __shfl_sync(0xFFFFFFFFu, (int)rm.live, src) != 0;
                 }
-                __syncwarp();
+#pragma unroll 1
+                for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                    uint32_t o[32];
+                    W4_TLD32(o, o_col(t) + lanes + c0);
+                    uint4 y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i].x = pack2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f);
+                        y[i].y = pack2(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f);
+                        y[i].z = pack2(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f);
+                        y[i].w = pack2(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f);
+                    }
+#pragma unroll
+                    for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(i & d))
+                                swap4(y[i], y[i ^ d], d, (lane & d) != 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (live[i])
+                            *reinterpret_cast<uint4 *>(to[i] + c0) = y[i];
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                    uint32_t o[32];
+                    W4_TLD32(o, o_col(t) + lanes + c0);
+                    if (rm.live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            prow[(size_t)((c0 + i) / 4) * S::ROWS] =
+                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                            __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                    }
+                    __syncwarp();
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -1093,8 +1157,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 ml[0] = m;
                 ml[1] = l;
             }
+            if (special)
+                __syncwarp(); // a row's output may come from its neighbour lanes
             if (special && rm.live)
-                add_specials(a, w, rm, kvh, dv0, [&](int d, float f) {
+                add_specials<D, TREE>(a, w, rm, kvh, dv0, [&](int d, float f) {
                     if (whole) {
                         const float o = __uint_as_float((uint32_t)orow[d] << 16) + f;
                         orow[d] = (uint16_t)(pack2(o, 0.f) & 0xFFFFu);
@@ -1102,22 +1168,68 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         reinterpret_cast<float *>(prow + (size_t)(d / 4) * S::ROWS)[d & 3] += f;
                     }
                 });
+            __syncwarp();
+            if (lane == 0)
+                done(piece);
         }
     } else if (lane == 0) {
-        // warp 3: what the merge needs to know about this CTA's partials.
+        // ------------- warp 3: the run's pieces, and what the merge needs to know
+        const int tt = a.tpt * S::TQ;
         int cont = 0, begins = 0;
-        Walk<D, TREE> w = w0;
-        for (; w.more(); w.next(a)) {
-            if (w.u > 0)
+        int tile = s_cut[0][0], s = s_cut[0][1], i = s_cut[0][2], u = s_cut[0][3];
+        const int end = s_cut[1][0], end_u = s_cut[1][3];
+        uint32_t piece = 0;
+        bool ok = true;
+        Seq q = {};
+        if (tile < end || (tile == end && u < end_u))
+            q = load_seq<TREE>(a, s);
+        while (ok && (tile < end || (tile == end && u < end_u))) {
+            Piece w;
+            w.hs = tile / s_tiles;
+            w.s = s;
+            w.t0 = i * tt;
+            w.nt = min(tt, q.lq - w.t0);
+            key_range<TREE>(a, q, w.t0, w.nt, w.lo, w.hi);
+            w.n = tile_units<TREE>(w.lo, w.hi);
+            w.u = u;
+            w.u1 = tile == end ? end_u : w.n;
+            w.units = w.u1 - w.u;
+            w.q0 = q.q0;
+            w.k0 = q.k0;
+            w.lk = q.lk;
+            w.off = q.off;
+            w.nq = S::TQ == 1 ? 1 : (w.nt > a.tpt ? 2 : 1);
+            if (piece >= (uint32_t)kPieces)
+                ok = wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1);
+            if (!ok)
+                break;
+            s_piece[piece % kPieces] = w;
+            mbar_arrive(smem_addr(&bars.pc_full[piece % kPieces]));
+            ++piece;
+            if (w.u > 0) {
                 cont = 1 | (w.u1 == w.n ? 2 : 0);
-            else if (!w.whole()) {
+            } else if (!w.whole()) {
                 begins = 1;
                 int32_t *p = a.where + 4 * blockIdx.x;
-                p[0] = w.q.q0 + w.t0;
+                p[0] = w.q0 + w.t0;
                 p[1] = w.nt;
                 p[2] = w.hs / S::NV;
                 p[3] = w.hs % S::NV;
             }
+            u = 0;
+            ++i;
+            if (++tile > end || (tile == end && end_u == 0))
+                break;
+            while (i * tt >= q.lq) { // ends: there is another row tile
+                i = 0;
+                s = s + 1 < a.B ? s + 1 : 0;
+                q = load_seq<TREE>(a, s);
+            }
+        }
+        if (ok && (piece < (uint32_t)kPieces ||
+                   wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1))) {
+            s_piece[piece % kPieces].units = 0;
+            mbar_arrive(smem_addr(&bars.pc_full[piece % kPieces]));
         }
         a.rec[2 * blockIdx.x] = cont;
         a.rec[2 * blockIdx.x + 1] = begins;

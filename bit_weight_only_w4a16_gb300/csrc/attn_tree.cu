@@ -33,7 +33,6 @@ cudaError_t run_attn_tree(const AttnTreeArgs &p, float *ws, int *err, int num_sm
     a.tpt = attn::kRowsQ / a.G;
     a.window = p.window;
     a.c = p.scale * 1.4426950408889634f;
-    a.gmin = 1;
     const long long rows = (long long)p.B * p.N, slots = (long long)p.B * p.T;
     const attn::Rows q = {p.q, rows, a.ldo}, k = {p.k, slots, a.ldv}, v = {p.v, slots, a.ldv};
     const attn::Rows kt = {p.k_tree, rows, a.ldv}, vt = {p.v_tree, rows, a.ldv};
