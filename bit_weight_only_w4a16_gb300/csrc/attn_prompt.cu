@@ -35,7 +35,7 @@ cudaError_t run_attn_prompt(const AttnPromptArgs &p, float *ws, int *err, int nu
         const long long tt = (long long)a.tpt * S::TQ;
         const long long tiles = (p.total_q / tt + p.B) * p.Hkv * S::NV;
         const bool may_cut = p.total_k > attn::kKeys;
-        return attn::launch<S::KC * 64, false>(a, q, k, v, k, v, tiles, may_cut, ws, num_sms, s);
+        return attn::launch<S::DIM, false>(a, q, k, v, k, v, tiles, may_cut, ws, num_sms, s);
     };
     switch (p.D) {
     case 64: return run(attn::Shape<64>{});

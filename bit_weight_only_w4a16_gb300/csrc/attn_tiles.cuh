@@ -22,10 +22,10 @@
 // tile that was cut leaves partial sums (accumulator, m, sum) in the scratch,
 // which a second kernel merges in key order (deterministic).
 //
-//   warp 0    tensor copies: the Q tile, then K and V chunks (16 KiB) through a ring
+//   warp 0    tensor copies: the Q tile, then K and V stages (32 KiB) through a ring
 //   warp 1    issues tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
 //             read from tensor memory
-//   warp 2    repairs V chunks of edge tiles in shared memory: the rows that no
+//   warp 2    repairs V stages of edge tiles in shared memory: the rows that no
 //             query row keeps become zeros (0 * NaN would poison the product)
 //   warps 4+  softmax: one thread per row, scores from tensor memory, P back
 //             over them; at the end of a row tile the same threads read O
@@ -46,8 +46,8 @@ namespace attn {
 
 constexpr int kKeys = 128;      // keys per tile
 constexpr int kRowsQ = 128;     // rows of one MMA tile
-constexpr int kChunk = 16384;   // ring slot
-constexpr int kSmemChunks = 14; // Q tiles and ring together
+constexpr int kBlock = 16384;   // 128 rows x 64 dims: a block of Q or K
+constexpr int kSmemBlocks = 14; // Q tiles and ring together
 constexpr int kPieces = 4;      // pieces in flight between the warps
 // Cutting the work, a row tile counts as its units and this many more (copying
 // Q, the first scores without a product beside them, reading the accumulator)
@@ -59,20 +59,26 @@ constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is sta
 
 template <int D>
 struct Shape {
+    static constexpr int DIM = D;
     static constexpr int NV = D > 256 ? 2 : 1;       // slices of the value width (tensor memory holds 256 columns of O)
     static constexpr int DV = D / NV;                // width of a slice
     static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
-    static constexpr int KC = D / 64;                // key chunks per tile: 128 keys x 64 dims
-    static constexpr int VKEYS = DV == 64 ? 128 : (DV == 128 ? 64 : 32); // keys per value chunk
-    static constexpr int VC = kKeys / VKEYS;
+    static constexpr int QB = D / 64;                // blocks of a row tile's Q
+    // Ring stages of two blocks: waiting for a stage, issuing its products and
+    // freeing it costs the issuing thread as much as the products take when a
+    // stage is one block (16 KiB).
+    static constexpr int STAGE = D == 64 ? kBlock : 2 * kBlock;
+    static constexpr int KC = D * kKeys * 2 / STAGE;                         // key stages per tile
+    static constexpr int KB = STAGE / kBlock;                                // blocks of a key stage
+    static constexpr int VKEYS = DV <= 128 ? 128 : 64;                       // keys per value stage
+    static constexpr int VC = kKeys / VKEYS;                                 // value stages per tile
     static constexpr int VBYTES = VKEYS * DV * 2;
-    static constexpr int QCHUNKS = TQ * KC;
-    static constexpr int NS = kSmemChunks - QCHUNKS; // ring slots
+    static constexpr int NS = (kSmemBlocks - TQ * QB) * kBlock / STAGE;      // ring stages
     static constexpr int ROWS = TQ * kRowsQ;
     static constexpr int THREADS = 128 + TQ * 128;
-    static constexpr size_t SMEM = (size_t)kSmemChunks * kChunk + 1024;
-    static_assert(VBYTES <= kChunk, "value chunk");
-    static_assert(NS >= 6, "ring");
+    static constexpr size_t SMEM = (size_t)kSmemBlocks * kBlock + 1024;
+    static_assert(VBYTES <= STAGE, "value stage");
+    static_assert(NS >= 3 && NS <= 12, "ring");
 };
 
 // Scratch of a call with `grid` CTAs (floats): accumulators, (m, sum) per row,
@@ -165,6 +171,15 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
                  "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
                  : "memory");
+}
+
+// One lane of the warp, in a form the compiler knows to be a single thread:
+// issuing products from `lane == 0` instead took twice as long per instruction.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -518,7 +533,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t q_base = smem_addr(smem);
-    const uint32_t ring = q_base + S::QCHUNKS * kChunk;
+    const uint32_t ring = q_base + S::TQ * S::QB * kBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -663,7 +678,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     if (warp == 0) {
         // ---------------------------------------------------- copies
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t g = 0, piece = 0;
             uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
             bool ok = true;
@@ -682,10 +697,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     break; // the Q copies waited for below are the previous piece's
                 }
                 const int nq = w.nq, units = w.units;
-                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(nq * S::KC * a.tpt * a.G * 128));
+                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(nq * S::QB * a.tpt * a.G * 128));
                 for (int t = 0; t < nq; ++t)
-                    for (int c = 0; c < S::KC; ++c)
-                        tma_3d(q_base + (t * S::KC + c) * kChunk, &maps.q, 64 * c, kvh * a.G,
+                    for (int c = 0; c < S::QB; ++c)
+                        tma_3d(q_base + (t * S::QB + c) * kBlock, &maps.q, 64 * c, kvh * a.G,
                                w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
                 auto slot_wait = [&]() {
                     const uint32_t u = g / S::NS;
@@ -701,8 +716,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             return false;
                         const uint32_t slot = g % S::NS, bar = smem_addr(&bars.full[slot]);
                         onedge &= ~(1u << slot);
-                        mbar_arrive_expect_tx(bar, kChunk);
-                        tma_3d(ring + slot * kChunk, m, 64 * c, kvh, row, bar);
+                        mbar_arrive_expect_tx(bar, S::STAGE);
+#pragma unroll
+                        for (int b = 0; b < S::KB; ++b)
+                            tma_3d(ring + slot * S::STAGE + b * kBlock, m, 64 * (c * S::KB + b), kvh, row, bar);
                     }
                     return true;
                 };
@@ -721,7 +738,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         mbar_arrive_expect_tx(bar, S::VBYTES);
 #pragma unroll
                         for (int b = 0; b < S::DV / 64; ++b)
-                            tma_3d(ring + slot * kChunk + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
+                            tma_3d(ring + slot * S::STAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
                                    row + c * S::VKEYS, bar);
                     }
                     return true;
@@ -750,22 +767,24 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issue
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
-            uint32_t g = 0, piece = 0, it = 0; // chunks, pieces, units so far
+            uint32_t g = 0, piece = 0, it = 0; // stages, pieces, units so far
             bool ok = true;
-            // S_b = Q_t K^T from chunks gk ..; `last` frees them.
+            // S_b = Q_t K^T from stages gk ..; `last` frees them.
             auto scores = [&](int t, int b, uint32_t gk, bool first, bool last) {
                 for (int c = 0; c < S::KC; ++c) {
                     const uint32_t gg = gk + c, slot = gg % S::NS;
                     if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
                         return false;
                     tc_fence_after();
-                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::KC + c) * kChunk);
-                    const uint64_t bd = sdesc_kmajor(ring + slot * kChunk);
+                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
+                    const uint64_t bd = sdesc_kmajor(ring + slot * S::STAGE);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(s_col(b), ad + 2u * k, bd + 2u * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < 4 * S::KB; ++k) {
+                        const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
+                        mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                    }
                     if (last)
                         mma_commit(smem_addr(&bars.empty[slot]));
                 }
@@ -778,7 +797,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
                         return false;
                     tc_fence_after();
-                    const uint64_t bd = sdesc_mnmajor(ring + slot * kChunk, S::VKEYS * 128);
+                    const uint64_t bd = sdesc_mnmajor(ring + slot * S::STAGE, S::VKEYS * 128);
 #pragma unroll
                     for (int k = 0; k < S::VKEYS / 16; ++k)
                         mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
@@ -847,7 +866,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         }
     } else if (warp == 2) {
         // ------------------------------------- value rows of edge tiles
-        uint32_t base = 0, par = 0; // chunks before the piece; phase of each slot's edge barrier
+        uint32_t base = 0, par = 0; // stages before the piece; phase of each slot's edge barrier
         int piece = 0;
         bool ok = true;
         for (; ok; ++piece) {
@@ -869,7 +888,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                                     (S::TQ == 1 && j + 1 < units ? S::KC : 0);
                 for (int c = 0; ok && c < S::VC; ++c) {
                     const uint32_t slot = (gv + c) % S::NS;
-                    // Classes of this chunk's keys: key c * VKEYS + 32 h + lane in bits 2h, 2h + 1.
+                    // Classes of this stage's keys: key c * VKEYS + 32 h + lane in bits 2h, 2h + 1.
                     uint32_t cls = 0;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
@@ -878,7 +897,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     if (!ok)
                         break;
                     par ^= 1u << slot;
-                    const uint32_t vb = ring + slot * kChunk;
+                    const uint32_t vb = ring + slot * S::STAGE;
                     bool found = false;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h) {

@@ -40,7 +40,7 @@ cudaError_t run_attn_tree(const AttnTreeArgs &p, float *ws, int *err, int num_sm
         using S = decltype(shape);
         const int tt = a.tpt * S::TQ;
         const long long tiles = (long long)p.B * ((p.N + tt - 1) / tt) * p.Hkv * S::NV;
-        return attn::launch<S::KC * 64, true>(a, q, k, v, kt, vt, tiles, true, ws, num_sms, s);
+        return attn::launch<S::DIM, true>(a, q, k, v, kt, vt, tiles, true, ws, num_sms, s);
     };
     switch (p.D) {
     case 64: return run(attn::Shape<64>{});
