@@ -22,12 +22,15 @@
 // tile that was cut leaves partial sums (accumulator, m, sum) in the scratch,
 // which a second kernel merges in key order (deterministic).
 //
-//   warp 0    tensor copies: the Q tile, then K and V stages (32 KiB) through a ring
-//   warp 1    issues tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
-//             read from tensor memory
+//   warp 0    tensor copies: the Q tile, then K and V stages through a ring each
+//   warp 1    issues S = Q K^T into tensor memory
+//   last warp issues O += P V with P read from tensor memory. Two issuing threads:
+//             waiting on a barrier (about 150 cycles even when it is complete) and
+//             issuing take one thread longer than the tensor core needs
 //   warp 2    repairs V stages of edge tiles in shared memory: the rows that no
 //             query row keeps become zeros (0 * NaN would poison the product)
-//   warps 4+  softmax: one thread per row, scores from tensor memory, P back
+//   warp 3    announces the run's pieces of row tiles
+//   4 warps per MMA row tile  softmax: one thread per row, scores from tensor memory, P back
 //             over them; at the end of a row tile the same threads read O
 //
 // Value rows that some rows of a tile keep and others do not (the diagonal, a
@@ -47,7 +50,8 @@ namespace attn {
 constexpr int kKeys = 128;      // keys per tile
 constexpr int kRowsQ = 128;     // rows of one MMA tile
 constexpr int kBlock = 16384;   // 128 rows x 64 dims: a block of Q or K
-constexpr int kSmemBlocks = 14; // Q tiles and ring together
+constexpr int kSmemBlocks = 14; // Q tiles and rings together, at most
+constexpr int kMaxSlots = 6;    // slots of a ring
 constexpr int kPieces = 4;      // pieces in flight between the warps
 // Cutting the work, a row tile counts as its units and this many more (copying
 // Q, the first scores without a product beside them, reading the accumulator)
@@ -64,21 +68,25 @@ struct Shape {
     static constexpr int DV = D / NV;                // width of a slice
     static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
     static constexpr int QB = D / 64;                // blocks of a row tile's Q
-    // Ring stages of two blocks: waiting for a stage, issuing its products and
-    // freeing it costs the issuing thread as much as the products take when a
-    // stage is one block (16 KiB).
-    static constexpr int STAGE = D == 64 ? kBlock : 2 * kBlock;
-    static constexpr int KC = D * kKeys * 2 / STAGE;                         // key stages per tile
-    static constexpr int KB = STAGE / kBlock;                                // blocks of a key stage
-    static constexpr int VKEYS = DV <= 128 ? 128 : 64;                       // keys per value stage
-    static constexpr int VC = kKeys / VKEYS;                                 // value stages per tile
-    static constexpr int VBYTES = VKEYS * DV * 2;
-    static constexpr int NS = (kSmemBlocks - TQ * QB) * kBlock / STAGE;      // ring stages
+    // Two rings, one for each issuing thread: a parity wait tells only
+    // neighbouring uses of a slot apart, so a thread must see every use of its
+    // slots. Stages of up to 32 KiB: waiting for a stage, issuing its products and
+    // freeing it costs a thread as much as the products take at 16 KiB.
+    static constexpr int KB = D == 64 ? 1 : 2;                  // blocks of a key stage
+    static constexpr int KSTAGE = KB * kBlock;
+    static constexpr int KC = QB / KB;                          // key stages per tile
+    static constexpr int VKEYS = DV <= 128 ? 128 : (D == 256 ? 64 : 32); // keys per value stage
+    static constexpr int VC = kKeys / VKEYS;                    // value stages per tile
+    static constexpr int VSTAGE = VKEYS * DV * 2;
+    static constexpr int NK = D == 64 ? 6 : (D <= 256 ? 3 : 2); // ring slots
+    static constexpr int NVS = D == 64 ? 6 : (D == 384 ? 5 : 2);
     static constexpr int ROWS = TQ * kRowsQ;
-    static constexpr int THREADS = 128 + TQ * 128;
-    static constexpr size_t SMEM = (size_t)kSmemBlocks * kBlock + 1024;
-    static_assert(VBYTES <= STAGE, "value stage");
-    static_assert(NS >= 3 && NS <= 12, "ring");
+    static constexpr int PV_WARP = 4 + 4 * TQ;       // the last warp
+    static constexpr int THREADS = 32 * (PV_WARP + 1);
+    static constexpr int QBYTES = TQ * QB * kBlock;
+    static constexpr size_t SMEM = (size_t)QBYTES + NK * KSTAGE + NVS * VSTAGE + 1024;
+    static_assert(VSTAGE % 1024 == 0 && NK <= kMaxSlots && NVS <= kMaxSlots, "rings");
+    static_assert(SMEM <= (size_t)kSmemBlocks * kBlock + 1024, "shared memory");
 };
 
 // Scratch of a call with `grid` CTAs (floats): accumulators, (m, sum) per row,
@@ -469,9 +477,10 @@ __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, cons
 // ------------------------------------------------------------- kernel ----
 
 struct Bars {
-    unsigned long long full[12], efull[12], empty[12];
+    unsigned long long kfull[kMaxSlots], kempty[kMaxSlots];
+    unsigned long long vfull[kMaxSlots], vedge[kMaxSlots], vempty[kMaxSlots];
     unsigned long long q_full, q_empty;
-    unsigned long long s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    unsigned long long s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], drain[2];
     unsigned long long pc_full[kPieces], pc_empty[kPieces];
 };
 
@@ -529,31 +538,34 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     __shared__ int s_special[4];
     __shared__ int s_cut[2][4], s_tiles;
     __shared__ Piece s_piece[kPieces];
-    __shared__ int warp_sums[12];
+    __shared__ int warp_sums[16];
 
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t q_base = smem_addr(smem);
-    const uint32_t ring = q_base + S::TQ * S::QB * kBlock;
+    const uint32_t kring = q_base + S::QBYTES, vring = kring + S::NK * S::KSTAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::NS; ++i) {
-            mbar_init(smem_addr(&bars.full[i]), 1);
-            mbar_init(smem_addr(&bars.efull[i]), 1);
-            mbar_init(smem_addr(&bars.empty[i]), 1);
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(smem_addr(&bars.kfull[i]), 1);
+            mbar_init(smem_addr(&bars.kempty[i]), 1);
+            mbar_init(smem_addr(&bars.vfull[i]), 1);
+            mbar_init(smem_addr(&bars.vedge[i]), 1); // a copied stage that warp 2 repairs before vfull
+            mbar_init(smem_addr(&bars.vempty[i]), 1);
         }
         mbar_init(smem_addr(&bars.q_full), 1);
         mbar_init(smem_addr(&bars.q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.s_full[i]), 1);
+            mbar_init(smem_addr(&bars.s_free[i]), 1);
+            mbar_init(smem_addr(&bars.drain[i]), 1);
             mbar_init(smem_addr(&bars.p_full[i]), 4);
             mbar_init(smem_addr(&bars.o_done[i]), 1);
             mbar_init(smem_addr(&bars.o_free[i]), 4);
         }
-        mbar_init(smem_addr(&bars.drain), 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&bars.pc_full[i]), 1);
-            mbar_init(smem_addr(&bars.pc_empty[i]), 3 + 4 * S::TQ);
+            mbar_init(smem_addr(&bars.pc_empty[i]), 4 + 4 * S::TQ);
         }
         s_abort = 0;
         for (int i = 0; i < 4; ++i)
@@ -679,8 +691,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     if (warp == 0) {
         // ---------------------------------------------------- copies
         if (elect_one()) {
-            uint32_t g = 0, piece = 0;
-            uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
+            uint32_t gk = 0, gv = 0, piece = 0; // key and value stages, pieces so far
+            uint32_t par = 0, onedge = 0; // per value slot: uses of its edge barrier (parity), the last use was one
             bool ok = true;
             for (; ok; ++piece) {
                 if (!take(piece)) {
@@ -702,24 +714,20 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     for (int c = 0; c < S::QB; ++c)
                         tma_3d(q_base + (t * S::QB + c) * kBlock, &maps.q, 64 * c, kvh * a.G,
                                w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
-                auto slot_wait = [&]() {
-                    const uint32_t u = g / S::NS;
-                    return u == 0 || wait(bars.empty[g % S::NS], (u - 1) & 1);
-                };
                 auto keys = [&](int j) {
                     const int x = w.u + j;
                     const bool tr = tree_unit<TREE>(w, x);
                     const CUtensorMap *m = tr ? &maps.kt : &maps.k;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
-                    for (int c = 0; c < S::KC; ++c, ++g) {
-                        if (!slot_wait())
+                    for (int c = 0; c < S::KC; ++c, ++gk) {
+                        const uint32_t slot = gk % S::NK, use = gk / S::NK;
+                        if (use > 0 && !wait(bars.kempty[slot], (use - 1) & 1))
                             return false;
-                        const uint32_t slot = g % S::NS, bar = smem_addr(&bars.full[slot]);
-                        onedge &= ~(1u << slot);
-                        mbar_arrive_expect_tx(bar, S::STAGE);
+                        const uint32_t bar = smem_addr(&bars.kfull[slot]);
+                        mbar_arrive_expect_tx(bar, S::KSTAGE);
 #pragma unroll
                         for (int b = 0; b < S::KB; ++b)
-                            tma_3d(ring + slot * S::STAGE + b * kBlock, m, 64 * (c * S::KB + b), kvh, row, bar);
+                            tma_3d(kring + slot * S::KSTAGE + b * kBlock, m, 64 * (c * S::KB + b), kvh, row, bar);
                     }
                     return true;
                 };
@@ -728,17 +736,17 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     const bool tr = tree_unit<TREE>(w, x), edge = edge_unit<TREE>(a, w, x);
                     const CUtensorMap *m = tr ? &maps.vt : &maps.v;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
-                    for (int c = 0; c < S::VC; ++c, ++g) {
-                        if (!slot_wait())
+                    for (int c = 0; c < S::VC; ++c, ++gv) {
+                        const uint32_t slot = gv % S::NVS, use = gv / S::NVS;
+                        if (use > 0 && !wait(bars.vempty[slot], (use - 1) & 1))
                             return false;
-                        const uint32_t slot = g % S::NS;
-                        const uint32_t bar = smem_addr(edge ? &bars.efull[slot] : &bars.full[slot]);
+                        const uint32_t bar = smem_addr(edge ? &bars.vedge[slot] : &bars.vfull[slot]);
                         onedge = edge ? onedge | (1u << slot) : onedge & ~(1u << slot);
                         par ^= edge ? 1u << slot : 0u;
-                        mbar_arrive_expect_tx(bar, S::VBYTES);
+                        mbar_arrive_expect_tx(bar, S::VSTAGE);
 #pragma unroll
                         for (int b = 0; b < S::DV / 64; ++b)
-                            tma_3d(ring + slot * S::STAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
+                            tma_3d(vring + slot * S::VSTAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
                                    row + c * S::VKEYS, bar);
                     }
                     return true;
@@ -754,119 +762,119 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             }
             if (!ok) {
                 // Copies in flight write this CTA's shared memory: let them land.
-                for (int i = 0; i < S::NS; ++i) {
-                    const uint32_t uses = (g + S::NS - 1 - i) / S::NS;
+                for (int i = 0; i < S::NK; ++i) {
+                    const uint32_t uses = (gk + S::NK - 1 - i) / S::NK;
+                    if (uses > 0)
+                        mbar_wait_bounded(smem_addr(&bars.kfull[i]), (uses - 1) & 1, 64);
+                }
+                for (int i = 0; i < S::NVS; ++i) {
+                    const uint32_t uses = (gv + S::NVS - 1 - i) / S::NVS;
                     if ((onedge >> i) & 1)
-                        mbar_wait_bounded(smem_addr(&bars.efull[i]), ((par >> i) & 1) ^ 1, 64);
+                        mbar_wait_bounded(smem_addr(&bars.vedge[i]), ((par >> i) & 1) ^ 1, 64);
                     else if (uses > 0)
-                        mbar_wait_bounded(smem_addr(&bars.full[i]), (uses - 1) & 1, 64);
+                        mbar_wait_bounded(smem_addr(&bars.vfull[i]), (uses - 1) & 1, 64);
                 }
                 if (piece > 0)
                     mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
             }
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issue
+        // ------------------------------------------- scores: S = Q K^T
         if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
-            uint32_t g = 0, piece = 0, it = 0; // stages, pieces, units so far
+            constexpr uint32_t id_s = idesc_bf16(kKeys, false);
+            uint32_t g = 0;          // key stages so far
+            uint32_t it[2] = {0, 0}; // units of each row tile
             bool ok = true;
-            // S_b = Q_t K^T from stages gk ..; `last` frees them.
-            auto scores = [&](int t, int b, uint32_t gk, bool first, bool last) {
-                for (int c = 0; c < S::KC; ++c) {
-                    const uint32_t gg = gk + c, slot = gg % S::NS;
-                    if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
-                        return false;
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
-                    const uint64_t bd = sdesc_kmajor(ring + slot * S::STAGE);
-#pragma unroll
-                    for (int k = 0; k < 4 * S::KB; ++k) {
-                        const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
-                        mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
-                    }
-                    if (last)
-                        mma_commit(smem_addr(&bars.empty[slot]));
-                }
-                mma_commit(smem_addr(&bars.s_full[b]));
-                return true;
-            };
-            auto product = [&](int t, int b, uint32_t gv, bool acc, bool first, bool last) {
-                for (int c = 0; c < S::VC; ++c) {
-                    const uint32_t gg = gv + c, slot = gg % S::NS;
-                    if (first && !wait(bars.full[slot], (gg / S::NS) & 1))
-                        return false;
-                    tc_fence_after();
-                    const uint64_t bd = sdesc_mnmajor(ring + slot * S::STAGE, S::VKEYS * 128);
-#pragma unroll
-                    for (int k = 0; k < S::VKEYS / 16; ++k)
-                        mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
-                               (acc || c > 0 || k > 0) ? 1u : 0u);
-                    if (last)
-                        mma_commit(smem_addr(&bars.empty[slot]));
-                }
-                mma_commit(smem_addr(&bars.o_done[t]));
-                return true;
-            };
-            uint32_t itq[2] = {0, 0}, pcq[2] = {0, 0}; // units and pieces of each row tile (TQ == 2)
-            for (; ok; ++piece) {
+            for (uint32_t piece = 0; ok; ++piece) {
                 if (!(ok = take(piece)))
                     break;
                 const int units = s_piece[piece % kPieces].units, nq = s_piece[piece % kPieces].nq;
                 done(piece);
                 if (units == 0 || !(ok = wait(bars.q_full, piece & 1)))
                     break;
-                if (S::TQ == 1) {
-                    ok = scores(0, it & 1, g, true, true);
-                    g += S::KC;
-                    for (int j = 0; ok && j < units; ++j, ++it) {
-                        if (j + 1 < units) {
-                            ok = scores(0, (it + 1) & 1, g, true, true);
-                            g += S::KC;
-                        }
-                        if (ok && (j + 2 == units || units == 1))
-                            mma_commit(smem_addr(&bars.q_empty));
-                        ok = ok && wait(bars.p_full[it & 1], (it >> 1) & 1) &&
-                             (j > 0 || piece == 0 || wait(bars.o_free[0], (piece - 1) & 1));
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        ok = product(0, it & 1, g, j > 0, true, true);
-                        g += S::VC;
-                    }
-                } else {
-                    for (int t = 0; ok && t < nq; ++t)
-                        ok = scores(t, t, g, t == 0, t == nq - 1);
-                    g += S::KC;
-                    if (units == 1)
-                        mma_commit(smem_addr(&bars.q_empty));
-                    for (int j = 0; ok && j < units; ++j) {
-                        for (int t = 0; ok && t < nq; ++t) {
-                            ok = wait(bars.p_full[t], itq[t] & 1) &&
-                                 (j > 0 || pcq[t] == 0 || wait(bars.o_free[t], (pcq[t] - 1) & 1));
-                            if (!ok)
+                for (int j = 0; ok && j < units; ++j, g += S::KC) {
+                    for (int t = 0; ok && t < nq; ++t) {
+                        // The buffer's weights have been used: the product of two units ago
+                        // (two buffers in turn), of the last unit (one buffer per row tile).
+                        const uint32_t i = it[t]++, b = S::TQ == 1 ? i & 1 : (uint32_t)t;
+                        const uint32_t use = S::TQ == 1 ? i >> 1 : i;
+                        ok = use == 0 || wait(bars.s_free[b], (use - 1) & 1);
+                        for (int c = 0; ok && c < S::KC; ++c) {
+                            const uint32_t slot = (g + c) % S::NK;
+                            if (t == 0 && !(ok = wait(bars.kfull[slot], ((g + c) / S::NK) & 1)))
                                 break;
-                            ++itq[t];
                             tc_fence_after();
-                            ok = product(t, t, g, j > 0, t == 0, t == nq - 1);
-                            if (ok && j + 1 < units)
-                                ok = scores(t, t, g + S::VC, t == 0, t == nq - 1);
+                            const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
+                            const uint64_t bd = sdesc_kmajor(kring + slot * S::KSTAGE);
+#pragma unroll
+                            for (int k = 0; k < 4 * S::KB; ++k) {
+                                const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
+                                mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                            }
+                            if (t == nq - 1)
+                                mma_commit(smem_addr(&bars.kempty[slot]));
                         }
-                        g += S::VC + (j + 1 < units ? S::KC : 0);
-                        if (j + 2 == units)
-                            mma_commit(smem_addr(&bars.q_empty));
+                        if (ok)
+                            mma_commit(smem_addr(&bars.s_full[b]));
                     }
-                    for (int t = 0; t < nq; ++t)
-                        ++pcq[t];
                 }
+                if (ok)
+                    mma_commit(smem_addr(&bars.q_empty));
             }
-            // Every MMA has finished before tensor memory is freed.
-            mma_commit(smem_addr(&bars.drain));
-            mbar_wait_bounded(smem_addr(&bars.drain), 0, 1024);
+            // Every product has finished before tensor memory is freed.
+            mma_commit(smem_addr(&bars.drain[0]));
+            mbar_wait_bounded(smem_addr(&bars.drain[0]), 0, 1024);
+        }
+    } else if (warp == S::PV_WARP) {
+        // ------------------------------------------- products: O += P V
+        if (elect_one()) {
+            constexpr uint32_t id_o = idesc_bf16(S::DV, true);
+            uint32_t g = 0;                              // value stages so far
+            uint32_t it[2] = {0, 0}, pieces[2] = {0, 0}; // units and pieces of each row tile
+            bool ok = true;
+            for (uint32_t piece = 0; ok; ++piece) {
+                if (!(ok = take(piece)))
+                    break;
+                const int units = s_piece[piece % kPieces].units, nq = s_piece[piece % kPieces].nq;
+                done(piece);
+                if (units == 0)
+                    break;
+                for (int j = 0; ok && j < units; ++j, g += S::VC) {
+                    for (int t = 0; ok && t < nq; ++t) {
+                        const uint32_t i = it[t]++, b = S::TQ == 1 ? i & 1 : (uint32_t)t;
+                        const uint32_t use = S::TQ == 1 ? i >> 1 : i;
+                        // The row tile's weights; at its first unit the last piece's
+                        // accumulator has been read.
+                        ok = wait(bars.p_full[b], use & 1) &&
+                             (j > 0 || pieces[t] == 0 || wait(bars.o_free[t], (pieces[t] - 1) & 1));
+                        for (int c = 0; ok && c < S::VC; ++c) {
+                            const uint32_t slot = (g + c) % S::NVS;
+                            if (t == 0 && !(ok = wait(bars.vfull[slot], ((g + c) / S::NVS) & 1)))
+                                break;
+                            tc_fence_after();
+                            const uint64_t bd = sdesc_mnmajor(vring + slot * S::VSTAGE, S::VKEYS * 128);
+#pragma unroll
+                            for (int k = 0; k < S::VKEYS / 16; ++k)
+                                mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k,
+                                       id_o, (j > 0 || c > 0 || k > 0) ? 1u : 0u);
+                            if (t == nq - 1)
+                                mma_commit(smem_addr(&bars.vempty[slot]));
+                        }
+                        if (ok) {
+                            mma_commit(smem_addr(&bars.o_done[t])); // before s_free: see the waits on it
+                            mma_commit(smem_addr(&bars.s_free[b]));
+                        }
+                    }
+                }
+                for (int t = 0; t < nq; ++t)
+                    ++pieces[t];
+            }
+            mma_commit(smem_addr(&bars.drain[1]));
+            mbar_wait_bounded(smem_addr(&bars.drain[1]), 0, 1024);
         }
     } else if (warp == 2) {
         // ------------------------------------- value rows of edge tiles
-        uint32_t base = 0, par = 0; // stages before the piece; phase of each slot's edge barrier
+        uint32_t base = 0, par = 0; // value stages before the piece; phase of each slot's edge barrier
         int piece = 0;
         bool ok = true;
         for (; ok; ++piece) {
@@ -884,20 +892,19 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 const int x = w.u + j;
                 if (!edge_unit<TREE>(a, w, x))
                     continue;
-                const uint32_t gv = base + (uint32_t)(j * (S::KC + S::VC) + S::KC) +
-                                    (S::TQ == 1 && j + 1 < units ? S::KC : 0);
+                const uint32_t gv = base + (uint32_t)(j * S::VC);
                 for (int c = 0; ok && c < S::VC; ++c) {
-                    const uint32_t slot = (gv + c) % S::NS;
+                    const uint32_t slot = (gv + c) % S::NVS;
                     // Classes of this stage's keys: key c * VKEYS + 32 h + lane in bits 2h, 2h + 1.
                     uint32_t cls = 0;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
                         cls |= (uint32_t)key_class<TREE>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
-                    ok = __all_sync(0xFFFFFFFFu, wait(bars.efull[slot], (par >> slot) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(bars.vedge[slot], (par >> slot) & 1));
                     if (!ok)
                         break;
                     par ^= 1u << slot;
-                    const uint32_t vb = ring + slot * S::STAGE;
+                    const uint32_t vb = vring + slot * S::VSTAGE;
                     bool found = false;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h) {
@@ -944,10 +951,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_addr(&bars.full[slot]));
+                        mbar_arrive(smem_addr(&bars.vfull[slot]));
                 }
             }
-            base += (uint32_t)(units * (S::KC + S::VC));
+            base += (uint32_t)(units * S::VC);
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ softmax
