@@ -22,16 +22,18 @@
 // tile that was cut leaves partial sums (accumulator, m, sum) in the scratch,
 // which a second kernel merges in key order (deterministic).
 //
-//   warp 0    tensor copies: the Q tile, then K and V stages through a ring each
-//   warp 1    issues S = Q K^T into tensor memory
-//   last warp issues O += P V with P read from tensor memory. Two issuing threads:
-//             waiting on a barrier (about 150 cycles even when it is complete) and
-//             issuing take one thread longer than the tensor core needs
-//   warp 2    repairs V stages of edge tiles in shared memory: the rows that no
-//             query row keeps become zeros (0 * NaN would poison the product)
-//   warp 3    announces the run's pieces of row tiles
-//   4 warps per MMA row tile  softmax: one thread per row, scores from tensor memory, P back
-//             over them; at the end of a row tile the same threads read O
+//   warp 0      tensor copies of Q and of K stages through a ring
+//   warp 13     tensor copies of V stages through a ring
+//   warps 1, 12 issue tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
+//               read from tensor memory. Two threads, because waiting on barriers
+//               (about 150 cycles even on a complete one) and issuing take one
+//               thread longer than the tensor core needs. D <= 128: each has one of
+//               two row tiles; above: one issues the scores, the other the products
+//   warp 2      repairs V stages of edge tiles in shared memory: the rows that no
+//               query row keeps become zeros (0 * NaN would poison the product)
+//   warp 3      announces the run's pieces of row tiles
+//   warps 4-11  softmax: scores from tensor memory, P back over them; at the end
+//               of a row tile the same threads read O
 //
 // Value rows that some rows of a tile keep and others do not (the diagonal, a
 // window's start, siblings in a tree) are searched for NaN and infinities as
@@ -50,14 +52,13 @@ namespace attn {
 constexpr int kKeys = 128;      // keys per tile
 constexpr int kRowsQ = 128;     // rows of one MMA tile
 constexpr int kBlock = 16384;   // 128 rows x 64 dims: a block of Q or K
-constexpr int kSmemBlocks = 14; // Q tiles and rings together, at most
 constexpr int kMaxSlots = 6;    // slots of a ring
 constexpr int kPieces = 4;      // pieces in flight between the warps
 // Cutting the work, a row tile counts as its units and this many more (copying
 // Q, the first scores without a product beside them, reading the accumulator)
 // when there are as many row tiles as CTAs: a run is then at least 1 + kTileCost
 // long and holds a unit. With fewer row tiles the units alone are cut.
-constexpr int kTileCost = 2;
+constexpr int kTileCost = 3;
 constexpr int kWaitLimit = 1 << 15;
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
@@ -68,25 +69,24 @@ struct Shape {
     static constexpr int DV = D / NV;                // width of a slice
     static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
     static constexpr int QB = D / 64;                // blocks of a row tile's Q
-    // Two rings, one for each issuing thread: a parity wait tells only
-    // neighbouring uses of a slot apart, so a thread must see every use of its
-    // slots. Stages of up to 32 KiB: waiting for a stage, issuing its products and
-    // freeing it costs a thread as much as the products take at 16 KiB.
-    static constexpr int KB = D == 64 ? 1 : 2;                  // blocks of a key stage
-    static constexpr int KSTAGE = KB * kBlock;
-    static constexpr int KC = QB / KB;                          // key stages per tile
-    static constexpr int VKEYS = DV <= 128 ? 128 : (D == 256 ? 64 : 32); // keys per value stage
-    static constexpr int VC = kKeys / VKEYS;                    // value stages per tile
+    // Two rings of 16 KiB stages: a parity wait tells only neighbouring uses of a
+    // slot apart, so every thread that waits sees every use of the slots. Each
+    // ring covers one copy's latency (about 1500 cycles) at D <= 256.
+    static constexpr int KC = QB;                                        // key stages per tile: 64 dims
+    static constexpr int VKEYS = DV == 64 ? 128 : (DV == 128 ? 64 : 32); // keys per value stage
+    static constexpr int VC = kKeys / VKEYS;                             // value stages per tile
     static constexpr int VSTAGE = VKEYS * DV * 2;
-    static constexpr int NK = D == 64 ? 6 : (D <= 256 ? 3 : 2); // ring slots
-    static constexpr int NVS = D == 64 ? 6 : (D == 384 ? 5 : 2);
+    static constexpr int NK = D == 64 ? 6 : (D == 512 ? 4 : 5);          // ring slots
+    static constexpr int NVS = D == 64 ? 6 : (D == 512 ? 2 : (D == 384 ? 4 : 5));
     static constexpr int ROWS = TQ * kRowsQ;
-    static constexpr int PV_WARP = 4 + 4 * TQ;       // the last warp
-    static constexpr int THREADS = 32 * (PV_WARP + 1);
+    static constexpr bool PAIR = TQ == 1;            // two threads per row, each with half of the keys
+    static constexpr int ROW_WARPS = PAIR ? 8 : 4;   // warps that serve one MMA row tile
+    static constexpr int THREADS = 448;
     static constexpr int QBYTES = TQ * QB * kBlock;
-    static constexpr size_t SMEM = (size_t)QBYTES + NK * KSTAGE + NVS * VSTAGE + 1024;
+    static constexpr size_t TILES = (size_t)QBYTES + NK * kBlock + NVS * VSTAGE;
+    static constexpr size_t SMEM = TILES + 3072;
     static_assert(VSTAGE % 1024 == 0 && NK <= kMaxSlots && NVS <= kMaxSlots, "rings");
-    static_assert(SMEM <= (size_t)kSmemBlocks * kBlock + 1024, "shared memory");
+    static_assert(SMEM <= 232448, "shared memory");
 };
 
 // Scratch of a call with `grid` CTAs (floats): accumulators, (m, sum) per row,
@@ -440,7 +440,7 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int t
 // keys that warp 2 took out of the product and that this row keeps.
 template <int D, bool TREE, typename Add>
 __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, const RowMask &m, int kvh,
-                                             int dv0, Add add)
+                                             int dv0, int d0, int d1, Add add)
 {
 #pragma unroll 1
     for (int x = w.u; x < w.u1; ++x) {
@@ -465,7 +465,7 @@ __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, cons
             if (!kept)
                 continue;
 #pragma unroll 1
-            for (int d = 0; d < Shape<D>::DV; ++d) {
+            for (int d = d0; d < d1; ++d) {
                 const uint32_t b = row[dv0 + d];
                 if ((b & 0x7F80u) == 0x7F80u)
                     add(d, __uint_as_float(b << 16));
@@ -483,6 +483,44 @@ struct Bars {
     unsigned long long s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], drain[2];
     unsigned long long pc_full[kPieces], pc_empty[kPieces];
 };
+
+// What lies behind the tiles in shared memory.
+struct Shared {
+    Bars bars;
+    Piece piece[kPieces];
+    float x[2][2][kRowsQ]; // the two threads of a row: maxima, sums ([unit parity][half][row])
+    int xok[2][8];         // and whether their waits ended well ([parity][softmax warp])
+    int cut[2][4], tiles;
+    int special[4];        // piece whose value rows had NaN or infinities
+    int warp_sums[16];
+    uint32_t tmem;
+    volatile int abort;
+};
+static_assert(sizeof(Shared) <= 3072, "shared memory");
+
+__device__ __forceinline__ unsigned long long pack64(float lo, float hi)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack64(unsigned long long v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // Lanes that differ in bit d of their number swap: the lower one's b for the
 // upper one's a.
@@ -531,50 +569,48 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
 attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using S = Shape<D>;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) Bars bars;
-    __shared__ uint32_t tmem_base;
-    __shared__ volatile int s_abort;
-    __shared__ int s_special[4];
-    __shared__ int s_cut[2][4], s_tiles;
-    __shared__ Piece s_piece[kPieces];
-    __shared__ int warp_sums[16];
-
-    unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t q_base = smem_addr(smem);
-    const uint32_t kring = q_base + S::QBYTES, vring = kring + S::NK * S::KSTAGE;
+    const uint32_t kring = q_base + S::QBYTES, vring = kring + S::NK * kBlock;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + S::TILES);
+    Bars &bars = sh.bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (q_base & 1023u) { // the swizzle's atoms are 1024 bytes; there is no static shared memory before them
+        if (threadIdx.x == 0)
+            atomicOr(a.err, 8);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(smem_addr(&bars.kfull[i]), 1);
-            mbar_init(smem_addr(&bars.kempty[i]), 1);
+            mbar_init(smem_addr(&bars.kempty[i]), S::TQ); // with two row tiles both issuing threads
             mbar_init(smem_addr(&bars.vfull[i]), 1);
             mbar_init(smem_addr(&bars.vedge[i]), 1); // a copied stage that warp 2 repairs before vfull
-            mbar_init(smem_addr(&bars.vempty[i]), 1);
+            mbar_init(smem_addr(&bars.vempty[i]), S::TQ);
         }
         mbar_init(smem_addr(&bars.q_full), 1);
-        mbar_init(smem_addr(&bars.q_empty), 1);
+        mbar_init(smem_addr(&bars.q_empty), S::TQ);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.s_full[i]), 1);
             mbar_init(smem_addr(&bars.s_free[i]), 1);
             mbar_init(smem_addr(&bars.drain[i]), 1);
-            mbar_init(smem_addr(&bars.p_full[i]), 4);
+            mbar_init(smem_addr(&bars.p_full[i]), S::ROW_WARPS);
             mbar_init(smem_addr(&bars.o_done[i]), 1);
-            mbar_init(smem_addr(&bars.o_free[i]), 4);
+            mbar_init(smem_addr(&bars.o_free[i]), S::ROW_WARPS);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&bars.pc_full[i]), 1);
-            mbar_init(smem_addr(&bars.pc_empty[i]), 4 + 4 * S::TQ);
+            mbar_init(smem_addr(&bars.pc_empty[i]), 5 + 8);
         }
-        s_abort = 0;
+        sh.abort = 0;
         for (int i = 0; i < 4; ++i)
-            s_special[i] = -1;
+            sh.special[i] = -1;
         fence_mbar_init();
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(&tmem_base)),
+                         smem_addr(&sh.tmem)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -583,7 +619,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     // -------------------------------------------------- this CTA's run
     // Row tiles in order of (head and slice, sequence, token), with their units
-    // and kTileCost each, cut at equal costs: s_cut[e] is where the run begins
+    // and kTileCost each, cut at equal costs: sh.cut[e] is where the run begins
     // (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within
     // the sequence, unit.
     {
@@ -594,7 +630,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             const int s = s0 + (int)threadIdx.x;
             const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
             int total;
-            const int incl = block_scan<S::THREADS>(nt, warp_sums, total);
+            const int incl = block_scan<S::THREADS>(nt, sh.warp_sums, total);
             if (s < a.B)
                 sbase[s] = R + incl - nt;
             R += total;
@@ -622,7 +658,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         for (int r0 = 0; r0 < R; r0 += S::THREADS) {
             const int r = r0 + (int)threadIdx.x;
             int total, s;
-            block_scan<S::THREADS>(r < R ? units_of(r, s) + extra : 0, warp_sums, total);
+            block_scan<S::THREADS>(r < R ? units_of(r, s) + extra : 0, sh.warp_sums, total);
             W += total;
         }
         const long long all = W * HS;
@@ -636,8 +672,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             at[e] = x - hs[e] * W;
         }
         if (threadIdx.x < 2) { // the end of the last run, until a tile claims the place
-            s_cut[threadIdx.x][0] = HS * R;
-            s_cut[threadIdx.x][3] = 0;
+            sh.cut[threadIdx.x][0] = HS * R;
+            sh.cut[threadIdx.x][3] = 0;
         }
         long long before = 0;
         for (int r0 = 0; r0 < R; r0 += S::THREADS) {
@@ -645,28 +681,28 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             int total, s = 0;
             const int n = r < R ? units_of(r, s) : 0;
             const int cost = n > 0 ? n + extra : 0;
-            const int incl = block_scan<S::THREADS>(cost, warp_sums, total);
+            const int incl = block_scan<S::THREADS>(cost, sh.warp_sums, total);
             const long long p = before + incl - cost;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (cost > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost) {
-                    s_cut[e][0] = hs[e] * R + r;
-                    s_cut[e][1] = s;
-                    s_cut[e][2] = r - sbase[s];
-                    s_cut[e][3] = (int)max(0ll, at[e] - p - extra);
+                    sh.cut[e][0] = hs[e] * R + r;
+                    sh.cut[e][1] = s;
+                    sh.cut[e][2] = r - sbase[s];
+                    sh.cut[e][3] = (int)max(0ll, at[e] - p - extra);
                 }
             before += total;
             if (max(at[0], at[1]) < before)
                 break;
         }
         if (threadIdx.x == 0)
-            s_tiles = R;
+            sh.tiles = R;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // sbase reads before the ring's copies
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     }
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = sh.tmem;
     // S (and P over it) in columns [128 b, 128 b + 128), O_t from 256 + t * DV.
     auto s_col = [&](int b) { return tmem + 128u * (uint32_t)b; };
     auto o_col = [&](int t) { return tmem + 256u + (uint32_t)(t * S::DV); };
@@ -676,70 +712,87 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         for (int i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(b, parity, 20000u))
                 return true;
-            if (s_abort)
+            if (sh.abort)
                 return false;
         }
-        s_abort = 1;
+        sh.abort = 1;
         atomicOr(a.err, 8);
         return false;
     };
 
-    // Piece p is in s_piece[p % kPieces] between these two.
+    // Piece p is in sh.piece[p % kPieces] between these two.
     auto take = [&](uint32_t p) { return wait(bars.pc_full[p % kPieces], (p / kPieces) & 1); };
     auto done = [&](uint32_t p) { mbar_arrive(smem_addr(&bars.pc_empty[p % kPieces])); };
 
     if (warp == 0) {
-        // ---------------------------------------------------- copies
+        // -------------------------------------------- copies of Q and K
         if (elect_one()) {
-            uint32_t gk = 0, gv = 0, piece = 0; // key and value stages, pieces so far
-            uint32_t par = 0, onedge = 0; // per value slot: uses of its edge barrier (parity), the last use was one
+            uint32_t g = 0, piece = 0; // key stages, pieces so far
             bool ok = true;
             for (; ok; ++piece) {
-                if (!take(piece)) {
-                    ok = false;
+                if (!(ok = take(piece)))
                     break;
-                }
-                const Piece w = s_piece[piece % kPieces];
+                const Piece w = sh.piece[piece % kPieces];
                 done(piece);
                 if (w.units == 0)
                     break;
-                const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
-                if (piece > 0 && !wait(bars.q_empty, (piece - 1) & 1)) {
-                    ok = false;
+                if (piece > 0 && !(ok = wait(bars.q_empty, (piece - 1) & 1)))
                     break; // the Q copies waited for below are the previous piece's
-                }
-                const int nq = w.nq, units = w.units;
-                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(nq * S::QB * a.tpt * a.G * 128));
-                for (int t = 0; t < nq; ++t)
+                const int kvh = w.hs / S::NV;
+                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(w.nq * S::QB * a.tpt * a.G * 128));
+                for (int t = 0; t < w.nq; ++t)
                     for (int c = 0; c < S::QB; ++c)
                         tma_3d(q_base + (t * S::QB + c) * kBlock, &maps.q, 64 * c, kvh * a.G,
                                w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
-                auto keys = [&](int j) {
+                for (int j = 0; ok && j < w.units; ++j) {
                     const int x = w.u + j;
                     const bool tr = tree_unit<TREE>(w, x);
                     const CUtensorMap *m = tr ? &maps.kt : &maps.k;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
-                    for (int c = 0; c < S::KC; ++c, ++gk) {
-                        const uint32_t slot = gk % S::NK, use = gk / S::NK;
-                        if (use > 0 && !wait(bars.kempty[slot], (use - 1) & 1))
-                            return false;
+                    for (int c = 0; c < S::KC; ++c, ++g) {
+                        const uint32_t slot = g % S::NK, use = g / S::NK;
+                        if (use > 0 && !(ok = wait(bars.kempty[slot], (use - 1) & 1)))
+                            break;
                         const uint32_t bar = smem_addr(&bars.kfull[slot]);
-                        mbar_arrive_expect_tx(bar, S::KSTAGE);
-#pragma unroll
-                        for (int b = 0; b < S::KB; ++b)
-                            tma_3d(kring + slot * S::KSTAGE + b * kBlock, m, 64 * (c * S::KB + b), kvh, row, bar);
+                        mbar_arrive_expect_tx(bar, kBlock);
+                        tma_3d(kring + slot * kBlock, m, 64 * c, kvh, row, bar);
                     }
-                    return true;
-                };
-                auto values = [&](int j) {
+                }
+            }
+            if (!ok) {
+                // Copies in flight write this CTA's shared memory: let them land.
+                for (int i = 0; i < S::NK; ++i) {
+                    const uint32_t uses = (g + S::NK - 1 - i) / S::NK;
+                    if (uses > 0)
+                        mbar_wait_bounded(smem_addr(&bars.kfull[i]), (uses - 1) & 1, 64);
+                }
+                if (piece > 0)
+                    mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
+            }
+        }
+    } else if (warp == 13) {
+        // -------------------------------------------------- copies of V
+        if (elect_one()) {
+            uint32_t g = 0;               // value stages so far
+            uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
+            bool ok = true;
+            for (uint32_t piece = 0; ok; ++piece) {
+                if (!(ok = take(piece)))
+                    break;
+                const Piece w = sh.piece[piece % kPieces];
+                done(piece);
+                if (w.units == 0)
+                    break;
+                const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
+                for (int j = 0; ok && j < w.units; ++j) {
                     const int x = w.u + j;
                     const bool tr = tree_unit<TREE>(w, x), edge = edge_unit<TREE>(a, w, x);
                     const CUtensorMap *m = tr ? &maps.vt : &maps.v;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
-                    for (int c = 0; c < S::VC; ++c, ++gv) {
-                        const uint32_t slot = gv % S::NVS, use = gv / S::NVS;
-                        if (use > 0 && !wait(bars.vempty[slot], (use - 1) & 1))
-                            return false;
+                    for (int c = 0; c < S::VC; ++c, ++g) {
+                        const uint32_t slot = g % S::NVS, use = g / S::NVS;
+                        if (use > 0 && !(ok = wait(bars.vempty[slot], (use - 1) & 1)))
+                            break;
                         const uint32_t bar = smem_addr(edge ? &bars.vedge[slot] : &bars.vfull[slot]);
                         onedge = edge ? onedge | (1u << slot) : onedge & ~(1u << slot);
                         par ^= edge ? 1u << slot : 0u;
@@ -749,128 +802,130 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             tma_3d(vring + slot * S::VSTAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
                                    row + c * S::VKEYS, bar);
                     }
-                    return true;
-                };
-                ok = keys(0);
-                for (int j = 0; ok && j < units; ++j) {
-                    if (S::TQ == 1) {
-                        ok = (j + 1 >= units || keys(j + 1)) && values(j);
-                    } else {
-                        ok = values(j) && (j + 1 >= units || keys(j + 1));
-                    }
                 }
             }
             if (!ok) {
-                // Copies in flight write this CTA's shared memory: let them land.
-                for (int i = 0; i < S::NK; ++i) {
-                    const uint32_t uses = (gk + S::NK - 1 - i) / S::NK;
-                    if (uses > 0)
-                        mbar_wait_bounded(smem_addr(&bars.kfull[i]), (uses - 1) & 1, 64);
-                }
                 for (int i = 0; i < S::NVS; ++i) {
-                    const uint32_t uses = (gv + S::NVS - 1 - i) / S::NVS;
+                    const uint32_t uses = (g + S::NVS - 1 - i) / S::NVS;
                     if ((onedge >> i) & 1)
                         mbar_wait_bounded(smem_addr(&bars.vedge[i]), ((par >> i) & 1) ^ 1, 64);
                     else if (uses > 0)
                         mbar_wait_bounded(smem_addr(&bars.vfull[i]), (uses - 1) & 1, 64);
                 }
-                if (piece > 0)
-                    mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
             }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------- scores: S = Q K^T
+    } else if (warp == 1 || warp == 12) {
+        // ---------------------------------------------- tensor-core issue
         if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(kKeys, false);
-            uint32_t g = 0;          // key stages so far
-            uint32_t it[2] = {0, 0}; // units of each row tile
+            constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
+            const int me = warp == 1 ? 0 : 1;
+            uint32_t gk = 0, gv = 0; // key and value stages so far
             bool ok = true;
-            for (uint32_t piece = 0; ok; ++piece) {
-                if (!(ok = take(piece)))
-                    break;
-                const int units = s_piece[piece % kPieces].units, nq = s_piece[piece % kPieces].nq;
-                done(piece);
-                if (units == 0 || !(ok = wait(bars.q_full, piece & 1)))
-                    break;
-                for (int j = 0; ok && j < units; ++j, g += S::KC) {
-                    for (int t = 0; ok && t < nq; ++t) {
-                        // The buffer's weights have been used: the product of two units ago
-                        // (two buffers in turn), of the last unit (one buffer per row tile).
-                        const uint32_t i = it[t]++, b = S::TQ == 1 ? i & 1 : (uint32_t)t;
-                        const uint32_t use = S::TQ == 1 ? i >> 1 : i;
-                        ok = use == 0 || wait(bars.s_free[b], (use - 1) & 1);
-                        for (int c = 0; ok && c < S::KC; ++c) {
-                            const uint32_t slot = (g + c) % S::NK;
-                            if (t == 0 && !(ok = wait(bars.kfull[slot], ((g + c) / S::NK) & 1)))
-                                break;
-                            tc_fence_after();
-                            const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
-                            const uint64_t bd = sdesc_kmajor(kring + slot * S::KSTAGE);
+            // Scores of row tile t into buffer b; frees the key stages.
+            auto scores = [&](int t, int b) {
+                for (int c = 0; c < S::KC; ++c, ++gk) {
+                    const uint32_t slot = gk % S::NK;
+                    if (!wait(bars.kfull[slot], (gk / S::NK) & 1))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c) * kBlock);
+                    const uint64_t bd = sdesc_kmajor(kring + slot * kBlock);
 #pragma unroll
-                            for (int k = 0; k < 4 * S::KB; ++k) {
-                                const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
-                                mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
-                            }
-                            if (t == nq - 1)
-                                mma_commit(smem_addr(&bars.kempty[slot]));
-                        }
-                        if (ok)
-                            mma_commit(smem_addr(&bars.s_full[b]));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(s_col(b), ad + 2u * k, bd + 2u * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(smem_addr(&bars.kempty[slot]));
                 }
-                if (ok)
-                    mma_commit(smem_addr(&bars.q_empty));
-            }
-            // Every product has finished before tensor memory is freed.
-            mma_commit(smem_addr(&bars.drain[0]));
-            mbar_wait_bounded(smem_addr(&bars.drain[0]), 0, 1024);
-        }
-    } else if (warp == S::PV_WARP) {
-        // ------------------------------------------- products: O += P V
-        if (elect_one()) {
-            constexpr uint32_t id_o = idesc_bf16(S::DV, true);
-            uint32_t g = 0;                              // value stages so far
-            uint32_t it[2] = {0, 0}, pieces[2] = {0, 0}; // units and pieces of each row tile
-            bool ok = true;
+                mma_commit(smem_addr(&bars.s_full[b]));
+                return true;
+            };
+            // O_t (+)= P V with the weights in buffer b; frees the value stages.
+            auto product = [&](int t, int b, bool acc) {
+                for (int c = 0; c < S::VC; ++c, ++gv) {
+                    const uint32_t slot = gv % S::NVS;
+                    if (!wait(bars.vfull[slot], (gv / S::NVS) & 1))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t bd = sdesc_mnmajor(vring + slot * S::VSTAGE, S::VKEYS * 128);
+#pragma unroll
+                    for (int k = 0; k < S::VKEYS / 16; ++k)
+                        mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
+                               (acc || c > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(smem_addr(&bars.vempty[slot]));
+                }
+                mma_commit(smem_addr(&bars.o_done[t]));
+                return true;
+            };
+            uint32_t it = 0, mine = 0; // units, pieces of this thread's row tile
             for (uint32_t piece = 0; ok; ++piece) {
                 if (!(ok = take(piece)))
                     break;
-                const int units = s_piece[piece % kPieces].units, nq = s_piece[piece % kPieces].nq;
+                const int units = sh.piece[piece % kPieces].units, nq = sh.piece[piece % kPieces].nq;
                 done(piece);
                 if (units == 0)
                     break;
-                for (int j = 0; ok && j < units; ++j, g += S::VC) {
-                    for (int t = 0; ok && t < nq; ++t) {
-                        const uint32_t i = it[t]++, b = S::TQ == 1 ? i & 1 : (uint32_t)t;
-                        const uint32_t use = S::TQ == 1 ? i >> 1 : i;
-                        // The row tile's weights; at its first unit the last piece's
-                        // accumulator has been read.
-                        ok = wait(bars.p_full[b], use & 1) &&
-                             (j > 0 || pieces[t] == 0 || wait(bars.o_free[t], (pieces[t] - 1) & 1));
-                        for (int c = 0; ok && c < S::VC; ++c) {
-                            const uint32_t slot = (g + c) % S::NVS;
-                            if (t == 0 && !(ok = wait(bars.vfull[slot], ((g + c) / S::NVS) & 1)))
+                if (S::TQ == 2) {
+                    // Thread t issues for row tile t. Its scores go over the weights that
+                    // its product before them has read: one thread's tensor-core
+                    // instructions execute in the order of their issue.
+                    if (!(ok = wait(bars.q_full, piece & 1)))
+                        break;
+                    if (me < nq) {
+                        ok = scores(me, me);
+                        for (int j = 0; ok && j < units; ++j, ++it) {
+                            if (j + 1 == units)
+                                mma_commit(smem_addr(&bars.q_empty));
+                            ok = wait(bars.p_full[me], it & 1) &&
+                                 (j > 0 || mine == 0 || wait(bars.o_free[me], (mine - 1) & 1));
+                            if (!ok)
                                 break;
                             tc_fence_after();
-                            const uint64_t bd = sdesc_mnmajor(vring + slot * S::VSTAGE, S::VKEYS * 128);
-#pragma unroll
-                            for (int k = 0; k < S::VKEYS / 16; ++k)
-                                mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k,
-                                       id_o, (j > 0 || c > 0 || k > 0) ? 1u : 0u);
-                            if (t == nq - 1)
-                                mma_commit(smem_addr(&bars.vempty[slot]));
+                            ok = product(me, me, j > 0) && (j + 1 >= units || scores(me, me));
                         }
-                        if (ok) {
-                            mma_commit(smem_addr(&bars.o_done[t])); // before s_free: see the waits on it
-                            mma_commit(smem_addr(&bars.s_free[b]));
+                        ++mine;
+                    } else {
+                        // No such row tile in this piece: see its stages and free them.
+                        mbar_arrive(smem_addr(&bars.q_empty));
+                        for (int n = units * S::KC; ok && n > 0; --n, ++gk) {
+                            if (n <= (units - 1) * S::KC && n % S::KC == 0)
+                                for (int c = 0; ok && c < S::VC; ++c, ++gv) {
+                                    ok = wait(bars.vfull[gv % S::NVS], (gv / S::NVS) & 1);
+                                    mbar_arrive(smem_addr(&bars.vempty[gv % S::NVS]));
+                                }
+                            ok = ok && wait(bars.kfull[gk % S::NK], (gk / S::NK) & 1);
+                            mbar_arrive(smem_addr(&bars.kempty[gk % S::NK]));
+                        }
+                        for (int c = 0; ok && c < S::VC; ++c, ++gv) {
+                            ok = wait(bars.vfull[gv % S::NVS], (gv / S::NVS) & 1);
+                            mbar_arrive(smem_addr(&bars.vempty[gv % S::NVS]));
                         }
                     }
+                } else if (me == 0) {
+                    // Scores of the units in turn into two buffers, once a buffer's
+                    // weights (of two units ago) have been used.
+                    if (!(ok = wait(bars.q_full, piece & 1)))
+                        break;
+                    for (int j = 0; ok && j < units; ++j, ++it)
+                        ok = (it < 2 || wait(bars.s_free[it & 1], ((it >> 1) - 1) & 1)) && scores(0, it & 1);
+                    if (ok)
+                        mma_commit(smem_addr(&bars.q_empty));
+                } else {
+                    // Products, once the weights are there and, at a piece's first, the
+                    // last piece's accumulator has been read.
+                    for (int j = 0; ok && j < units; ++j, ++it) {
+                        ok = wait(bars.p_full[it & 1], (it >> 1) & 1) &&
+                             (j > 0 || mine == 0 || wait(bars.o_free[0], (mine - 1) & 1));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if ((ok = product(0, it & 1, j > 0)))
+                            mma_commit(smem_addr(&bars.s_free[it & 1])); // after o_done: see the waits on it
+                    }
+                    ++mine;
                 }
-                for (int t = 0; t < nq; ++t)
-                    ++pieces[t];
             }
-            mma_commit(smem_addr(&bars.drain[1]));
-            mbar_wait_bounded(smem_addr(&bars.drain[1]), 0, 1024);
+            // Every product has finished before tensor memory is freed.
+            mma_commit(smem_addr(&bars.drain[me]));
+            mbar_wait_bounded(smem_addr(&bars.drain[me]), 0, 1024);
         }
     } else if (warp == 2) {
         // ------------------------------------- value rows of edge tiles
@@ -881,7 +936,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             ok = __all_sync(0xFFFFFFFFu, take(piece));
             if (!ok)
                 break;
-            const Piece w = s_piece[piece % kPieces];
+            const Piece w = sh.piece[piece % kPieces];
             __syncwarp();
             if (lane == 0)
                 done(piece);
@@ -947,7 +1002,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         }
                     }
                     if (found)
-                        s_special[piece & 3] = piece;
+                        sh.special[piece & 3] = piece;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0)
@@ -958,18 +1013,36 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ softmax
-        const int t = (warp - 4) >> 2;  // MMA row tile
+        // Two row tiles: a thread has a row. One row tile: two threads (warps w and
+        // w + 4) have a row, 64 keys and half of the accumulator's columns each.
+        const int t = S::PAIR ? 0 : (warp - 4) >> 2; // MMA row tile
+        const int half = S::PAIR ? (warp - 4) >> 2 : 0;
         const int wq = warp & 3;        // tensor-memory lanes 32 wq ..
         const int row = 32 * wq + lane; // row of the MMA tile
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const int tok_in = row / a.G, head = row - tok_in * a.G;
+        constexpr int OC = S::PAIR ? S::DV / 2 : S::DV; // accumulator columns of this thread
         uint32_t it = 0, piece = 0; // units of this row tile; pieces of the run
+        uint32_t xs = 0;            // exchanges so far
         bool ok = true;
-        for (; ok; ++piece) {
+        // The row's two threads exchange a value, and whether their waits ended well:
+        // both leave at the same exchange, so neither is left at the barrier.
+        auto exchange = [&](float mine) -> float {
+            const int par = xs++ & 1;
+            sh.x[par][half][row] = mine;
+            if (lane == 0)
+                sh.xok[par][warp - 4] = ok;
+            named_sync(1 + wq, 64);
+            ok = ok && sh.xok[par][(warp - 4) ^ 4];
+            return sh.x[par][half ^ 1][row];
+        };
+        for (;; ++piece) {
             ok = __all_sync(0xFFFFFFFFu, take(piece));
+            if (S::PAIR)
+                exchange(0.f);
             if (!ok)
                 break;
-            const Piece &w = s_piece[piece % kPieces];
+            const Piece &w = sh.piece[piece % kPieces];
             const int units = w.units;
             if (units == 0)
                 break;
@@ -982,11 +1055,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             const int tok = t * a.tpt + tok_in;
             const RowMask rm = row_mask<TREE>(a, w, tok, tok_in < a.tpt && tok < w.nt);
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; ok && j < units; ++j, ++it) {
+            for (int j = 0; j < units; ++j, ++it) {
                 const int x = w.u + j, kb = key0(w, x);
                 const bool tr = tree_unit<TREE>(w, x);
-                const uint32_t b = S::TQ == 1 ? (it & 1) : (uint32_t)t;
-                const uint32_t ph = S::TQ == 1 ? (it >> 1) & 1 : it & 1;
+                const uint32_t b = S::PAIR ? (it & 1) : (uint32_t)t;
+                const uint32_t ph = S::PAIR ? (it >> 1) & 1 : it & 1;
                 // Kept keys of this row, one bit each; `all`: the warp keeps every key.
                 uint32_t km[4];
                 bool all = false;
@@ -1022,20 +1095,17 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     for (int h = 0; h < 4; ++h)
                         km[h] = below(hi - 32 * h) & ~below(lo - 32 * h);
                 }
-                ok = __all_sync(0xFFFFFFFFu, wait(bars.s_full[b], ph));
-                if (!ok)
+                ok = ok && __all_sync(0xFFFFFFFFu, wait(bars.s_full[b], ph));
+                if (!S::PAIR && !ok)
                     break;
                 tc_fence_after();
-                // The row's 128 scores in two halves of 64 registers: the upper half is
-                // read for the maximum, the lower half for the maximum and its weights,
-                // then the upper half again (P goes over columns that were read).
                 const uint32_t sa = s_col(b) + lanes;
                 uint32_t v[64];
-                auto mask = [&](int h0) {
+                auto mask = [&](uint32_t k0, uint32_t k1) {
                     if (!all) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
-                            if (!((km[h0 + (i >> 5)] >> (i & 31)) & 1u))
+                            if (!(((i < 32 ? k0 : k1) >> (i & 31)) & 1u))
                                 v[i] = 0xFF800000u;
                     }
                 };
@@ -1051,12 +1121,26 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[i + q]), __uint_as_float(v[i + q + 4])));
                     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
-                W4_TLD64(v, sa + 64u);
-                mask(2);
-                float mt = most();
-                W4_TLD64(v, sa);
-                mask(0);
-                mt = fmaxf(mt, most()) * a.c;
+                float mt;
+                if (S::PAIR) {
+                    W4_TLD64(v, sa + 64u * half);
+                    mask(half ? km[2] : km[0], half ? km[3] : km[1]);
+                    mt = most();
+                    // Also: both halves have read their scores, P may go over them.
+                    mt = fmaxf(mt, exchange(mt)) * a.c;
+                    if (!ok)
+                        break;
+                } else {
+                    // 64 registers at a time: the upper half is read for the maximum, the
+                    // lower half for the maximum and its weights, then the upper half again
+                    // (P goes over columns that were read).
+                    W4_TLD64(v, sa + 64u);
+                    mask(km[2], km[3]);
+                    mt = most();
+                    W4_TLD64(v, sa);
+                    mask(km[0], km[1]);
+                    mt = fmaxf(mt, most()) * a.c;
+                }
                 float alpha = 1.f;
                 if (rm.live && mt > m + 8.f) { // also the first kept key (m = -inf)
                     alpha = ex2(m - mt);
@@ -1066,11 +1150,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
                     // O holds the units before this one: wait for their product.
                     ok = __all_sync(0xFFFFFFFFu, wait(bars.o_done[t], (it - 1) & 1));
-                    if (!ok)
+                    if (!S::PAIR && !ok)
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                    for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                         uint32_t o[32];
                         W4_TLD32(o, o_col(t) + lanes + c0);
 #pragma unroll
@@ -1080,43 +1164,55 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const unsigned long long cc = pack64(a.c, a.c), nm = pack64(-mm, -mm);
+                unsigned long long sum[2] = {0ull, 0ull};
                 auto weights = [&](uint32_t to) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float p0 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i]), a.c, -mm));
-                            const float p1 = ex2(fmaf(__uint_as_float(v[32 * c + 2 * i + 1]), a.c, -mm));
-                            sum[i & 3] += p0 + p1;
+                            float p0, p1;
+                            unpack64(fma2(pack64(__uint_as_float(v[32 * c + 2 * i]),
+                                                 __uint_as_float(v[32 * c + 2 * i + 1])),
+                                          cc, nm),
+                                     p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[i & 1] = add2(sum[i & 1], pack64(p0, p1));
                             pk[i] = pack2(p0, p1);
                         }
                         W4_TST16(pk, 0, to + 16u * c);
                     }
                 };
-                weights(sa);
-                W4_TLD64(v, sa + 64u);
-                mask(2);
-                weights(sa + 32u);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                weights(sa + 32u * half);
+                if (!S::PAIR) {
+                    W4_TLD64(v, sa + 64u);
+                    mask(km[2], km[3]);
+                    weights(sa + 32u);
+                }
+                float s0, s1;
+                unpack64(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&bars.p_full[b]));
             }
-            if (!ok)
+            if (!S::PAIR && !ok)
                 break;
             // ------------------------------------------------- epilogue
             // With two score buffers the last scores say nothing of the product before
             // last, and a parity wait tells only neighbouring phases apart.
-            ok = __all_sync(0xFFFFFFFFu, (S::TQ == 2 || units < 2 || wait(bars.o_done[t], it & 1)) &&
-                                             wait(bars.o_done[t], (it - 1) & 1));
+            ok = ok && __all_sync(0xFFFFFFFFu, (!S::PAIR || units < 2 || wait(bars.o_done[t], it & 1)) &&
+                                                   wait(bars.o_done[t], (it - 1) & 1));
+            if (S::PAIR)
+                l += exchange(l);
             if (!ok)
                 break;
             tc_fence_after();
-            const bool whole = w.whole(), special = s_special[piece & 3] == (int)piece;
+            const bool whole = w.whole(), special = sh.special[piece & 3] == (int)piece;
             const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
             uint16_t *orow = a.out + (size_t)((long long)w.q0 + w.t0 + tok) * a.ldo +
                              (size_t)(kvh * a.G + head) * D + dv0;
@@ -1137,7 +1233,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     live[i] = __shfl_sync(0xFFFFFFFFu, (int)rm.live, src) != 0;
                 }
 #pragma unroll 1
-                for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                     uint32_t o[32];
                     W4_TLD32(o, o_col(t) + lanes + c0);
                     uint4 y[4];
@@ -1161,7 +1257,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 }
             } else {
 #pragma unroll 1
-                for (int c0 = 0; c0 < S::DV; c0 += 32) {
+                for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                     uint32_t o[32];
                     W4_TLD32(o, o_col(t) + lanes + c0);
                     if (rm.live) {
@@ -1178,7 +1274,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&bars.o_free[t]));
-            if (!whole && rm.live) {
+            if (!whole && rm.live && half == 0) {
                 float *ml = a.ws_ml + ((size_t)slot * 256 + t * kRowsQ + row) * 2;
                 ml[0] = m;
                 ml[1] = l;
@@ -1186,7 +1282,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             if (special)
                 __syncwarp(); // a row's output may come from its neighbour lanes
             if (special && rm.live)
-                add_specials<D, TREE>(a, w, rm, kvh, dv0, [&](int d, float f) {
+                add_specials<D, TREE>(a, w, rm, kvh, dv0, half * OC, half * OC + OC, [&](int d, float f) {
                     if (whole) {
                         const float o = __uint_as_float((uint32_t)orow[d] << 16) + f;
                         orow[d] = (uint16_t)(pack2(o, 0.f) & 0xFFFFu);
@@ -1202,8 +1298,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         // ------------- warp 3: the run's pieces, and what the merge needs to know
         const int tt = a.tpt * S::TQ;
         int cont = 0, begins = 0;
-        int tile = s_cut[0][0], s = s_cut[0][1], i = s_cut[0][2], u = s_cut[0][3];
-        const int end = s_cut[1][0], end_u = s_cut[1][3];
+        int tile = sh.cut[0][0], s = sh.cut[0][1], i = sh.cut[0][2], u = sh.cut[0][3];
+        const int end = sh.cut[1][0], end_u = sh.cut[1][3];
         uint32_t piece = 0;
         bool ok = true;
         Seq q = {};
@@ -1211,7 +1307,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             q = load_seq<TREE>(a, s);
         while (ok && (tile < end || (tile == end && u < end_u))) {
             Piece w;
-            w.hs = tile / s_tiles;
+            w.hs = tile / sh.tiles;
             w.s = s;
             w.t0 = i * tt;
             w.nt = min(tt, q.lq - w.t0);
@@ -1229,7 +1325,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 ok = wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1);
             if (!ok)
                 break;
-            s_piece[piece % kPieces] = w;
+            sh.piece[piece % kPieces] = w;
             mbar_arrive(smem_addr(&bars.pc_full[piece % kPieces]));
             ++piece;
             if (w.u > 0) {
@@ -1254,7 +1350,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         }
         if (ok && (piece < (uint32_t)kPieces ||
                    wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1))) {
-            s_piece[piece % kPieces].units = 0;
+            sh.piece[piece % kPieces].units = 0;
             mbar_arrive(smem_addr(&bars.pc_full[piece % kPieces]));
         }
         a.rec[2 * blockIdx.x] = cont;
