@@ -22,13 +22,9 @@
 // tile that was cut leaves partial sums (accumulator, m, sum) in the scratch,
 // which a second kernel merges in key order (deterministic).
 //
-//   warp 0      tensor copies of Q and of K stages through a ring
-//   warp 13     tensor copies of V stages through a ring
-//   warps 1, 12 issue tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
-//               read from tensor memory. Two threads, because waiting on barriers
-//               (about 150 cycles even on a complete one) and issuing take one
-//               thread longer than the tensor core needs. D <= 128: each has one of
-//               two row tiles; above: one issues the scores, the other the products
+//   warp 0      tensor copies of Q, then of K and V stages through a ring
+//   warp 1      issues tcgen05.mma: S = Q K^T into tensor memory, O += P V with P
+//               read from tensor memory
 //   warp 2      repairs V stages of edge tiles in shared memory: the rows that no
 //               query row keeps become zeros (0 * NaN would poison the product)
 //   warp 3      announces the run's pieces of row tiles
@@ -45,6 +41,7 @@
 #include "internal.h"
 
 #include <cuda.h>
+#include <type_traits>
 
 namespace w4 {
 namespace attn {
@@ -52,13 +49,9 @@ namespace attn {
 constexpr int kKeys = 128;      // keys per tile
 constexpr int kRowsQ = 128;     // rows of one MMA tile
 constexpr int kBlock = 16384;   // 128 rows x 64 dims: a block of Q or K
-constexpr int kMaxSlots = 6;    // slots of a ring
+constexpr int kSmemBlocks = 14; // Q tiles and ring together
+constexpr int kMaxSlots = 12;   // ring slots
 constexpr int kPieces = 4;      // pieces in flight between the warps
-// Cutting the work, a row tile counts as its units and this many more (copying
-// Q, the first scores without a product beside them, reading the accumulator)
-// when there are as many row tiles as CTAs: a run is then at least 1 + kTileCost
-// long and holds a unit. With fewer row tiles the units alone are cut.
-constexpr int kTileCost = 3;
 constexpr int kWaitLimit = 1 << 15;
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
@@ -69,23 +62,31 @@ struct Shape {
     static constexpr int DV = D / NV;                // width of a slice
     static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
     static constexpr int QB = D / 64;                // blocks of a row tile's Q
-    // Two rings of 16 KiB stages: a parity wait tells only neighbouring uses of a
-    // slot apart, so every thread that waits sees every use of the slots. Each
-    // ring covers one copy's latency (about 1500 cycles) at D <= 256.
-    static constexpr int KC = QB;                                        // key stages per tile: 64 dims
-    static constexpr int VKEYS = DV == 64 ? 128 : (DV == 128 ? 64 : 32); // keys per value stage
-    static constexpr int VC = kKeys / VKEYS;                             // value stages per tile
-    static constexpr int VSTAGE = VKEYS * DV * 2;
-    static constexpr int NK = D == 64 ? 6 : (D == 512 ? 4 : 5);          // ring slots
-    static constexpr int NVS = D == 64 ? 6 : (D == 512 ? 2 : (D == 384 ? 4 : 5));
+    // One ring of stages in the order of use. 32 KiB where the ring then still
+    // covers a copy's latency (about 1500 cycles): waiting for a stage and freeing
+    // it leave the tensor core about 60 cycles without work.
+    static constexpr int STAGE = D == 64 || D == 512 ? kBlock : 2 * kBlock;
+    static constexpr int KB = STAGE / kBlock;             // blocks of a key stage
+    static constexpr int KC = QB / KB;                    // key stages per tile
+    static constexpr int VKEYS = DV <= 128 ? 128 : (D == 512 ? 32 : 64); // keys per value stage
+    static constexpr int VC = kKeys / VKEYS;              // value stages per tile
+    static constexpr int VBYTES = VKEYS * DV * 2;
+    static constexpr int NS = (kSmemBlocks - TQ * QB) * kBlock / STAGE;  // ring slots
     static constexpr int ROWS = TQ * kRowsQ;
     static constexpr bool PAIR = TQ == 1;            // two threads per row, each with half of the keys
     static constexpr int ROW_WARPS = PAIR ? 8 : 4;   // warps that serve one MMA row tile
-    static constexpr int THREADS = 448;
+    static constexpr int THREADS = 12 * 32;
+    // Cutting the work, a row tile counts as its units and this many more (copying
+    // Q, the first scores without a product beside them, reading the accumulator)
+    // when there are as many row tiles as CTAs: a run is then at least
+    // 1 + TILE_COST long and holds a unit. With fewer the units alone are cut.
+    // Measured (8192 tokens, 8 heads): runs of many short row tiles took a third
+    // longer than the others with 3 at D = 256, as long with 4.
+    static constexpr int TILE_COST = D == 256 ? 4 : (D > 256 ? 3 : 2);
     static constexpr int QBYTES = TQ * QB * kBlock;
-    static constexpr size_t TILES = (size_t)QBYTES + NK * kBlock + NVS * VSTAGE;
+    static constexpr size_t TILES = (size_t)QBYTES + NS * STAGE;
     static constexpr size_t SMEM = TILES + 3072;
-    static_assert(VSTAGE % 1024 == 0 && NK <= kMaxSlots && NVS <= kMaxSlots, "rings");
+    static_assert(VBYTES <= STAGE && VBYTES % 1024 == 0 && NS <= kMaxSlots, "ring");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -477,10 +478,9 @@ __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, cons
 // ------------------------------------------------------------- kernel ----
 
 struct Bars {
-    unsigned long long kfull[kMaxSlots], kempty[kMaxSlots];
-    unsigned long long vfull[kMaxSlots], vedge[kMaxSlots], vempty[kMaxSlots];
+    unsigned long long full[kMaxSlots], edge[kMaxSlots], empty[kMaxSlots];
     unsigned long long q_full, q_empty;
-    unsigned long long s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], drain[2];
+    unsigned long long s_full[2], p_full[2], o_done[2], o_free[2], drain;
     unsigned long long pc_full[kPieces], pc_empty[kPieces];
 };
 
@@ -571,7 +571,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     using S = Shape<D>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t q_base = smem_addr(smem);
-    const uint32_t kring = q_base + S::QBYTES, vring = kring + S::NK * kBlock;
+    const uint32_t ring = q_base + S::QBYTES;
     Shared &sh = *reinterpret_cast<Shared *>(smem + S::TILES);
     Bars &bars = sh.bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -583,25 +583,22 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
-            mbar_init(smem_addr(&bars.kfull[i]), 1);
-            mbar_init(smem_addr(&bars.kempty[i]), S::TQ); // with two row tiles both issuing threads
-            mbar_init(smem_addr(&bars.vfull[i]), 1);
-            mbar_init(smem_addr(&bars.vedge[i]), 1); // a copied stage that warp 2 repairs before vfull
-            mbar_init(smem_addr(&bars.vempty[i]), S::TQ);
+            mbar_init(smem_addr(&bars.full[i]), 1);
+            mbar_init(smem_addr(&bars.edge[i]), 1); // a copied stage that warp 2 repairs before `full`
+            mbar_init(smem_addr(&bars.empty[i]), 1);
         }
         mbar_init(smem_addr(&bars.q_full), 1);
-        mbar_init(smem_addr(&bars.q_empty), S::TQ);
+        mbar_init(smem_addr(&bars.q_empty), 1);
+        mbar_init(smem_addr(&bars.drain), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.s_full[i]), 1);
-            mbar_init(smem_addr(&bars.s_free[i]), 1);
-            mbar_init(smem_addr(&bars.drain[i]), 1);
             mbar_init(smem_addr(&bars.p_full[i]), S::ROW_WARPS);
             mbar_init(smem_addr(&bars.o_done[i]), 1);
             mbar_init(smem_addr(&bars.o_free[i]), S::ROW_WARPS);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&bars.pc_full[i]), 1);
-            mbar_init(smem_addr(&bars.pc_empty[i]), 5 + 8);
+            mbar_init(smem_addr(&bars.pc_empty[i]), 3 + 8);
         }
         sh.abort = 0;
         for (int i = 0; i < 4; ++i)
@@ -619,7 +616,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     // -------------------------------------------------- this CTA's run
     // Row tiles in order of (head and slice, sequence, token), with their units
-    // and kTileCost each, cut at equal costs: sh.cut[e] is where the run begins
+    // and TILE_COST each, cut at equal costs: sh.cut[e] is where the run begins
     // (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within
     // the sequence, unit.
     {
@@ -636,7 +633,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             R += total;
         }
         __syncthreads();
-        const int extra = (long long)R * HS >= (long long)gridDim.x ? kTileCost : 0;
+        const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
         auto units_of = [&](int r, int &s) {
             // The last sequence that begins at or before r (empty ones begin where the next does).
             int x = 0, y = a.B - 1;
@@ -702,7 +699,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         __syncthreads();
         tc_fence_after();
     }
-    const uint32_t tmem = sh.tmem;
+    // All 512 columns: they begin at 0, which keeps the addresses constants.
+    constexpr uint32_t tmem = 0;
     // S (and P over it) in columns [128 b, 128 b + 128), O_t from 256 + t * DV.
     auto s_col = [&](int b) { return tmem + 128u * (uint32_t)b; };
     auto o_col = [&](int t) { return tmem + 256u + (uint32_t)(t * S::DV); };
@@ -725,9 +723,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     auto done = [&](uint32_t p) { mbar_arrive(smem_addr(&bars.pc_empty[p % kPieces])); };
 
     if (warp == 0) {
-        // -------------------------------------------- copies of Q and K
+        // ---------------------------------------------------- copies
         if (elect_one()) {
-            uint32_t g = 0, piece = 0; // key stages, pieces so far
+            uint32_t g = 0, piece = 0;    // stages, pieces so far
+            uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
             bool ok = true;
             for (; ok; ++piece) {
                 if (!(ok = take(piece)))
@@ -738,198 +737,190 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     break;
                 if (piece > 0 && !(ok = wait(bars.q_empty, (piece - 1) & 1)))
                     break; // the Q copies waited for below are the previous piece's
-                const int kvh = w.hs / S::NV;
+                const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
                 mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(w.nq * S::QB * a.tpt * a.G * 128));
                 for (int t = 0; t < w.nq; ++t)
                     for (int c = 0; c < S::QB; ++c)
                         tma_3d(q_base + (t * S::QB + c) * kBlock, &maps.q, 64 * c, kvh * a.G,
                                w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
-                for (int j = 0; ok && j < w.units; ++j) {
+                auto keys = [&](int j) {
                     const int x = w.u + j;
                     const bool tr = tree_unit<TREE>(w, x);
                     const CUtensorMap *m = tr ? &maps.kt : &maps.k;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::KC; ++c, ++g) {
-                        const uint32_t slot = g % S::NK, use = g / S::NK;
-                        if (use > 0 && !(ok = wait(bars.kempty[slot], (use - 1) & 1)))
-                            break;
-                        const uint32_t bar = smem_addr(&bars.kfull[slot]);
-                        mbar_arrive_expect_tx(bar, kBlock);
-                        tma_3d(kring + slot * kBlock, m, 64 * c, kvh, row, bar);
+                        const uint32_t slot = g % S::NS, use = g / S::NS;
+                        if (use > 0 && !wait(bars.empty[slot], (use - 1) & 1))
+                            return false;
+                        const uint32_t bar = smem_addr(&bars.full[slot]);
+                        onedge &= ~(1u << slot);
+                        mbar_arrive_expect_tx(bar, S::STAGE);
+#pragma unroll
+                        for (int b = 0; b < S::KB; ++b)
+                            tma_3d(ring + slot * S::STAGE + b * kBlock, m, 64 * (c * S::KB + b), kvh, row, bar);
                     }
-                }
-            }
-            if (!ok) {
-                // Copies in flight write this CTA's shared memory: let them land.
-                for (int i = 0; i < S::NK; ++i) {
-                    const uint32_t uses = (g + S::NK - 1 - i) / S::NK;
-                    if (uses > 0)
-                        mbar_wait_bounded(smem_addr(&bars.kfull[i]), (uses - 1) & 1, 64);
-                }
-                if (piece > 0)
-                    mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
-            }
-        }
-    } else if (warp == 13) {
-        // -------------------------------------------------- copies of V
-        if (elect_one()) {
-            uint32_t g = 0;               // value stages so far
-            uint32_t par = 0, onedge = 0; // per slot: uses of its edge barrier (parity), the last use was one
-            bool ok = true;
-            for (uint32_t piece = 0; ok; ++piece) {
-                if (!(ok = take(piece)))
-                    break;
-                const Piece w = sh.piece[piece % kPieces];
-                done(piece);
-                if (w.units == 0)
-                    break;
-                const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
-                for (int j = 0; ok && j < w.units; ++j) {
+                    return true;
+                };
+                auto values = [&](int j) {
                     const int x = w.u + j;
                     const bool tr = tree_unit<TREE>(w, x), edge = edge_unit<TREE>(a, w, x);
                     const CUtensorMap *m = tr ? &maps.vt : &maps.v;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::VC; ++c, ++g) {
-                        const uint32_t slot = g % S::NVS, use = g / S::NVS;
-                        if (use > 0 && !(ok = wait(bars.vempty[slot], (use - 1) & 1)))
-                            break;
-                        const uint32_t bar = smem_addr(edge ? &bars.vedge[slot] : &bars.vfull[slot]);
+                        const uint32_t slot = g % S::NS, use = g / S::NS;
+                        if (use > 0 && !wait(bars.empty[slot], (use - 1) & 1))
+                            return false;
+                        const uint32_t bar = smem_addr(edge ? &bars.edge[slot] : &bars.full[slot]);
                         onedge = edge ? onedge | (1u << slot) : onedge & ~(1u << slot);
                         par ^= edge ? 1u << slot : 0u;
-                        mbar_arrive_expect_tx(bar, S::VSTAGE);
+                        mbar_arrive_expect_tx(bar, S::VBYTES);
 #pragma unroll
                         for (int b = 0; b < S::DV / 64; ++b)
-                            tma_3d(vring + slot * S::VSTAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
+                            tma_3d(ring + slot * S::STAGE + b * (S::VKEYS * 128), m, dv0 + 64 * b, kvh,
                                    row + c * S::VKEYS, bar);
                     }
+                    return true;
+                };
+                ok = keys(0);
+                for (int j = 0; ok && j < w.units; ++j) {
+                    const bool more = j + 1 < w.units;
+                    ok = S::PAIR ? (!more || keys(j + 1)) && values(j) : values(j) && (!more || keys(j + 1));
                 }
             }
             if (!ok) {
-                for (int i = 0; i < S::NVS; ++i) {
-                    const uint32_t uses = (g + S::NVS - 1 - i) / S::NVS;
+                // Copies in flight write this CTA's shared memory: let them land.
+                for (int i = 0; i < S::NS; ++i) {
+                    const uint32_t uses = (g + S::NS - 1 - i) / S::NS;
                     if ((onedge >> i) & 1)
-                        mbar_wait_bounded(smem_addr(&bars.vedge[i]), ((par >> i) & 1) ^ 1, 64);
+                        mbar_wait_bounded(smem_addr(&bars.edge[i]), ((par >> i) & 1) ^ 1, 64);
                     else if (uses > 0)
-                        mbar_wait_bounded(smem_addr(&bars.vfull[i]), (uses - 1) & 1, 64);
+                        mbar_wait_bounded(smem_addr(&bars.full[i]), (uses - 1) & 1, 64);
                 }
+                if (piece > 0)
+                    mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
             }
         }
-    } else if (warp == 1 || warp == 12) {
+    } else if (warp == 1) {
         // ---------------------------------------------- tensor-core issue
+        // One thread's tensor-core instructions execute in the order of their issue:
+        // scores may go over weights that a product issued before them reads. Its
+        // shared-memory accesses queue behind them, and the queue holds about six:
+        // what the next stage needs is waited for in the middle of a stage, so that
+        // there is something to issue as soon as the wait is over.
         if (elect_one()) {
             constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(S::DV, true);
-            const int me = warp == 1 ? 0 : 1;
-            uint32_t gk = 0, gv = 0; // key and value stages so far
-            bool ok = true;
-            // Scores of row tile t into buffer b; frees the key stages.
-            auto scores = [&](int t, int b) {
-                for (int c = 0; c < S::KC; ++c, ++gk) {
-                    const uint32_t slot = gk % S::NK;
-                    if (!wait(bars.kfull[slot], (gk / S::NK) & 1))
-                        return false;
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c) * kBlock);
-                    const uint64_t bd = sdesc_kmajor(kring + slot * kBlock);
+            uint32_t g = 0; // stages so far
+            auto ready = [&](uint32_t i) { return wait(bars.full[i % S::NS], (i / S::NS) & 1); };
+            // Scores of row tile t into buffer b from the stages i ..; `next` waits for
+            // what follows; `free`: the last user of the stages.
+            auto scores = [&](int t, int b, uint32_t i, bool see, bool free, auto next) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(s_col(b), ad + 2u * k, bd + 2u * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(smem_addr(&bars.kempty[slot]));
+                for (int c = 0; c < S::KC; ++c, ++i) {
+                    const uint32_t slot = i % S::NS;
+                    const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
+                    const uint64_t bd = sdesc_kmajor(ring + slot * S::STAGE);
+#pragma unroll
+                    for (int k = 0; k < 4 * S::KB; ++k) {
+                        if (k == 2 * S::KB && !(c + 1 < S::KC ? !see || ready(i + 1) : next()))
+                            return false;
+                        const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
+                        mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                    }
+                    if (free)
+                        mma_commit(smem_addr(&bars.empty[slot]));
                 }
                 mma_commit(smem_addr(&bars.s_full[b]));
                 return true;
             };
-            // O_t (+)= P V with the weights in buffer b; frees the value stages.
-            auto product = [&](int t, int b, bool acc) {
-                for (int c = 0; c < S::VC; ++c, ++gv) {
-                    const uint32_t slot = gv % S::NVS;
-                    if (!wait(bars.vfull[slot], (gv / S::NVS) & 1))
-                        return false;
-                    tc_fence_after();
-                    const uint64_t bd = sdesc_mnmajor(vring + slot * S::VSTAGE, S::VKEYS * 128);
+            // O_t (+)= P V with the weights in buffer b.
+            auto product = [&](int t, int b, uint32_t i, uint32_t acc, bool see, bool free, auto next) {
 #pragma unroll
-                    for (int k = 0; k < S::VKEYS / 16; ++k)
+                for (int c = 0; c < S::VC; ++c, ++i) {
+                    const uint32_t slot = i % S::NS;
+                    const uint64_t bd = sdesc_mnmajor(ring + slot * S::STAGE, S::VKEYS * 128);
+#pragma unroll
+                    for (int k = 0; k < S::VKEYS / 16; ++k) {
+                        if (k == S::VKEYS / 32 && !(c + 1 < S::VC ? !see || ready(i + 1) : next()))
+                            return false;
                         mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
-                               (acc || c > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(smem_addr(&bars.vempty[slot]));
+                               c > 0 || k > 0 ? 1u : acc);
+                    }
+                    if (free)
+                        mma_commit(smem_addr(&bars.empty[slot]));
                 }
                 mma_commit(smem_addr(&bars.o_done[t]));
                 return true;
             };
-            uint32_t it = 0, mine = 0; // units, pieces of this thread's row tile
+            // The weights of a row tile's next product; at a piece's first unit the last
+            // piece's accumulator has been read.
+            auto weights_in = [&](int t, int b, uint32_t use, bool begin, uint32_t mine) {
+                if (!wait(bars.p_full[b], use & 1) || !(!begin || mine == 0 || wait(bars.o_free[t], (mine - 1) & 1)))
+                    return false;
+                tc_fence_after();
+                return true;
+            };
+            auto nothing = [] { return true; };
+            uint32_t n = 0, n1 = 0;        // units so far, of the second row tile
+            uint32_t mine = 0, mine1 = 0;  // pieces so far, with a second row tile
+            bool ok = true;
             for (uint32_t piece = 0; ok; ++piece) {
                 if (!(ok = take(piece)))
                     break;
                 const int units = sh.piece[piece % kPieces].units, nq = sh.piece[piece % kPieces].nq;
                 done(piece);
-                if (units == 0)
+                if (units == 0 || !(ok = wait(bars.q_full, piece & 1) && ready(g)))
                     break;
-                if (S::TQ == 2) {
-                    // Thread t issues for row tile t. Its scores go over the weights that
-                    // its product before them has read: one thread's tensor-core
-                    // instructions execute in the order of their issue.
-                    if (!(ok = wait(bars.q_full, piece & 1)))
-                        break;
-                    if (me < nq) {
-                        ok = scores(me, me);
-                        for (int j = 0; ok && j < units; ++j, ++it) {
-                            if (j + 1 == units)
-                                mma_commit(smem_addr(&bars.q_empty));
-                            ok = wait(bars.p_full[me], it & 1) &&
-                                 (j > 0 || mine == 0 || wait(bars.o_free[me], (mine - 1) & 1));
-                            if (!ok)
-                                break;
-                            tc_fence_after();
-                            ok = product(me, me, j > 0) && (j + 1 >= units || scores(me, me));
+                if (S::PAIR) {
+                    // Two score buffers: S(j + 1) before the product of unit j. Stages:
+                    // K(0), K(1), V(0), K(2), V(1), ..., V(n - 1).
+                    ok = scores(0, n & 1, g, true, true, [&] { return units == 1 || ready(g + S::KC); });
+                    g += S::KC;
+                    for (int j = 0; ok && j < units; ++j, ++n) {
+                        const int b = n & 1;
+                        auto operands = [&](uint32_t v) { return ready(v) && weights_in(0, b, n >> 1, j == 0, mine); };
+                        if (j + 1 < units) {
+                            ok = scores(0, b ^ 1, g, true, true, [&] { return operands(g + S::KC); });
+                            g += S::KC;
+                        } else {
+                            ok = operands(g);
                         }
-                        ++mine;
-                    } else {
-                        // No such row tile in this piece: see its stages and free them.
-                        mbar_arrive(smem_addr(&bars.q_empty));
-                        for (int n = units * S::KC; ok && n > 0; --n, ++gk) {
-                            if (n <= (units - 1) * S::KC && n % S::KC == 0)
-                                for (int c = 0; ok && c < S::VC; ++c, ++gv) {
-                                    ok = wait(bars.vfull[gv % S::NVS], (gv / S::NVS) & 1);
-                                    mbar_arrive(smem_addr(&bars.vempty[gv % S::NVS]));
-                                }
-                            ok = ok && wait(bars.kfull[gk % S::NK], (gk / S::NK) & 1);
-                            mbar_arrive(smem_addr(&bars.kempty[gk % S::NK]));
-                        }
-                        for (int c = 0; ok && c < S::VC; ++c, ++gv) {
-                            ok = wait(bars.vfull[gv % S::NVS], (gv / S::NVS) & 1);
-                            mbar_arrive(smem_addr(&bars.vempty[gv % S::NVS]));
-                        }
+                        if (ok && (j + 2 == units || units == 1))
+                            mma_commit(smem_addr(&bars.q_empty));
+                        ok = ok && product(0, b, g, j > 0 ? 1u : 0u, true, true,
+                                           [&] { return j + 2 >= units || ready(g + S::VC); });
+                        g += S::VC;
                     }
-                } else if (me == 0) {
-                    // Scores of the units in turn into two buffers, once a buffer's
-                    // weights (of two units ago) have been used.
-                    if (!(ok = wait(bars.q_full, piece & 1)))
-                        break;
-                    for (int j = 0; ok && j < units; ++j, ++it)
-                        ok = (it < 2 || wait(bars.s_free[it & 1], ((it >> 1) - 1) & 1)) && scores(0, it & 1);
-                    if (ok)
-                        mma_commit(smem_addr(&bars.q_empty));
                 } else {
-                    // Products, once the weights are there and, at a piece's first, the
-                    // last piece's accumulator has been read.
-                    for (int j = 0; ok && j < units; ++j, ++it) {
-                        ok = wait(bars.p_full[it & 1], (it >> 1) & 1) &&
-                             (j > 0 || mine == 0 || wait(bars.o_free[0], (mine - 1) & 1));
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        if ((ok = product(0, it & 1, j > 0)))
-                            mma_commit(smem_addr(&bars.s_free[it & 1])); // after o_done: see the waits on it
+                    // One score buffer per row tile: its product, then its next scores.
+                    // Stages: K(0), V(0), K(1), V(1), ...
+                    const bool two = nq == 2;
+                    ok = scores(0, 0, g, true, !two, nothing) && (!two || scores(1, 1, g, false, true, nothing));
+                    g += S::KC;
+                    for (int j = 0; ok && j < units; ++j, ++n) {
+                        const bool more = j + 1 < units;
+                        const uint32_t acc = j > 0 ? 1u : 0u;
+                        if (!more)
+                            mma_commit(smem_addr(&bars.q_empty));
+                        auto second = [&] { return !two || weights_in(1, 1, n1, j == 0, mine1); };
+                        ok = ready(g) && weights_in(0, 0, n, j == 0, mine) &&
+                             product(0, 0, g, acc, true, !two, [&] { return more ? ready(g + S::VC) : second(); }) &&
+                             (!more || scores(0, 0, g + S::VC, true, !two, second)) &&
+                             (!two || (product(1, 1, g, acc, false, true, nothing) &&
+                                       (!more || scores(1, 1, g + S::VC, false, true, nothing))));
+                        g += S::VC + (more ? S::KC : 0);
+                        n1 += two ? 1u : 0u;
                     }
-                    ++mine;
+                    mine1 += two ? 1u : 0u;
                 }
+                ++mine;
             }
             // Every product has finished before tensor memory is freed.
-            mma_commit(smem_addr(&bars.drain[me]));
-            mbar_wait_bounded(smem_addr(&bars.drain[me]), 0, 1024);
+            mma_commit(smem_addr(&bars.drain));
+            mbar_wait_bounded(smem_addr(&bars.drain), 0, 1024);
         }
     } else if (warp == 2) {
         // ------------------------------------- value rows of edge tiles
-        uint32_t base = 0, par = 0; // value stages before the piece; phase of each slot's edge barrier
+        uint32_t base = 0, par = 0; // stages before the piece; phase of each slot's edge barrier
         int piece = 0;
         bool ok = true;
         for (; ok; ++piece) {
@@ -947,19 +938,20 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 const int x = w.u + j;
                 if (!edge_unit<TREE>(a, w, x))
                     continue;
-                const uint32_t gv = base + (uint32_t)(j * S::VC);
+                const uint32_t gv = base + (uint32_t)(j * (S::KC + S::VC) + S::KC) +
+                                    (S::PAIR && j + 1 < units ? S::KC : 0);
                 for (int c = 0; ok && c < S::VC; ++c) {
-                    const uint32_t slot = (gv + c) % S::NVS;
+                    const uint32_t slot = (gv + c) % S::NS;
                     // Classes of this stage's keys: key c * VKEYS + 32 h + lane in bits 2h, 2h + 1.
                     uint32_t cls = 0;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
                         cls |= (uint32_t)key_class<TREE>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
-                    ok = __all_sync(0xFFFFFFFFu, wait(bars.vedge[slot], (par >> slot) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(bars.edge[slot], (par >> slot) & 1));
                     if (!ok)
                         break;
                     par ^= 1u << slot;
-                    const uint32_t vb = vring + slot * S::VSTAGE;
+                    const uint32_t vb = ring + slot * S::STAGE;
                     bool found = false;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h) {
@@ -1006,10 +998,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_addr(&bars.vfull[slot]));
+                        mbar_arrive(smem_addr(&bars.full[slot]));
                 }
             }
-            base += (uint32_t)(units * S::VC);
+            base += (uint32_t)(units * (S::KC + S::VC));
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------ softmax
