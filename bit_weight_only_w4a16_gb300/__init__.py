@@ -326,26 +326,53 @@ def w4_decode_prologue(token, pos, qtable, scales, group: int = 32, x_next=None,
     return o
 
 
-def _rows16(t, name, heads=None, D=None):
-    """A bf16 [rows][heads][D] tensor whose rows may be strided (a view of a wider
-    projection); returns the elements between rows."""
+# The calls below are made several times per decode step: their checks are
+# written out and the stream handle is taken as a number (about 9 us less a call
+# than through Stream objects and c_void_p).
+_BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+
+
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _tensor(t, name, dtypes, shape):
+    """A contiguous CUDA tensor of these types and this shape; its address."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} is not served")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ints(t, name, n):
+    """A contiguous CUDA int32 tensor of n elements; its address."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 with {n} elements")
+    return t.data_ptr()
+
+
+def _rows(t, name, rows, heads, D):
+    """bf16 [rows][heads][D] whose rows may be strided (a view of a wider
+    projection): elements between rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _BITS16:
         raise TypeError(f"{name} must be bf16 (or its raw 16-bit bits)")
-    if t.dim() != 3 or (D is not None and t.shape[2] != D) or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [rows][heads][D]")
-    s = t.stride()
-    if (t.shape[2] > 1 and s[2] != 1) or (t.shape[1] > 1 and s[1] != t.shape[2]):
-        raise ValueError(f"{name}: heads and D must be contiguous")
-    return s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * t.shape[2])
-
-
-def _i32(t, name, n):
-    _cuda(t, name)
-    if t.dtype != torch.int32 or t.numel() != n:
-        raise ValueError(f"{name} must be int32 with {n} elements")
-    return t
+    if t.shape != (rows, heads, D):
+        raise ValueError(f"{name} must be [{rows}][{heads}][{D}], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        raise ValueError(f"{name}: heads and head width must be contiguous")
+    return s0 if rows > 1 else heads * D
 
 
 def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0, out=None, stream=None):
@@ -355,23 +382,17 @@ def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0
     cu_q, cu_k int32 [B + 1]: the sequences' first rows (cu_k None: as cu_q). A
     sequence's queries are the last of its keys' positions; window 0 = no window.
     """
-    ldq = _rows16(q, "q")
     Sq, Hq, D = q.shape
-    ldk = _rows16(k, "k", D=D)
     Sk, Hkv, _ = k.shape
-    ldv = _rows16(v, "v", Hkv, D)
-    if v.shape[0] != Sk:
-        raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}")
     B = cu_q.numel() - 1
-    _i32(cu_q, "cu_q", B + 1)
-    if cu_k is not None:
-        _i32(cu_k, "cu_k", B + 1)
     o = torch.empty((Sq, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    ldo = _rows16(o, "out", Hq, D)
-    if o.shape[0] != Sq:
-        raise ValueError(f"out must be [{Sq}][{Hq}][{D}]")
-    _check(_lib.w4_attn_prompt(_ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), B, Sq, Sk, Hq, Hkv, D,
-                               ldq, ldk, ldv, ldo, int(window), float(scale), _stream(stream)), "w4_attn_prompt")
+    ldq, ldk, ldv = _rows(q, "q", Sq, Hq, D), _rows(k, "k", Sk, Hkv, D), _rows(v, "v", Sk, Hkv, D)
+    ldo = Hq * D if out is None else _rows(o, "out", Sq, Hq, D)
+    rc = _lib.w4_attn_prompt(o.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ints(cu_q, "cu_q", B + 1),
+                             None if cu_k is None else _ints(cu_k, "cu_k", B + 1), B, Sq, Sk, Hq, Hkv, D, ldq, ldk,
+                             ldv, ldo, window, scale, _raw_stream(stream, q))
+    if rc:
+        _check(rc, "w4_attn_prompt")
     return o
 
 
@@ -385,24 +406,18 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
     level's position (cached positions below it are kept); kpos int32 [B][T]
     recorded positions of a ring, or None (slot t holds position t).
     """
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (k_tree, "k_tree"), (v_tree, "v_tree")):
-        _bits16(t, n)
     B, N, Hq, D = q.shape
-    T, Hkv = k.shape[1], k.shape[2]
-    if tuple(k.shape) != (B, T, Hkv, D) or v.shape != k.shape or tuple(k_tree.shape) != (B, N, Hkv, D) or \
-            v_tree.shape != k_tree.shape:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
-                         f"k_tree {tuple(k_tree.shape)}, v_tree {tuple(v_tree.shape)}")
-    _i32(parents, "parents", B * N)
-    _i32(pos, "pos", B)
-    if kpos is not None:
-        _i32(kpos, "kpos", B * T)
-    o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else _bits16(out, "out")
-    if tuple(o.shape) != (B, N, Hq, D):
-        raise ValueError(f"out must be [{B}][{N}][{Hq}][{D}]")
-    _check(_lib.w4_attn_tree(_ptr(o), _ptr(q), _ptr(k), _ptr(v), _ptr(kpos), _ptr(k_tree), _ptr(v_tree),
-                             _ptr(parents), _ptr(pos), B, N, T, Hq, Hkv, D, int(window), float(scale),
-                             _stream(stream)), "w4_attn_tree")
+    _, T, Hkv, _ = k.shape
+    o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    cache, tree, rows = (B, T, Hkv, D), (B, N, Hkv, D), (B, N, Hq, D)
+    rc = _lib.w4_attn_tree(_tensor(o, "out", _BITS16, rows), _tensor(q, "q", _BITS16, rows),
+                           _tensor(k, "k", _BITS16, cache), _tensor(v, "v", _BITS16, cache),
+                           None if kpos is None else _ints(kpos, "kpos", B * T),
+                           _tensor(k_tree, "k_tree", _BITS16, tree), _tensor(v_tree, "v_tree", _BITS16, tree),
+                           _ints(parents, "parents", B * N), _ints(pos, "pos", B), B, N, T, Hq, Hkv, D, window, scale,
+                           _raw_stream(stream, q))
+    if rc:
+        _check(rc, "w4_attn_tree")
     return o
 
 
@@ -412,18 +427,20 @@ def w4_logprobs(logits, targets=None, topk: int = 0, status=None, stream=None):
     if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
     M, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+    s0, s1 = logits.stride()
+    if s1 != 1 and V > 1:
         raise ValueError("a row of logits must be contiguous")
-    ld = logits.stride(0) if M > 1 else max(logits.stride(0), V)
-    if targets is not None:
-        _i32(targets, "targets", M)
-    k = int(topk)
-    dev = logits.device
-    f = torch.empty((2 + max(k, 0), M), dtype=torch.float32, device=dev)
-    lp, ent, top = (f[0] if targets is not None else None), f[1], f[2:].view(M, max(k, 0))
-    ids = torch.empty((M, max(k, 0)), dtype=torch.int32, device=dev)
-    _check(_lib.w4_logprobs(_ptr(lp), _ptr(ent), _ptr(top) if k > 0 else None, _ptr(ids) if k > 0 else None,
-                            _ptr(logits), _ptr(targets), M, V, ld, k, _ptr(status), _stream(stream)), "w4_logprobs")
+    k, dev = max(int(topk), 0), logits.device
+    lp = None if targets is None else torch.empty((M,), dtype=torch.float32, device=dev)
+    ent = torch.empty((M,), dtype=torch.float32, device=dev)
+    top = torch.empty((M, k), dtype=torch.float32, device=dev)
+    ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+    rc = _lib.w4_logprobs(None if lp is None else lp.data_ptr(), ent.data_ptr(), top.data_ptr() if k else None,
+                          ids.data_ptr() if k else None, logits.data_ptr(),
+                          None if targets is None else _ints(targets, "targets", M), M, V, s0 if M > 1 else V,
+                          topk, None if status is None else _ints(status, "status", 1), _raw_stream(stream, logits))
+    if rc:
+        _check(rc, "w4_logprobs")
     return lp, ent, top, ids
 
 
@@ -431,13 +448,13 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
     """Store the accepted tokens: rows path[b][j] (j < count[b]) of the trees k_tree,
     v_tree bf16 [L][B][N][W] become position pos[b] + j of the caches [L][B][T][W]
     (a ring when kpos int32 [B][T] is given: it records the positions)."""
-    _bits16(k_cache, "k_cache"); _bits16(v_cache, "v_cache"); _bits16(k_tree, "k_tree"); _bits16(v_tree, "v_tree")
     L, B, T, W = k_cache.shape
     N = k_tree.shape[2]
-    if v_cache.shape != k_cache.shape or tuple(k_tree.shape) != (L, B, N, W) or v_tree.shape != k_tree.shape:
-        raise ValueError("cache / tree shape mismatch")
-    _i32(path, "path", B * N); _i32(count, "count", B); _i32(pos, "pos", B)
-    if kpos is not None:
-        _i32(kpos, "kpos", B * T)
-    _check(_lib.w4_kv_commit(_ptr(k_cache), _ptr(v_cache), _ptr(kpos), _ptr(k_tree), _ptr(v_tree), _ptr(path),
-                             _ptr(count), _ptr(pos), L, B, N, T, W, _ptr(status), _stream(stream)), "w4_kv_commit")
+    cache, tree = (L, B, T, W), (L, B, N, W)
+    rc = _lib.w4_kv_commit(_tensor(k_cache, "k_cache", _BITS16, cache), _tensor(v_cache, "v_cache", _BITS16, cache),
+                           None if kpos is None else _ints(kpos, "kpos", B * T),
+                           _tensor(k_tree, "k_tree", _BITS16, tree), _tensor(v_tree, "v_tree", _BITS16, tree),
+                           _ints(path, "path", B * N), _ints(count, "count", B), _ints(pos, "pos", B), L, B, N, T, W,
+                           None if status is None else _ints(status, "status", 1), _raw_stream(stream, k_cache))
+    if rc:
+        _check(rc, "w4_kv_commit")

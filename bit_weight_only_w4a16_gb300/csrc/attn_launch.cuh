@@ -3,6 +3,8 @@
 
 #include "attn_tiles.cuh"
 
+#include <atomic>
+
 namespace w4 {
 namespace attn {
 
@@ -50,8 +52,8 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     if (!encode_rows(&m.q, q.p, q.rows, a.Hq, D, q.ld, a.G, a.tpt) ||
         !encode_rows(&m.k, k.p, k.rows, a.Hkv, D, k.ld, 1, kKeys) ||
         !encode_rows(&m.v, v.p, v.rows, a.Hkv, D, v.ld, 1, S::VKEYS) ||
-        !encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||
-        !encode_rows(&m.vt, vt.p, vt.rows, a.Hkv, D, vt.ld, 1, S::VKEYS))
+        (TREE && (!encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||
+                  !encode_rows(&m.vt, vt.p, vt.rows, a.Hkv, D, vt.ld, 1, S::VKEYS))))
         return cudaErrorInvalidValue;
     a.ws_o = ws;
     a.ws_ml = ws + (size_t)2 * num_sms * kSlotFloats;
@@ -59,9 +61,19 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     a.where = a.rec + 2 * num_sms;
 
     auto kern = attn_kernel<D, TREE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    // Once per device: the attribute belongs to the kernel there.
+    static std::atomic<unsigned long long> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    if (dev >= 64 || !((set.load(std::memory_order_relaxed) >> dev) & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
