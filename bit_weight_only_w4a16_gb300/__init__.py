@@ -330,6 +330,7 @@ def w4_decode_prologue(token, pos, qtable, scales, group: int = 32, x_next=None,
 # written out and the stream handle is taken as a number (about 9 us less a call
 # than through Stream objects and c_void_p).
 _BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+_F32, _I32 = frozenset((torch.float32,)), frozenset((torch.int32,))
 
 
 def _raw_stream(stream, t):
@@ -421,9 +422,10 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
     return o
 
 
-def w4_logprobs(logits, targets=None, topk: int = 0, status=None, stream=None):
+def w4_logprobs(logits, targets=None, topk: int = 0, status=None, out=None, stream=None):
     """(logprob [M] or None, entropy [M], top_logprob [M][topk], top_id [M][topk]) of
-    fp32 logits [M][V] (rows may be strided) and int32 targets [M]."""
+    fp32 logits [M][V] (rows may be strided) and int32 targets [M]. out: the four
+    tensors to write instead (None in the place of one that is not wanted)."""
     if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
     M, V = logits.shape
@@ -431,12 +433,20 @@ def w4_logprobs(logits, targets=None, topk: int = 0, status=None, stream=None):
     if s1 != 1 and V > 1:
         raise ValueError("a row of logits must be contiguous")
     k, dev = max(int(topk), 0), logits.device
-    lp = None if targets is None else torch.empty((M,), dtype=torch.float32, device=dev)
-    ent = torch.empty((M,), dtype=torch.float32, device=dev)
-    top = torch.empty((M, k), dtype=torch.float32, device=dev)
-    ids = torch.empty((M, k), dtype=torch.int32, device=dev)
-    rc = _lib.w4_logprobs(None if lp is None else lp.data_ptr(), ent.data_ptr(), top.data_ptr() if k else None,
-                          ids.data_ptr() if k else None, logits.data_ptr(),
+    if out is None:
+        lp = None if targets is None else torch.empty((M,), dtype=torch.float32, device=dev)
+        ent = torch.empty((M,), dtype=torch.float32, device=dev)
+        top = torch.empty((M, k), dtype=torch.float32, device=dev)
+        ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+    else:
+        lp, ent, top, ids = out
+        for t, name, dt, shape in ((lp, "logprob", _F32, (M,)), (ent, "entropy", _F32, (M,)),
+                                   (top, "top_logprob", _F32, (M, k)), (ids, "top_id", _I32, (M, k))):
+            if t is not None:
+                _tensor(t, name, dt, shape)
+    rc = _lib.w4_logprobs(None if lp is None else lp.data_ptr(), None if ent is None else ent.data_ptr(),
+                          top.data_ptr() if k and top is not None else None,
+                          ids.data_ptr() if k and ids is not None else None, logits.data_ptr(),
                           None if targets is None else _ints(targets, "targets", M), M, V, s0 if M > 1 else V,
                           topk, None if status is None else _ints(status, "status", 1), _raw_stream(stream, logits))
     if rc:

@@ -7,7 +7,7 @@
 // for any m; one pass keeps m near the running maximum. m moves only when the
 // maximum has grown by more than 2^8 (a weight is then at most 256, which bf16
 // holds with the same relative error), so the accumulator in tensor memory is
-// rarely rescaled. Weights are rounded to bf16 (relative 2^-9) for the tensor
+// rarely rescaled. Weights are rounded to bf16 (relative 2^-8) for the tensor
 // core's value product: the output is bf16, whose own rounding is as large. The
 // sum of the weights, m and the accumulator are fp32.
 //

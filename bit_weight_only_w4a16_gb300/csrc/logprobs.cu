@@ -32,6 +32,9 @@ constexpr int kChunk = 256; // logits per chunk: two float4 per lane
 constexpr int kWarps = 8;
 constexpr int kBatch = 4; // chunks in flight per warp
 constexpr float kLog2e = 1.4426950408889634f;
+// Differences from the maximum are cut here where they are factors: 0 * -inf (a
+// masked logit, or finite logits further apart than fp32 reaches) is not 0.
+constexpr float kLeast = -1e30f;
 
 struct LogprobArgs {
     const float *x;
@@ -97,7 +100,7 @@ __device__ __forceinline__ void merge_stats(float &m, float &s, float &u, float 
         u += u2;
         return;
     }
-    const float d = m - M, d2 = m2 - M;
+    const float d = fmaxf(m - M, kLeast), d2 = fmaxf(m2 - M, kLeast);
     const float f = ex2f(d * kLog2e), f2 = ex2f(d2 * kLog2e);
     u = f * fmaf(d, s, u) + f2 * fmaf(d2, s2, u2);
     s = f * s + f2 * s2;
@@ -148,7 +151,7 @@ logprob_stream_kernel(const LogprobArgs a)
         }
         if (bm > m) {
             if (m != -INFINITY) {
-                const float d = m - bm, f = ex2f(d * kLog2e);
+                const float d = fmaxf(m - bm, kLeast), f = ex2f(d * kLog2e);
                 u = f * fmaf(d, s, u);
                 s *= f;
             }
@@ -162,7 +165,7 @@ logprob_stream_kernel(const LogprobArgs a)
                 const float d = v[b][i] - ref;
                 const float e = ex2f(d * kLog2e);
                 s += e;
-                u = fmaf(e, fmaxf(d, -1e30f), u); // a masked logit (-inf) adds 0
+                u = fmaf(e, fmaxf(d, kLeast), u);
             }
     }
 #pragma unroll

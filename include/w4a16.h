@@ -313,7 +313,7 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  *   16-byte aligned pointers, cu_* 4-byte; ld* multiples of 8, at least heads * D.
  *   B in 1..4096, Hq / Hkv a whole number in 1..128, D in {64, 128, 256, 384,
  *   512}, scale > 0 and finite; rows and ld* below 2^31.
- * Scores and sums fp32; weights bf16 (relative 2^-9) in the value product, out
+ * Scores and sums fp32; weights bf16 (relative 2^-8) in the value product, out
  * rounded once. What a row does not keep never reaches it, NaN and infinities
  * included. Lengths are read when the kernels run: one captured call serves
  * every batch with the same total_q and total_k. Uses the library's split
