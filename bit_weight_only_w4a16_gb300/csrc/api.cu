@@ -31,6 +31,7 @@ struct DeviceState {
     int num_sms = 0;
     unsigned long long *keys = nullptr;
     int *err = nullptr; // device error word written by kernels whose bounded waits ran out
+    int *left = nullptr; // log probabilities: blocks of each row that have finished (zeros between calls)
     float *ws = nullptr; // prefill split-K and attention partials, ws_capacity(num_sms) floats
 };
 
@@ -83,10 +84,15 @@ int device_state(DeviceState **out)
         if (e != cudaSuccess)
             return cuda_fail(e);
         void *w = nullptr;
-        e = cudaMalloc(&w, ws_capacity(sms) * sizeof(float));
+        const size_t ws_bytes = ws_capacity(sms) * sizeof(float), left_bytes = w4::kLogprobRows * sizeof(int);
+        e = cudaMalloc(&w, ws_bytes + left_bytes);
         if (e != cudaSuccess)
             return cuda_fail(e);
         st.ws = static_cast<float *>(w);
+        st.left = reinterpret_cast<int *>(static_cast<char *>(w) + ws_bytes);
+        e = cudaMemset(st.left, 0, left_bytes);
+        if (e != cudaSuccess)
+            return cuda_fail(e);
         st.num_sms = sms;
         // One-time lookups that plans use, done here so that a call captured
         // into a graph later makes none of them.
@@ -631,7 +637,7 @@ int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top
     p.ld = ld;
     p.k = top_logprob || top_id ? topk : 0;
     p.status = status;
-    cudaError_t e = w4::run_logprobs(p, st->ws, ws_capacity(st->num_sms), st->num_sms,
+    cudaError_t e = w4::run_logprobs(p, st->ws, ws_capacity(st->num_sms), st->left, st->num_sms,
                                      static_cast<cudaStream_t>(stream));
     if (e == cudaErrorNotSupported)
         return W4_ERR_UNSUPPORTED;

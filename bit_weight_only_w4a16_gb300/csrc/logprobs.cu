@@ -15,7 +15,8 @@
 // keeps the maximum of every 256 logits. In the order (value descending, index
 // ascending) the k largest logits lie in the k chunks whose maxima are first in
 // that order, because an element of any other chunk has k chunk maxima before
-// it. The second kernel picks those chunks and looks at them alone.
+// it. The block that finishes a row last picks those chunks and looks at them
+// alone, while other rows' blocks still stream.
 //
 // Bound by the read of the logits: 4 V bytes a row.
 #include "common.cuh"
@@ -42,6 +43,7 @@ struct LogprobArgs {
     int V, nc, S; // logits per row, chunks per row, blocks per row
     float *cmax;  // [rows][nc]
     float *part;  // [rows][S][4]: m, s, u
+    int *left;    // [rows] blocks that have finished; 0 before and after a call
     const int32_t *targets;
     float *logprob, *entropy, *top_logprob;
     int32_t *top_id;
@@ -107,8 +109,196 @@ __device__ __forceinline__ void merge_stats(float &m, float &s, float &u, float 
     m = M;
 }
 
+// --------------------------------------------------- lists of the largest ----
+
+// A key orders (value descending, index ascending): larger keys come first.
+// Zeros of either sign are equal. 0 is below every key.
+__device__ __forceinline__ unsigned long long make_key(float x, uint32_t index)
+{
+    const uint32_t b = __float_as_uint(x + 0.f);
+    const uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    return ((unsigned long long)o << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(unsigned long long k)
+{
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint32_t key_index(unsigned long long k) { return ~(uint32_t)k; }
+
+__device__ __forceinline__ unsigned long long cmp_xchg(unsigned long long k, int d, bool keep_max)
+{
+    const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, k, d);
+    return keep_max == (k > o) ? k : o;
+}
+
+// 32 keys, one per lane, into descending order by lane.
+__device__ __forceinline__ unsigned long long sort32(unsigned long long k, int lane)
+{
+#pragma unroll
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+        for (int d = n >> 1; d; d >>= 1)
+            k = cmp_xchg(k, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
+    return k;
+}
+
+// The 32 largest of two descending lists, in descending order.
+__device__ __forceinline__ unsigned long long merge32(unsigned long long list, unsigned long long other, int lane)
+{
+    const unsigned long long r = __shfl_sync(0xFFFFFFFFu, other, 31 - lane);
+    unsigned long long k = list > r ? list : r;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        k = cmp_xchg(k, d, (lane & d) == 0);
+    return k;
+}
+
+// The block's lists into one, held by every warp: a tree of merges.
+__device__ __forceinline__ unsigned long long merge_block(unsigned long long list, unsigned long long (*sl)[32],
+                                                          int lane, int w)
+{
+    static_assert(kWarps == 8, "three rounds");
+#pragma unroll
+    for (int d = 4; d; d >>= 1) {
+        __syncthreads(); // the lists of the round before have been read
+        if (w >= d && w < 2 * d)
+            sl[w][lane] = list;
+        __syncthreads();
+        if (w < d)
+            list = merge32(list, sl[w + d][lane], lane);
+    }
+    if (w == 0)
+        sl[0][lane] = list;
+    __syncthreads();
+    return sl[0][lane];
+}
+
+// A row's outputs from its blocks' parts and its chunk maxima; they come from other
+// SMs, so they are read from L2.
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
+{
+    __shared__ unsigned long long sl[kWarps][32], pend[kWarps][kChunk + 32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const float *row = a.x + r * a.ld;
+    const int mis = row_mis(row);
+
+    // Sums: every warp merges all blocks' parts (lane i: parts i, i + 32, ...) in the same order.
+    float m = -INFINITY, s = 0.f, u = 0.f;
+    for (int i = lane; i < a.S; i += 32) {
+        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part + (r * a.S + i) * 4));
+        merge_stats(m, s, u, p.x, p.y, p.z);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d),
+                    u2 = __shfl_xor_sync(0xFFFFFFFFu, u, d);
+        // the lower lane's part first: both lanes form the same sums
+        if (lane & d) {
+            float mm = m2, s1 = s2, u1 = u2;
+            merge_stats(mm, s1, u1, m, s, u);
+            m = mm;
+            s = s1;
+            u = u1;
+        } else {
+            merge_stats(m, s, u, m2, s2, u2);
+        }
+    }
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    const bool bad = s != s;            // a NaN or +inf among the logits
+    const bool none = m == -INFINITY;   // every logit is -inf
+    const float logs = bad ? nan : logf(s);
+    if (threadIdx.x == 0) {
+        if (a.entropy)
+            a.entropy[r] = bad ? nan : (none ? 0.f : logs - u / s);
+        if (a.logprob) {
+            const int t = a.targets[r];
+            float y = 0.f;
+            if (t < 0 || t >= a.V) {
+                if (a.status)
+                    *a.status = 1;
+            } else {
+                const float x = row[t];
+                y = bad ? nan : (x == -INFINITY ? -INFINITY : (x - m) - logs);
+            }
+            a.logprob[r] = y;
+        }
+    }
+    if (a.k == 0)
+        return;
+
+    // The k first chunks by (maximum, index): four groups of 32 at a time per warp.
+    const float *cmax = a.cmax + r * a.nc;
+    unsigned long long list = 0;
+    for (int c0 = w * 32; c0 < a.nc; c0 += 4 * kWarps * 32) {
+        unsigned long long k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + j * kWarps * 32 + lane;
+            k[j] = c < a.nc ? make_key(__ldcg(cmax + c), c) : 0ull;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            k[j] = sort32(k[j], lane);
+        list = merge32(list, merge32(merge32(k[0], k[1], lane), merge32(k[2], k[3], lane), lane), lane);
+    }
+    const unsigned long long chunks = merge_block(list, sl, lane, w);
+    // Their logits, chunk i by warp i % kWarps. None below the k-th chunk's maximum
+    // is among the k largest; the others are collected and merged 32 at a time.
+    const unsigned long long last = __shfl_sync(0xFFFFFFFFu, chunks, a.k - 1);
+    const unsigned long long least = last >> 32 << 32; // any index
+    list = 0;
+    int n = 0; // logits collected in pend[w]
+    constexpr int kMine = 32 / kWarps; // chunks of a warp at most
+    float v[kMine][8];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const unsigned long long ck = __shfl_sync(0xFFFFFFFFu, chunks, w + i * kWarps);
+        if (w + i * kWarps < a.k && ck != 0) {
+            load_chunk(row, mis, a.V, (int)key_index(ck), lane, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.f; // not used
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const unsigned long long ck = __shfl_sync(0xFFFFFFFFu, chunks, w + i * kWarps);
+        const bool mine = w + i * kWarps < a.k && ck != 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long e = (long long)key_index(ck) * kChunk - mis + 4 * lane + (j >> 2) * 128 + (j & 3);
+            const unsigned long long key = mine && e >= 0 && e < a.V ? make_key(v[i][j], (uint32_t)e) : 0ull;
+            const bool in = key != 0 && key >= least;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+            if (in)
+                pend[w][n + __popc(who & ((1u << lane) - 1u))] = key;
+            n += __popc(who);
+        }
+        // At most 31 stay for the next chunk (none after the last).
+#pragma unroll 1
+        while (n >= 32 || (i == kMine - 1 && n > 0)) {
+            const int m = n < 32 ? n : 32;
+            __syncwarp();
+            list = merge32(list, sort32(lane < m ? pend[w][n - m + lane] : 0ull, lane), lane);
+            n -= m;
+            __syncwarp();
+        }
+    }
+    const unsigned long long best = merge_block(list, sl, lane, w);
+    if (w == 0 && lane < a.k) {
+        const float x = key_value(best);
+        const size_t o = r * a.k + lane;
+        if (a.top_id)
+            a.top_id[o] = bad || best == 0 ? -1 : (int32_t)key_index(best);
+        if (a.top_logprob)
+            a.top_logprob[o] = bad ? nan : (best == 0 || x == -INFINITY ? -INFINITY : (x - m) - logs);
+    }
+}
+
 __global__ void __launch_bounds__(kWarps * 32)
-logprob_stream_kernel(const LogprobArgs a)
+logprob_kernel(const LogprobArgs a)
 {
     __shared__ float sm[kWarps], ss[kWarps], su[kWarps];
     pdl_launch_dependents();
@@ -184,200 +374,28 @@ logprob_stream_kernel(const LogprobArgs a)
             merge_stats(m, s, u, sm[i], ss[i], su[i]);
         *reinterpret_cast<float4 *>(a.part + ((size_t)blockIdx.y * a.S + blockIdx.x) * 4) = make_float4(m, s, u, 0.f);
     }
-}
-
-// --------------------------------------------------- lists of the largest ----
-
-// A key orders (value descending, index ascending): larger keys come first.
-// Zeros of either sign are equal. 0 is below every key.
-__device__ __forceinline__ unsigned long long make_key(float x, uint32_t index)
-{
-    const uint32_t b = __float_as_uint(x + 0.f);
-    const uint32_t o = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    return ((unsigned long long)o << 32) | (uint32_t)~index;
-}
-__device__ __forceinline__ float key_value(unsigned long long k)
-{
-    const uint32_t o = (uint32_t)(k >> 32);
-    return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
-}
-__device__ __forceinline__ uint32_t key_index(unsigned long long k) { return ~(uint32_t)k; }
-
-__device__ __forceinline__ unsigned long long cmp_xchg(unsigned long long k, int d, bool keep_max)
-{
-    const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, k, d);
-    return keep_max == (k > o) ? k : o;
-}
-
-// 32 keys, one per lane, into descending order by lane.
-__device__ __forceinline__ unsigned long long sort32(unsigned long long k, int lane)
-{
-#pragma unroll
-    for (int n = 2; n <= 32; n <<= 1)
-#pragma unroll
-        for (int d = n >> 1; d; d >>= 1)
-            k = cmp_xchg(k, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
-    return k;
-}
-
-// The 32 largest of two descending lists, in descending order.
-__device__ __forceinline__ unsigned long long merge32(unsigned long long list, unsigned long long other, int lane)
-{
-    const unsigned long long r = __shfl_sync(0xFFFFFFFFu, other, 31 - lane);
-    unsigned long long k = list > r ? list : r;
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        k = cmp_xchg(k, d, (lane & d) == 0);
-    return k;
-}
-
-// The block's lists into one, held by every warp: a tree of merges.
-__device__ __forceinline__ unsigned long long merge_block(unsigned long long list, unsigned long long (*sl)[32],
-                                                          int lane, int w)
-{
-    static_assert(kWarps == 8, "three rounds");
-#pragma unroll
-    for (int d = 4; d; d >>= 1) {
-        __syncthreads(); // the lists of the round before have been read
-        if (w >= d && w < 2 * d)
-            sl[w][lane] = list;
-        __syncthreads();
-        if (w < d)
-            list = merge32(list, sl[w + d][lane], lane);
-    }
-    if (w == 0)
-        sl[0][lane] = list;
+    // The block that finishes last sees all parts and chunk maxima of the row: each
+    // block's are written before its count (fence), and read after all counts.
+    __threadfence();
     __syncthreads();
-    return sl[0][lane];
-}
-
-__global__ void __launch_bounds__(kWarps * 32)
-logprob_finish_kernel(const LogprobArgs a)
-{
-    __shared__ unsigned long long sl[kWarps][32], pend[kWarps][kChunk + 32];
-    pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const size_t r = blockIdx.x;
-    const float *row = a.x + r * a.ld;
-    const int mis = row_mis(row);
-
-    // Sums: every warp merges all blocks' parts (lane i: parts i, i + 32, ...) in the same order.
-    float m = -INFINITY, s = 0.f, u = 0.f;
-    for (int i = lane; i < a.S; i += 32) {
-        const float4 p = *reinterpret_cast<const float4 *>(a.part + (r * a.S + i) * 4);
-        merge_stats(m, s, u, p.x, p.y, p.z);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d),
-                    u2 = __shfl_xor_sync(0xFFFFFFFFu, u, d);
-        // the lower lane's part first: both lanes form the same sums
-        if (lane & d) {
-            float mm = m2, s1 = s2, u1 = u2;
-            merge_stats(mm, s1, u1, m, s, u);
-            m = mm;
-            s = s1;
-            u = u1;
-        } else {
-            merge_stats(m, s, u, m2, s2, u2);
-        }
-    }
-    const float nan = __uint_as_float(0x7FFFFFFFu);
-    const bool bad = s != s;            // a NaN or +inf among the logits
-    const bool none = m == -INFINITY;   // every logit is -inf
-    const float logs = bad ? nan : logf(s);
+    __shared__ int s_last;
     if (threadIdx.x == 0) {
-        if (a.entropy)
-            a.entropy[r] = bad ? nan : (none ? 0.f : logs - u / s);
-        if (a.logprob) {
-            const int t = a.targets[r];
-            float y = 0.f;
-            if (t < 0 || t >= a.V) {
-                if (a.status)
-                    *a.status = 1;
-            } else {
-                const float x = row[t];
-                y = bad ? nan : (x == -INFINITY ? -INFINITY : (x - m) - logs);
-            }
-            a.logprob[r] = y;
-        }
+        const int n = atomicAdd(a.left + blockIdx.y, 1);
+        s_last = n == a.S - 1;
+        if (s_last)
+            a.left[blockIdx.y] = 0;
     }
-    if (a.k == 0)
-        return;
-
-    // The k first chunks by (maximum, index): four groups of 32 at a time per warp.
-    const float *cmax = a.cmax + r * a.nc;
-    unsigned long long list = 0;
-    for (int c0 = w * 32; c0 < a.nc; c0 += 4 * kWarps * 32) {
-        unsigned long long k[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + j * kWarps * 32 + lane;
-            k[j] = c < a.nc ? make_key(cmax[c], c) : 0ull;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            k[j] = sort32(k[j], lane);
-        list = merge32(list, merge32(merge32(k[0], k[1], lane), merge32(k[2], k[3], lane), lane), lane);
-    }
-    const unsigned long long chunks = merge_block(list, sl, lane, w);
-    // Their logits, chunk i by warp i % kWarps. None below the k-th chunk's maximum
-    // is among the k largest; the others are collected and merged 32 at a time.
-    const unsigned long long last = __shfl_sync(0xFFFFFFFFu, chunks, a.k - 1);
-    const unsigned long long least = last >> 32 << 32; // any index
-    list = 0;
-    int n = 0; // logits collected in pend[w]
-    constexpr int kMine = 32 / kWarps; // chunks of a warp at most
-    float v[kMine][8];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const unsigned long long ck = __shfl_sync(0xFFFFFFFFu, chunks, w + i * kWarps);
-        if (w + i * kWarps < a.k && ck != 0) {
-            load_chunk(row, mis, a.V, (int)key_index(ck), lane, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = 0.f; // not used
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const unsigned long long ck = __shfl_sync(0xFFFFFFFFu, chunks, w + i * kWarps);
-        const bool mine = w + i * kWarps < a.k && ck != 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const long long e = (long long)key_index(ck) * kChunk - mis + 4 * lane + (j >> 2) * 128 + (j & 3);
-            const unsigned long long key = mine && e >= 0 && e < a.V ? make_key(v[i][j], (uint32_t)e) : 0ull;
-            const bool in = key != 0 && key >= least;
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            if (in)
-                pend[w][n + __popc(who & ((1u << lane) - 1u))] = key;
-            n += __popc(who);
-        }
-        // At most 31 stay for the next chunk (none after the last).
-#pragma unroll 1
-        while (n >= 32 || (i == kMine - 1 && n > 0)) {
-            const int m = n < 32 ? n : 32;
-            __syncwarp();
-            list = merge32(list, sort32(lane < m ? pend[w][n - m + lane] : 0ull, lane), lane);
-            n -= m;
-            __syncwarp();
-        }
-    }
-    const unsigned long long best = merge_block(list, sl, lane, w);
-    if (w == 0 && lane < a.k) {
-        const float x = key_value(best);
-        const size_t o = r * a.k + lane;
-        if (a.top_id)
-            a.top_id[o] = bad || best == 0 ? -1 : (int32_t)key_index(best);
-        if (a.top_logprob)
-            a.top_logprob[o] = bad ? nan : (best == 0 || x == -INFINITY ? -INFINITY : (x - m) - logs);
+    __syncthreads();
+    if (s_last) {
+        __threadfence();
+        finish_row(a, (size_t)blockIdx.y);
     }
 }
 
 } // namespace
 
-cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s)
+cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int *left, int num_sms,
+                         cudaStream_t s)
 {
     LogprobArgs a = {};
     a.ld = p.ld;
@@ -389,7 +407,7 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
     int occ = known.load(std::memory_order_relaxed);
     cudaError_t e = cudaSuccess;
     if (occ == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, logprob_stream_kernel, kWarps * 32, 0);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, logprob_kernel, kWarps * 32, 0);
         if (e != cudaSuccess)
             return e;
         occ = occ < 1 ? 1 : occ;
@@ -415,7 +433,8 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
     long long rows = (long long)((ws_floats - 4) / per_row); // rows of one pass
     if (rows < 1)
         return cudaErrorNotSupported; // a row's chunk maxima do not fit the scratch
-    rows = rows < 65535 ? rows : 65535;
+    rows = rows < kLogprobRows ? rows : kLogprobRows;
+    a.left = left;
 
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -436,11 +455,7 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, logprob_stream_kernel, a);
-        if (e != cudaSuccess)
-            return e;
-        cfg.gridDim = dim3(n);
-        e = cudaLaunchKernelEx(&cfg, logprob_finish_kernel, a);
+        e = cudaLaunchKernelEx(&cfg, logprob_kernel, a);
         if (e != cudaSuccess)
             return e;
     }
