@@ -23,7 +23,6 @@
 #include "internal.h"
 
 #include <atomic>
-#include <cmath>
 
 namespace w4 {
 
@@ -183,6 +182,17 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
     const float *row = a.x + r * a.ld;
     const int mis = row_mis(row);
 
+    // What the picks need first is asked for before the sums.
+    const float *cmax = a.cmax + r * a.nc;
+    float cm[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = w * 32 + j * kWarps * 32 + lane;
+        cm[j] = a.k > 0 && c < a.nc ? __ldcg(cmax + c) : 0.f;
+    }
+    const int t = threadIdx.x == 0 && a.logprob ? a.targets[r] : -1;
+    const float xt = t >= 0 && t < a.V ? row[t] : 0.f;
+
     // Sums: every warp merges all blocks' parts (lane i: parts i, i + 32, ...) in the same order.
     float m = -INFINITY, s = 0.f, u = 0.f;
     for (int i = lane; i < a.S; i += 32) {
@@ -212,14 +222,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
         if (a.entropy)
             a.entropy[r] = bad ? nan : (none ? 0.f : logs - u / s);
         if (a.logprob) {
-            const int t = a.targets[r];
             float y = 0.f;
             if (t < 0 || t >= a.V) {
                 if (a.status)
                     *a.status = 1;
             } else {
-                const float x = row[t];
-                y = bad ? nan : (x == -INFINITY ? -INFINITY : (x - m) - logs);
+                y = bad ? nan : (xt == -INFINITY ? -INFINITY : (xt - m) - logs);
             }
             a.logprob[r] = y;
         }
@@ -228,14 +236,13 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
         return;
 
     // The k first chunks by (maximum, index): four groups of 32 at a time per warp.
-    const float *cmax = a.cmax + r * a.nc;
     unsigned long long list = 0;
     for (int c0 = w * 32; c0 < a.nc; c0 += 4 * kWarps * 32) {
         unsigned long long k[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = c0 + j * kWarps * 32 + lane;
-            k[j] = c < a.nc ? make_key(__ldcg(cmax + c), c) : 0ull;
+            k[j] = c < a.nc ? make_key(c0 == w * 32 ? cm[j] : __ldcg(cmax + c), c) : 0ull;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -413,22 +420,16 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
         occ = occ < 1 ? 1 : occ;
         known.store(occ, std::memory_order_relaxed);
     }
-    // Blocks per row: as few as fill the GPU, in waves as full as can be (of the
-    // blocks that fit at once, `occ` per SM). Measured for 256 rows of 256003
-    // logits: 3 blocks a row (1.3 waves) 53.4 us, 7 (2.95 waves) 45.9 us.
-    const int most = (a.nc + kWarps - 1) / kWarps; // a chunk per warp at least
+    // Blocks per row: as many as fit at once (`occ` per SM), so that all stream from
+    // the start to the end; for more rows than that, several waves of blocks. Measured
+    // for 256 rows of 256003 logits (no alternatives): 1 block a row 74.7 us, 2 45.1,
+    // 4 46.5, 5 50.9, 7 47.8.
+    const long long most = (a.nc + kWarps - 1) / kWarps; // a chunk per warp at least
     const long long fit = (long long)num_sms * occ;
-    int S = 1;
-    double best = 0.;
-    for (int c = 1; c <= most && (c == 1 || (long long)p.M * (c - 1) < 4 * fit); ++c) {
-        const double waves = (double)p.M * c / (double)fit;
-        const double full = waves < 1. ? waves : waves / std::ceil(waves);
-        if (full > best + 0.02) {
-            best = full;
-            S = c;
-        }
-    }
-    a.S = S;
+    long long S = p.M <= fit ? fit / p.M : (4 * fit + p.M - 1) / p.M;
+    S = S < most ? S : most;
+    S = S < 1 ? 1 : S;
+    a.S = (int)S;
     const size_t per_row = (size_t)a.nc + (size_t)S * 4;
     long long rows = (long long)((ws_floats - 4) / per_row); // rows of one pass
     if (rows < 1)
@@ -450,7 +451,7 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
         a.top_logprob = p.top_logprob ? p.top_logprob + (size_t)r0 * p.k : nullptr;
         a.top_id = p.top_id ? p.top_id + (size_t)r0 * p.k : nullptr;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(S, n);
+        cfg.gridDim = dim3((unsigned)S, n);
         cfg.blockDim = dim3(kWarps * 32);
         cfg.stream = s;
         cfg.attrs = attr;
