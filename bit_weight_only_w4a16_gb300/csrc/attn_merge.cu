@@ -14,13 +14,16 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kMaxCtas = 512;
-constexpr int kMaxRows = 32; // rows per block
+constexpr int kMaxRows = 128; // rows per block
+constexpr int kBatch = 10;    // partials in flight per thread when threads share an item, 4 else
 
 // Block (x, y): the x-th cut row tile, its rows [y rb, y rb + rb). An item is four
 // columns of a row. When a block has fewer items than threads, `groups` threads
 // share an item: each takes every groups-th partial, and their sums are added in
 // the order of the groups.
-__global__ void __launch_bounds__(kThreads)
+// SHARED: such a block (one per SM, many loads per thread); else two blocks per SM.
+template <bool SHARED>
+__global__ void __launch_bounds__(kThreads, SHARED ? 1 : 2)
 merge_kernel(const MergeArgs a)
 {
     extern __shared__ float4 s_part[];  // [groups - 1][items], then weights [partials][rb]
@@ -58,71 +61,133 @@ merge_kernel(const MergeArgs a)
     // Partial p is slot 2 first + 1 for p = 0, else 2 (first + p).
     auto slot = [&](int p) { return p == 0 ? 2 * first + 1 : 2 * (first + p); };
     const int cols = a.DV / 4, items = a.rb * cols;
-    const int groups = items < kThreads ? kThreads / items : 1;
+    const int groups = SHARED ? kThreads / items : 1;
     float *s_w = reinterpret_cast<float *>(s_part + (size_t)(groups - 1) * items);
 
-    // Weights 2^(m_p - M) and the inverse of the sum; one warp per row.
-    for (int r = w; r < a.rb; r += kThreads / 32) {
-        float M = -INFINITY, L = 0.f;
-        for (int p = lane; p < n; p += 32)
-            M = fmaxf(M, a.ws_ml[((size_t)slot(p) * 256 + r0 + r) * 2]);
-        for (int d = 16; d; d >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-        for (int p = lane; p < n; p += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + ((size_t)slot(p) * 256 + r0 + r) * 2);
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            s_w[p * a.rb + r] = f;
-            L += f * ml.y;
+    // Weights 2^(m_p - M) and the inverse of the sum: a thread per row for a short
+    // chain, a warp per row for a long one.
+    auto ml_of = [&](int p, int r) {
+        return __ldcg(reinterpret_cast<const float2 *>(a.ws_ml + ((size_t)slot(p) * 256 + r0 + r) * 2));
+    };
+    if (n <= kBatch) {
+        if ((int)threadIdx.x < a.rb) {
+            float2 ml[kBatch];
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+                ml[p] = p < n ? ml_of(p, threadIdx.x) : make_float2(-INFINITY, 0.f);
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p)
+                M = fmaxf(M, ml[p].x);
+#pragma unroll
+            for (int p = 0; p < kBatch; ++p) {
+                const float f = ml[p].x == -INFINITY ? 0.f : ex2(ml[p].x - M);
+                if (p < n)
+                    s_w[p * a.rb + threadIdx.x] = f;
+                L += f * ml[p].y;
+            }
+            s_inv[threadIdx.x] = L == 0.f ? 0.f : 1.f / L;
         }
-        for (int d = 16; d; d >>= 1)
-            L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
-        if (lane == 0)
-            s_inv[r] = L == 0.f ? 0.f : 1.f / L;
+    } else {
+        for (int r = w; r < a.rb; r += kThreads / 32) {
+            float M = -INFINITY, L = 0.f;
+            float2 ml[kMaxCtas / 32];
+#pragma unroll
+            for (int q = 0; q < kMaxCtas / 32; ++q) {
+                const int p = lane + 32 * q;
+                ml[q] = p < n ? ml_of(p, r) : make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int q = 0; q < kMaxCtas / 32; ++q)
+                M = fmaxf(M, ml[q].x);
+            for (int d = 16; d; d >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+#pragma unroll
+            for (int q = 0; q < kMaxCtas / 32; ++q) {
+                const int p = lane + 32 * q;
+                const float f = ml[q].x == -INFINITY ? 0.f : ex2(ml[q].x - M);
+                if (p < n)
+                    s_w[p * a.rb + r] = f;
+                L += f * ml[q].y;
+            }
+            for (int d = 16; d; d >>= 1)
+                L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+            if (lane == 0)
+                s_inv[r] = L == 0.f ? 0.f : 1.f / L;
+        }
     }
     __syncthreads();
 
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-        const int i = groups > 1 ? (int)threadIdx.x % items : i0 + (int)threadIdx.x;
-        const int grp = groups > 1 ? (int)threadIdx.x / items : 0;
-        const bool mine = i < items && grp < groups;
-        const int rr = i % a.rb, c4 = i / a.rb, row = r0 + rr;
-        const int t = row / kRowsQ, in = row - t * kRowsQ;
+    // Where item i's columns lie in a partial, and its output (null: not a row).
+    auto offset = [&](int i) { return ((size_t)(i / a.rb) * a.rows_per_tile + r0 + i % a.rb) * 4; };
+    auto target = [&](int i) -> uint16_t * {
+        const int row = r0 + i % a.rb, c4 = i / a.rb, t = row / kRowsQ, in = row - t * kRowsQ;
         const int tok = t * a.tpt + in / a.G;
-        const bool live = mine && in / a.G < a.tpt && tok < nt;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) {
-            const size_t off = ((size_t)c4 * a.rows_per_tile + row) * 4;
-#pragma unroll 8
-            for (int p = grp; p < n; p += groups) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (size_t)slot(p) * kSlotFloats + off));
-                const float f = s_w[p * a.rb + rr];
-                o.x = fmaf(x.x, f, o.x);
-                o.y = fmaf(x.y, f, o.y);
-                o.z = fmaf(x.z, f, o.z);
-                o.w = fmaf(x.w, f, o.w);
+        if (i >= items || in / a.G >= a.tpt || tok >= nt)
+            return nullptr;
+        return a.out + (size_t)(tok0 + tok) * a.ldo + (size_t)(kvh * a.G + in % a.G) * a.D + slice * a.DV + 4 * c4;
+    };
+    auto load = [&](int p, size_t off) {
+        return __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (size_t)slot(p) * kSlotFloats + off));
+    };
+    auto add = [&](float4 &o, const float4 &x, float f) {
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+    };
+    auto store = [&](uint16_t *to, const float4 &o, float f) {
+        uint2 y;
+        y.x = pack2(o.x * f, o.y * f);
+        y.y = pack2(o.z * f, o.w * f);
+        *reinterpret_cast<uint2 *>(to) = y;
+    };
+    if (!SHARED) {
+        for (int i = threadIdx.x; i < items; i += kThreads) {
+            uint16_t *to = target(i);
+            if (!to)
+                continue;
+            const size_t off = offset(i);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p0 = 0; p0 < n; p0 += 4) {
+                float4 x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    x[q] = p0 + q < n ? load(p0 + q, off) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    add(o, x[q], p0 + q < n ? s_w[(p0 + q) * a.rb + i % a.rb] : 0.f);
+            }
+            store(to, o, s_inv[i % a.rb]);
+        }
+        return;
+    }
+    const int i = (int)threadIdx.x % items, grp = (int)threadIdx.x / items;
+    uint16_t *to = grp < groups ? target(i) : nullptr;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (to) {
+        const size_t off = offset(i);
+        for (int p0 = grp; p0 < n; p0 += kBatch * groups) {
+            float4 x[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int p = p0 + q * groups;
+                x[q] = p < n ? load(p, off) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int p = p0 + q * groups;
+                add(o, x[q], p < n ? s_w[p * a.rb + i % a.rb] : 0.f);
             }
         }
-        if (groups > 1) {
-            if (mine && grp > 0)
-                s_part[(grp - 1) * items + i] = o;
-            __syncthreads();
-            if (grp == 0)
-                for (int q = 1; q < groups; ++q) {
-                    const float4 x = s_part[(q - 1) * items + i];
-                    o.x += x.x;
-                    o.y += x.y;
-                    o.z += x.z;
-                    o.w += x.w;
-                }
-        }
-        if (live && grp == 0) {
-            const float f = s_inv[rr];
-            uint2 y;
-            y.x = pack2(o.x * f, o.y * f);
-            y.y = pack2(o.z * f, o.w * f);
-            *reinterpret_cast<uint2 *>(a.out + (size_t)(tok0 + tok) * a.ldo +
-                                       (size_t)(kvh * a.G + in % a.G) * a.D + slice * a.DV + 4 * c4) = y;
-        }
+    }
+    if (grp > 0 && grp < groups)
+        s_part[(grp - 1) * items + i] = o;
+    __syncthreads();
+    if (grp == 0 && to) {
+        for (int q = 1; q < groups; ++q)
+            add(o, s_part[(q - 1) * items + i], 1.f);
+        store(to, o, s_inv[i % a.rb]);
     }
 }
 
@@ -134,23 +199,43 @@ cudaError_t run_merge(const MergeArgs &m0, int tiles, cudaStream_t s)
     static_assert(kMaxCtas <= kThreads, "one thread per CTA");
     if (m.ctas > kMaxCtas)
         return cudaErrorInvalidValue;
-    // Rows per block: about four blocks per SM if every tile is cut; two at least
-    // (32 contiguous bytes of a partial).
+    // Rows per block: about one block per SM if every tile is cut (finding the tile
+    // and its partials takes a block 2 us); two rows at least (32 contiguous bytes of a
+    // partial).
     m.rb = 2;
-    while (m.rb < kMaxRows && (long long)tiles * (m.rows_per_tile / m.rb) > 4 * m.ctas)
+    while (m.rb < kMaxRows && (long long)tiles * (m.rows_per_tile / m.rb) > m.ctas)
         m.rb <<= 1;
     const int items = m.rb * (m.DV / 4), groups = items < kThreads ? kThreads / items : 1;
+    const size_t smem = (size_t)(groups - 1) * items * sizeof(float4) + (size_t)m.ctas * m.rb * sizeof(float);
+    // Once per device: up to kMaxRows weights for each CTA's partial.
+    static std::atomic<unsigned long long> set{0};
+    constexpr int kSmem = 16 * kThreads + 4 * kMaxRows * 256; // 136 KiB: 256 partials of 128 rows
+    if (smem > (size_t)kSmem)
+        return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !((set.load(std::memory_order_relaxed) >> dev) & 1)) {
+        e = cudaFuncSetAttribute(merge_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(merge_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles, m.rows_per_tile / m.rb);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)(groups - 1) * items * sizeof(float4) + (size_t)m.ctas * m.rb * sizeof(float);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel, m);
+    return groups > 1 ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, m) : cudaLaunchKernelEx(&cfg, merge_kernel<false>, m);
 }
 
 } // namespace attn

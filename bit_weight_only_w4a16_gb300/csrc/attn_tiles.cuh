@@ -246,6 +246,11 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
                  "r"(addr)                                                                                       \
                  : "memory")
 
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -611,6 +616,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    if (threadIdx.x == 32) {
+        const CUtensorMap *m = &maps.q;
+        for (int i = 0; i < (TREE ? 5 : 3); ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(m + i) : "memory");
+    }
     pdl_launch_dependents();
     pdl_wait();
 
@@ -956,39 +966,37 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h) {
                         const uint32_t mine = (cls >> (2 * h)) & 3u;
-                        uint32_t todo = __ballot_sync(0xFFFFFFFFu, mine != 0);
+                        const uint32_t some = __ballot_sync(0xFFFFFFFFu, mine == 1);
                         const uint32_t none = __ballot_sync(0xFFFFFFFFu, mine == 2);
                         // Four rows at a time, eight lanes of 16 bytes each per 64 dims.
+#pragma unroll 1
                         for (int r4 = 0; r4 < 32; r4 += 4) {
-                            if (!((todo >> r4) & 0xFu))
-                                continue;
                             const int rr = r4 + (lane >> 3);
-                            if ((todo >> rr) & 1u) {
-                                for (int b = 0; b < S::DV / 64; ++b) {
-                                    const uint32_t p = vb + b * (S::VKEYS * 128) + (32 * h + rr) * 128 + (lane & 7) * 16;
-                                    uint4 v = make_uint4(0, 0, 0, 0);
-                                    if (!((none >> rr) & 1u)) {
-                                        v = lds128(p);
-                                        uint32_t *e = reinterpret_cast<uint32_t *>(&v);
-                                        bool bad = false;
+                            const uint32_t p = vb + (32 * h + rr) * 128 + (lane & 7) * 16;
+                            if ((none >> rr) & 1u) {
 #pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            if ((e[i] & 0x7F80u) == 0x7F80u) {
-                                                e[i] &= 0xFFFF0000u;
-                                                bad = true;
-                                            }
-                                            if ((e[i] & 0x7F800000u) == 0x7F800000u) {
-                                                e[i] &= 0x0000FFFFu;
-                                                bad = true;
-                                            }
-                                        }
-                                        if (!bad)
-                                            continue;
-                                        found = true;
+                                for (int b = 0; b < S::DV / 64; ++b)
+                                    sts128(p + b * (S::VKEYS * 128), make_uint4(0, 0, 0, 0));
+                            } else if ((some >> rr) & 1u) {
+                                uint4 v[S::DV / 64];
+#pragma unroll
+                                for (int b = 0; b < S::DV / 64; ++b)
+                                    v[b] = lds128(p + b * (S::VKEYS * 128));
+#pragma unroll
+                                for (int b = 0; b < S::DV / 64; ++b) {
+                                    uint32_t *e = reinterpret_cast<uint32_t *>(&v[b]);
+                                    bool bad = false;
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const bool lo = (e[i] & 0x7F80u) == 0x7F80u;
+                                        const bool hi = (e[i] & 0x7F800000u) == 0x7F800000u;
+                                        e[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                                        bad = bad || lo || hi;
                                     }
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x),
-                                                 "r"(v.y), "r"(v.z), "r"(v.w)
-                                                 : "memory");
+                                    if (bad) {
+                                        found = true;
+                                        sts128(p + b * (S::VKEYS * 128), v[b]);
+                                    }
                                 }
                             }
                         }
