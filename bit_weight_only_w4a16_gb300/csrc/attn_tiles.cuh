@@ -661,12 +661,19 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             key_range<TREE>(a, q, t0, min(tt, q.lq - t0), lo, hi);
             return tile_units<TREE>(lo, hi);
         };
+        // Thread r of the last round of row tiles: its tile's sequence, units, cost and
+        // the costs up to it. With one round they serve the second pass as well.
+        int s_r = 0, n_r = 0, cost_r = 0, incl_r = 0, total_r = 0;
+        auto round = [&](int r0) {
+            const int r = r0 + (int)threadIdx.x;
+            n_r = r < R ? units_of(r, s_r) : 0;
+            cost_r = n_r > 0 ? n_r + extra : 0;
+            incl_r = block_scan<S::THREADS>(cost_r, sh.warp_sums, total_r);
+        };
         long long W = 0;
         for (int r0 = 0; r0 < R; r0 += S::THREADS) {
-            const int r = r0 + (int)threadIdx.x;
-            int total, s;
-            block_scan<S::THREADS>(r < R ? units_of(r, s) + extra : 0, sh.warp_sums, total);
-            W += total;
+            round(r0);
+            W += total_r;
         }
         const long long all = W * HS;
         long long at[2];
@@ -684,21 +691,21 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         }
         long long before = 0;
         for (int r0 = 0; r0 < R; r0 += S::THREADS) {
+            if (R > S::THREADS)
+                round(r0);
+            else
+                __syncthreads(); // after the defaults above
             const int r = r0 + (int)threadIdx.x;
-            int total, s = 0;
-            const int n = r < R ? units_of(r, s) : 0;
-            const int cost = n > 0 ? n + extra : 0;
-            const int incl = block_scan<S::THREADS>(cost, sh.warp_sums, total);
-            const long long p = before + incl - cost;
+            const long long p = before + incl_r - cost_r;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (cost > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost) {
+                if (cost_r > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost_r) {
                     sh.cut[e][0] = hs[e] * R + r;
-                    sh.cut[e][1] = s;
-                    sh.cut[e][2] = r - sbase[s];
+                    sh.cut[e][1] = s_r;
+                    sh.cut[e][2] = r - sbase[s_r];
                     sh.cut[e][3] = (int)max(0ll, at[e] - p - extra);
                 }
-            before += total;
+            before += total_r;
             if (max(at[0], at[1]) < before)
                 break;
         }
