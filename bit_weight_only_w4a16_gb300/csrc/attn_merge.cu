@@ -64,6 +64,42 @@ merge_kernel(const MergeArgs a)
     const int groups = SHARED ? kThreads / items : 1;
     float *s_w = reinterpret_cast<float *>(s_part + (size_t)(groups - 1) * items);
 
+    // Where item i's columns lie in a partial, and its output (null: not a row).
+    auto offset = [&](int i) { return ((size_t)(i / a.rb) * a.rows_per_tile + r0 + i % a.rb) * 4; };
+    auto target = [&](int i) -> uint16_t * {
+        const int row = r0 + i % a.rb, c4 = i / a.rb, t = row / kRowsQ, in = row - t * kRowsQ;
+        const int tok = t * a.tpt + in / a.G;
+        if (i >= items || in / a.G >= a.tpt || tok >= nt)
+            return nullptr;
+        return a.out + (size_t)(tok0 + tok) * a.ldo + (size_t)(kvh * a.G + in % a.G) * a.D + slice * a.DV + 4 * c4;
+    };
+    auto load = [&](int p, size_t off) {
+        return __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (size_t)slot(p) * kSlotFloats + off));
+    };
+    auto add = [&](float4 &o, const float4 &x, float f) {
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+    };
+    auto store = [&](uint16_t *to, const float4 &o, float f) {
+        uint2 y;
+        y.x = pack2(o.x * f, o.y * f);
+        y.y = pack2(o.z * f, o.w * f);
+        *reinterpret_cast<uint2 *>(to) = y;
+    };
+    // Threads that share items ask for their first partials before the weights.
+    const int i = SHARED ? (int)threadIdx.x % items : 0, grp = SHARED ? (int)threadIdx.x / items : 0;
+    uint16_t *to0 = SHARED && grp < groups ? target(i) : nullptr;
+    const size_t off0 = offset(i);
+    float4 x0[SHARED ? kBatch : 1];
+    if (SHARED) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int p = grp + q * groups;
+            x0[q] = to0 && p < n ? load(p, off0) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
     // Weights 2^(m_p - M) and the inverse of the sum: a thread per row for a short
     // chain, a warp per row for a long one.
     auto ml_of = [&](int p, int r) {
@@ -118,30 +154,6 @@ merge_kernel(const MergeArgs a)
     }
     __syncthreads();
 
-    // Where item i's columns lie in a partial, and its output (null: not a row).
-    auto offset = [&](int i) { return ((size_t)(i / a.rb) * a.rows_per_tile + r0 + i % a.rb) * 4; };
-    auto target = [&](int i) -> uint16_t * {
-        const int row = r0 + i % a.rb, c4 = i / a.rb, t = row / kRowsQ, in = row - t * kRowsQ;
-        const int tok = t * a.tpt + in / a.G;
-        if (i >= items || in / a.G >= a.tpt || tok >= nt)
-            return nullptr;
-        return a.out + (size_t)(tok0 + tok) * a.ldo + (size_t)(kvh * a.G + in % a.G) * a.D + slice * a.DV + 4 * c4;
-    };
-    auto load = [&](int p, size_t off) {
-        return __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (size_t)slot(p) * kSlotFloats + off));
-    };
-    auto add = [&](float4 &o, const float4 &x, float f) {
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
-    };
-    auto store = [&](uint16_t *to, const float4 &o, float f) {
-        uint2 y;
-        y.x = pack2(o.x * f, o.y * f);
-        y.y = pack2(o.z * f, o.w * f);
-        *reinterpret_cast<uint2 *>(to) = y;
-    };
     if (!SHARED) {
         for (int i = threadIdx.x; i < items; i += kThreads) {
             uint16_t *to = target(i);
@@ -162,17 +174,17 @@ merge_kernel(const MergeArgs a)
         }
         return;
     }
-    const int i = (int)threadIdx.x % items, grp = (int)threadIdx.x / items;
-    uint16_t *to = grp < groups ? target(i) : nullptr;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (to) {
-        const size_t off = offset(i);
+    if (to0) {
         for (int p0 = grp; p0 < n; p0 += kBatch * groups) {
             float4 x[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
                 const int p = p0 + q * groups;
-                x[q] = p < n ? load(p, off) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p0 == grp)
+                    x[q] = x0[q];
+                else
+                    x[q] = p < n ? load(p, off0) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
@@ -184,10 +196,10 @@ merge_kernel(const MergeArgs a)
     if (grp > 0 && grp < groups)
         s_part[(grp - 1) * items + i] = o;
     __syncthreads();
-    if (grp == 0 && to) {
+    if (grp == 0 && to0) {
         for (int q = 1; q < groups; ++q)
             add(o, s_part[(q - 1) * items + i], 1.f);
-        store(to, o, s_inv[i % a.rb]);
+        store(to0, o, s_inv[i % a.rb]);
     }
 }
 

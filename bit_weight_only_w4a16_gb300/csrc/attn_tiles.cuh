@@ -372,16 +372,19 @@ __device__ __forceinline__ bool edge_unit(const Args &a, const Piece &w, int x)
     return a.window > 0 && k < w.off + w.t0 + w.nt - a.window; // before the last row's first key
 }
 
-// A value row's part in the product: 0 = kept by every row, 1 = by some, 2 = by none.
+// A value row's part in the product: 0 = kept by every row (or zeros already), 1 = by
+// some, 2 = by none.
 template <bool TREE>
 __device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, int j)
 {
     if (TREE) {
+        // Rows past the last sequence's are past the tensor: copied as zeros.
+        const int past = w.s == a.B - 1 ? 0 : 2;
         if (tree_unit<TREE>(w, x))
-            return j < a.N ? 1 : 2;
+            return j < a.N ? 1 : past;
         const int k = key0(w, x) + j;
         if (k >= a.T)
-            return 2;
+            return past;
         const int p = a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
         if (p < 0 || p >= w.off)
             return 2;
@@ -569,6 +572,91 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
     return x + before;
 }
 
+// Cuts the call's row tiles, in order of (head and slice, sequence, token), with their
+// units and TILE_COST each, at equal costs: sh.cut[e] is where this CTA's run begins
+// (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within the
+// sequence, unit. sbase: space for the first row tile of each sequence.
+template <typename S, bool TREE>
+__device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, int tt, int HS, int &R)
+{
+    for (int s0 = 0; s0 < a.B; s0 += S::THREADS) {
+        const int s = s0 + (int)threadIdx.x;
+        const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
+        int total;
+        const int incl = block_scan<S::THREADS>(nt, sh.warp_sums, total);
+        if (s < a.B)
+            sbase[s] = R + incl - nt;
+        R += total;
+    }
+    __syncthreads();
+    const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
+    auto units_of = [&](int r, int &s) {
+        // The last sequence that begins at or before r (empty ones begin where the next does).
+        int x = 0, y = a.B - 1;
+        while (x < y) {
+            const int m = (x + y + 1) >> 1;
+            if (sbase[m] <= r)
+                x = m;
+            else
+                y = m - 1;
+        }
+        s = x;
+        const Seq q = load_seq<TREE>(a, s);
+        const int t0 = (r - sbase[s]) * tt;
+        int lo, hi;
+        key_range<TREE>(a, q, t0, min(tt, q.lq - t0), lo, hi);
+        return tile_units<TREE>(lo, hi);
+    };
+    // Thread r of the last round of row tiles: its tile's sequence, units, cost and
+    // the costs up to it. With one round they serve the second pass as well.
+    int s_r = 0, n_r = 0, cost_r = 0, incl_r = 0, total_r = 0;
+    auto round = [&](int r0) {
+        const int r = r0 + (int)threadIdx.x;
+        n_r = r < R ? units_of(r, s_r) : 0;
+        cost_r = n_r > 0 ? n_r + extra : 0;
+        incl_r = block_scan<S::THREADS>(cost_r, sh.warp_sums, total_r);
+    };
+    long long W = 0;
+    for (int r0 = 0; r0 < R; r0 += S::THREADS) {
+        round(r0);
+        W += total_r;
+    }
+    const long long all = W * HS;
+    long long at[2];
+    int hs[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const long long ctas = max(1ll, min((long long)gridDim.x, all)); // a unit each at least
+        const long long x = all * min((long long)blockIdx.x + e, ctas) / ctas;
+        hs[e] = W > 0 ? (int)(x / W) : 0;
+        at[e] = x - hs[e] * W;
+    }
+    if (threadIdx.x < 2) { // the end of the last run, until a tile claims the place
+        sh.cut[threadIdx.x][0] = HS * R;
+        sh.cut[threadIdx.x][3] = 0;
+    }
+    long long before = 0;
+    for (int r0 = 0; r0 < R; r0 += S::THREADS) {
+        if (R > S::THREADS)
+            round(r0);
+        else
+            __syncthreads(); // after the defaults above
+        const int r = r0 + (int)threadIdx.x;
+        const long long p = before + incl_r - cost_r;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (cost_r > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost_r) {
+                sh.cut[e][0] = hs[e] * R + r;
+                sh.cut[e][1] = s_r;
+                sh.cut[e][2] = r - sbase[s_r];
+                sh.cut[e][3] = (int)max(0ll, at[e] - p - extra);
+            }
+        before += total_r;
+        if (max(at[0], at[1]) < before)
+            break;
+    }
+}
+
 template <int D, bool TREE>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
 attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
@@ -625,89 +713,28 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     pdl_wait();
 
     // -------------------------------------------------- this CTA's run
-    // Row tiles in order of (head and slice, sequence, token), with their units
-    // and TILE_COST each, cut at equal costs: sh.cut[e] is where the run begins
-    // (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within
-    // the sequence, unit.
     {
         const int tt = a.tpt * S::TQ, HS = a.Hkv * S::NV;
-        int *sbase = reinterpret_cast<int *>(smem); // first row tile of each sequence
-        int R = 0;
-        for (int s0 = 0; s0 < a.B; s0 += S::THREADS) {
-            const int s = s0 + (int)threadIdx.x;
-            const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
-            int total;
-            const int incl = block_scan<S::THREADS>(nt, sh.warp_sums, total);
-            if (s < a.B)
-                sbase[s] = R + incl - nt;
-            R += total;
-        }
-        __syncthreads();
-        const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
-        auto units_of = [&](int r, int &s) {
-            // The last sequence that begins at or before r (empty ones begin where the next does).
-            int x = 0, y = a.B - 1;
-            while (x < y) {
-                const int m = (x + y + 1) >> 1;
-                if (sbase[m] <= r)
-                    x = m;
-                else
-                    y = m - 1;
+        int R = 0; // row tiles of a head
+        if (TREE && a.B == 1) {
+            // One tree: its row tiles have the same units.
+            if (threadIdx.x < 2) {
+                const Seq q = load_seq<TREE>(a, 0);
+                int lo, hi;
+                key_range<TREE>(a, q, 0, q.lq, lo, hi);
+                R = (q.lq + tt - 1) / tt;
+                const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
+                const long long cost = tile_units<TREE>(lo, hi) + extra, all = cost * R * HS;
+                const long long ctas = min((long long)gridDim.x, all); // a unit each at least
+                const long long x = all * min((long long)blockIdx.x + threadIdx.x, ctas) / ctas;
+                const int tile = (int)(x / cost);
+                sh.cut[threadIdx.x][0] = tile;
+                sh.cut[threadIdx.x][1] = 0;
+                sh.cut[threadIdx.x][2] = tile % R;
+                sh.cut[threadIdx.x][3] = (int)max(0ll, x - tile * cost - extra);
             }
-            s = x;
-            const Seq q = load_seq<TREE>(a, s);
-            const int t0 = (r - sbase[s]) * tt;
-            int lo, hi;
-            key_range<TREE>(a, q, t0, min(tt, q.lq - t0), lo, hi);
-            return tile_units<TREE>(lo, hi);
-        };
-        // Thread r of the last round of row tiles: its tile's sequence, units, cost and
-        // the costs up to it. With one round they serve the second pass as well.
-        int s_r = 0, n_r = 0, cost_r = 0, incl_r = 0, total_r = 0;
-        auto round = [&](int r0) {
-            const int r = r0 + (int)threadIdx.x;
-            n_r = r < R ? units_of(r, s_r) : 0;
-            cost_r = n_r > 0 ? n_r + extra : 0;
-            incl_r = block_scan<S::THREADS>(cost_r, sh.warp_sums, total_r);
-        };
-        long long W = 0;
-        for (int r0 = 0; r0 < R; r0 += S::THREADS) {
-            round(r0);
-            W += total_r;
-        }
-        const long long all = W * HS;
-        long long at[2];
-        int hs[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const long long ctas = max(1ll, min((long long)gridDim.x, all)); // a unit each at least
-            const long long x = all * min((long long)blockIdx.x + e, ctas) / ctas;
-            hs[e] = W > 0 ? (int)(x / W) : 0;
-            at[e] = x - hs[e] * W;
-        }
-        if (threadIdx.x < 2) { // the end of the last run, until a tile claims the place
-            sh.cut[threadIdx.x][0] = HS * R;
-            sh.cut[threadIdx.x][3] = 0;
-        }
-        long long before = 0;
-        for (int r0 = 0; r0 < R; r0 += S::THREADS) {
-            if (R > S::THREADS)
-                round(r0);
-            else
-                __syncthreads(); // after the defaults above
-            const int r = r0 + (int)threadIdx.x;
-            const long long p = before + incl_r - cost_r;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (cost_r > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost_r) {
-                    sh.cut[e][0] = hs[e] * R + r;
-                    sh.cut[e][1] = s_r;
-                    sh.cut[e][2] = r - sbase[s_r];
-                    sh.cut[e][3] = (int)max(0ll, at[e] - p - extra);
-                }
-            before += total_r;
-            if (max(at[0], at[1]) < before)
-                break;
+        } else {
+            plan_run<S, TREE>(a, sh, reinterpret_cast<int *>(smem), tt, HS, R);
         }
         if (threadIdx.x == 0)
             sh.tiles = R;
@@ -978,6 +1005,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         // Four rows at a time, eight lanes of 16 bytes each per 64 dims.
 #pragma unroll 1
                         for (int r4 = 0; r4 < 32; r4 += 4) {
+                            if ((((some | none) >> r4) & 0xFu) == 0)
+                                continue;
                             const int rr = r4 + (lane >> 3);
                             const uint32_t p = vb + (32 * h + rr) * 128 + (lane & 7) * 16;
                             if ((none >> rr) & 1u) {
