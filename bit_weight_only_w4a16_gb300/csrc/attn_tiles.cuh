@@ -436,7 +436,7 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int t
             p = __ldg(par + j);
         }
         m.hi = a.kpos ? w.off : w.lk;
-        m.lo = a.window > 0 ? (int)max(0ll, (long long)w.off + d - a.window + 1) : 0;
+        m.lo = a.window > 0 ? (int)min(0x7FFFFFFFll, max(0ll, (long long)w.off + d - a.window + 1)) : 0;
     } else {
         const int at = w.off + w.t0 + tok;
         m.hi = min(at + 1, w.lk);
@@ -488,7 +488,7 @@ __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, cons
 struct Bars {
     unsigned long long full[kMaxSlots], edge[kMaxSlots], empty[kMaxSlots];
     unsigned long long q_full, q_empty;
-    unsigned long long s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    unsigned long long s_full[2], p_full[2], o_done[2], o_last[2], o_free[2], drain;
     unsigned long long pc_full[kPieces], pc_empty[kPieces];
 };
 
@@ -686,7 +686,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bars.s_full[i]), 1);
             mbar_init(smem_addr(&bars.p_full[i]), S::ROW_WARPS);
-            mbar_init(smem_addr(&bars.o_done[i]), 1);
+            mbar_init(smem_addr(&bars.o_done[i]), 1); // a unit's product
+            mbar_init(smem_addr(&bars.o_last[i]), 1); // a piece's last one
             mbar_init(smem_addr(&bars.o_free[i]), S::ROW_WARPS);
         }
         for (int i = 0; i < kPieces; ++i) {
@@ -904,6 +905,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 return true;
             };
             auto nothing = [] { return true; };
+            auto finished = [&](int t, bool more) {
+                if (!more)
+                    mma_commit(smem_addr(&bars.o_last[t]));
+                return true;
+            };
             uint32_t n = 0, n1 = 0;        // units so far, of the second row tile
             uint32_t mine = 0, mine1 = 0;  // pieces so far, with a second row tile
             bool ok = true;
@@ -932,6 +938,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             mma_commit(smem_addr(&bars.q_empty));
                         ok = ok && product(0, b, g, j > 0 ? 1u : 0u, true, true,
                                            [&] { return j + 2 >= units || ready(g + S::VC); });
+                        if (j + 1 == units)
+                            mma_commit(smem_addr(&bars.o_last[0]));
                         g += S::VC;
                     }
                 } else {
@@ -948,9 +956,12 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                         auto second = [&] { return !two || weights_in(1, 1, n1, j == 0, mine1); };
                         ok = ready(g) && weights_in(0, 0, n, j == 0, mine) &&
                              product(0, 0, g, acc, true, !two, [&] { return more ? ready(g + S::VC) : second(); }) &&
+                             finished(0, more) &&
                              (!more || scores(0, 0, g + S::VC, true, !two, second)) &&
                              (!two || (product(1, 1, g, acc, false, true, nothing) &&
                                        (!more || scores(1, 1, g + S::VC, false, true, nothing))));
+                        if (!more && two)
+                            mma_commit(smem_addr(&bars.o_last[1]));
                         g += S::VC + (more ? S::KC : 0);
                         n1 += two ? 1u : 0u;
                     }
@@ -1058,7 +1069,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const int tok_in = row / a.G, head = row - tok_in * a.G;
         constexpr int OC = S::PAIR ? S::DV / 2 : S::DV; // accumulator columns of this thread
-        uint32_t it = 0, piece = 0; // units of this row tile; pieces of the run
+        uint32_t it = 0, mine = 0, piece = 0; // units, pieces of this row tile; pieces of the run
         uint32_t xs = 0;            // exchanges so far
         bool ok = true;
         // The row's two threads exchange a value, and whether their waits ended well:
@@ -1184,7 +1195,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     m = mt;
                 }
                 if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-                    // O holds the units before this one: wait for their product.
+                    // O holds the units before this one: wait for their product. (The last
+                    // one's phase is told apart: these scores were issued after the
+                    // product before it, and this unit's product waits for its weights.)
                     ok = __all_sync(0xFFFFFFFFu, wait(bars.o_done[t], (it - 1) & 1));
                     if (!S::PAIR && !ok)
                         break;
@@ -1239,10 +1252,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             if (!S::PAIR && !ok)
                 break;
             // ------------------------------------------------- epilogue
-            // With two score buffers the last scores say nothing of the product before
-            // last, and a parity wait tells only neighbouring phases apart.
-            ok = ok && __all_sync(0xFFFFFFFFu, (!S::PAIR || units < 2 || wait(bars.o_done[t], it & 1)) &&
-                                                   wait(bars.o_done[t], (it - 1) & 1));
+            ok = ok && __all_sync(0xFFFFFFFFu, wait(bars.o_last[t], mine & 1));
+            ++mine;
             if (S::PAIR)
                 l += exchange(l);
             if (!ok)

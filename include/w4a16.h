@@ -58,8 +58,8 @@ const char *w4_last_cuda_error(void);
 
 /*
  * Set up the library on the current device: checks that it is sm_103 and
- * allocates the library-owned device scratch (4 MB of argmax keys and one
- * error word, held until process exit). Idempotent and thread-safe. Call it
+ * allocates the library-owned device scratch (4 MB of argmax keys, one error word
+ * and about 40 MB of split partials, held until process exit). Idempotent and thread-safe. Call it
  * before capturing any call of this library in a CUDA graph; otherwise the
  * first call on a device does it.
  */
@@ -70,7 +70,7 @@ int w4_init(void);
  * cudaDeviceSynchronize. *code is 0 when every kernel finished normally. A set
  * bit means that a kernel's bounded wait on its own shared-memory pipeline ran
  * out: bit 0 the streaming decode kernel, bit 1 the prefill GEMM, bit 2 the
- * self-test below. That kernel then returned without hanging; its outputs are
+ * self-test below, bit 3 the prompt and tree attention. That kernel then returned without hanging; its outputs are
  * not valid, and the context stays usable.
  */
 int w4_device_error(int32_t *code);
