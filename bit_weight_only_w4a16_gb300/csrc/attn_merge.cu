@@ -4,7 +4,10 @@
 // of them, an accumulator O_p (fp32), a reference m_p and a sum l_p per row:
 //   out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),  M = max_p m_p,
 // added in the order of the keys. Reads 4 DV bytes per row and partial, written
-// shortly before by the attention kernel: they come from L2.
+// shortly before by the attention kernel. 150 cut tiles of two partials each (39 MB)
+// take 15 us, 152 partials of two tiles (20 MB) 13 us: finding a block's tile and its
+// partials costs 2 us, so blocks are few and take many rows; a long chain is shared
+// among threads instead.
 #include "attn_launch.cuh"
 
 namespace w4 {
@@ -65,13 +68,15 @@ merge_kernel(const MergeArgs a)
     float *s_w = reinterpret_cast<float *>(s_part + (size_t)(groups - 1) * items);
 
     // Where item i's columns lie in a partial, and its output (null: not a row).
-    auto offset = [&](int i) { return ((size_t)(i / a.rb) * a.rows_per_tile + r0 + i % a.rb) * 4; };
+    const int rmask = a.rb - 1, rshift = __ffs(a.rb) - 1; // rb is a power of two
+    auto offset = [&](int i) { return ((size_t)(i >> rshift) * a.rows_per_tile + r0 + (i & rmask)) * 4; };
     auto target = [&](int i) -> uint16_t * {
-        const int row = r0 + i % a.rb, c4 = i / a.rb, t = row / kRowsQ, in = row - t * kRowsQ;
-        const int tok = t * a.tpt + in / a.G;
-        if (i >= items || in / a.G >= a.tpt || tok >= nt)
+        const int row = r0 + (i & rmask), t = row / kRowsQ, in = row - t * kRowsQ;
+        const int ti = in / a.G, tok = t * a.tpt + ti;
+        if (i >= items || ti >= a.tpt || tok >= nt)
             return nullptr;
-        return a.out + (size_t)(tok0 + tok) * a.ldo + (size_t)(kvh * a.G + in % a.G) * a.D + slice * a.DV + 4 * c4;
+        return a.out + (size_t)(tok0 + tok) * a.ldo + (size_t)(kvh * a.G + in - ti * a.G) * a.D + slice * a.DV +
+               4 * (i >> rshift);
     };
     auto load = [&](int p, size_t off) {
         return __ldcg(reinterpret_cast<const float4 *>(a.ws_o + (size_t)slot(p) * kSlotFloats + off));
@@ -168,9 +173,9 @@ merge_kernel(const MergeArgs a)
                     x[q] = p0 + q < n ? load(p0 + q, off) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    add(o, x[q], p0 + q < n ? s_w[(p0 + q) * a.rb + i % a.rb] : 0.f);
+                    add(o, x[q], p0 + q < n ? s_w[(p0 + q) * a.rb + (i & rmask)] : 0.f);
             }
-            store(to, o, s_inv[i % a.rb]);
+            store(to, o, s_inv[i & rmask]);
         }
         return;
     }
@@ -189,7 +194,7 @@ merge_kernel(const MergeArgs a)
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
                 const int p = p0 + q * groups;
-                add(o, x[q], p < n ? s_w[p * a.rb + i % a.rb] : 0.f);
+                add(o, x[q], p < n ? s_w[p * a.rb + (i & rmask)] : 0.f);
             }
         }
     }
@@ -199,7 +204,7 @@ merge_kernel(const MergeArgs a)
     if (grp == 0 && to0) {
         for (int q = 1; q < groups; ++q)
             add(o, s_part[(q - 1) * items + i], 1.f);
-        store(to0, o, s_inv[i % a.rb]);
+        store(to0, o, s_inv[i & rmask]);
     }
 }
 

@@ -8,7 +8,9 @@
 // Row path[j] of a sequence's tree goes to position pos + j: 4 W bytes read and
 // 4 W written per token and layer, a few hundred kilobytes over all layers, so the
 // call is bound by its launch and two dependent reads (count, path). One block
-// per layer, sequence and cache (keys, values); thread = 16 bytes.
+// per layer, sequence and cache (keys, values); thread = 16 bytes, four in flight.
+// 28 layers, 4 tokens of 512 bytes: 4 us on the GPU with cold caches, a call 7.6 us
+// (host time).
 #include "common.cuh"
 #include "internal.h"
 

@@ -18,7 +18,10 @@
 // it. The block that finishes a row last picks those chunks and looks at them
 // alone, while other rows' blocks still stream.
 //
-// Bound by the read of the logits: 4 V bytes a row.
+// Bound by the read of the logits: 4 V bytes a row. 256 rows of 256003 logits (262 MB)
+// take 55 us with 5 alternatives, 45 us (5.8 TB/s) without: the picks of the rows that
+// finish last are not hidden. One row of 262144: 5 us on the GPU, less than the call's
+// host time.
 #include "common.cuh"
 #include "internal.h"
 
