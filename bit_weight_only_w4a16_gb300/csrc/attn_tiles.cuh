@@ -414,6 +414,8 @@ __device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, i
         return 0;
     }
     const int k = key0(w, x) + j;
+    if (k >= a.total_k - w.k0)
+        return 0; // past the tensor
     if (k >= w.hi || k < w.lo)
         return 2;
     if (k > w.off + w.t0)
@@ -596,7 +598,12 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
 template <typename S, bool TREE>
 __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, int tt, int HS, int &R)
 {
-    for (int s0 = 0; s0 < a.B; s0 += S::THREADS) {
+    if (a.B == 1) {
+        R = (load_seq<TREE>(a, 0).lq + tt - 1) / tt;
+        if (threadIdx.x == 0)
+            sbase[0] = 0;
+    }
+    for (int s0 = 0; a.B > 1 && s0 < a.B; s0 += S::THREADS) {
         const int s = s0 + (int)threadIdx.x;
         const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
         int total;
@@ -1296,7 +1303,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             8 * (lane & 3);
                     live[i] = __shfl_sync(0xFFFFFFFFu, (int)rm.live, src) != 0;
                 }
-#pragma unroll 1
+#pragma unroll 2
                 for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                     uint32_t o[32];
                     W4_TLD32(o, o_col(t) + lanes + c0);

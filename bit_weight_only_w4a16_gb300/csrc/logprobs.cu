@@ -196,27 +196,33 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
     const int t = threadIdx.x == 0 && a.logprob ? a.targets[r] : -1;
     const float xt = t >= 0 && t < a.V ? row[t] : 0.f;
 
-    // Sums: every warp merges all blocks' parts (lane i: parts i, i + 32, ...) in the same order.
+    // Sums: thread i has parts i, i + 256, ...; lanes, then warps are merged in order.
     float m = -INFINITY, s = 0.f, u = 0.f;
-    for (int i = lane; i < a.S; i += 32) {
+    for (int i = threadIdx.x; i < a.S; i += kWarps * 32) {
         const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part + (r * a.S + i) * 4));
         merge_stats(m, s, u, p.x, p.y, p.z);
     }
+    if (a.S > 1) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d),
-                    u2 = __shfl_xor_sync(0xFFFFFFFFu, u, d);
-        // the lower lane's part first: both lanes form the same sums
-        if (lane & d) {
-            float mm = m2, s1 = s2, u1 = u2;
-            merge_stats(mm, s1, u1, m, s, u);
-            m = mm;
-            s = s1;
-            u = u1;
-        } else {
-            merge_stats(m, s, u, m2, s2, u2);
+        for (int d = 1; d < 32; d <<= 1) {
+            const float m2 = __shfl_down_sync(0xFFFFFFFFu, m, d), s2 = __shfl_down_sync(0xFFFFFFFFu, s, d),
+                        u2 = __shfl_down_sync(0xFFFFFFFFu, u, d);
+            if (lane + d < 32)
+                merge_stats(m, s, u, m2, s2, u2);
         }
     }
+    __shared__ float sm[kWarps], ss[kWarps], su[kWarps];
+    if (lane == 0) {
+        sm[w] = m;
+        ss[w] = s;
+        su[w] = u;
+    }
+    __syncthreads();
+    m = sm[0];
+    s = ss[0];
+    u = su[0];
+    for (int i = 1; i < kWarps && i * 32 < a.S; ++i)
+        merge_stats(m, s, u, sm[i], ss[i], su[i]);
     const float nan = __uint_as_float(0x7FFFFFFFu);
     const bool bad = s != s;            // a NaN or +inf among the logits
     const bool none = m == -INFINITY;   // every logit is -inf
