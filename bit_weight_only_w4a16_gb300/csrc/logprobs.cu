@@ -201,7 +201,8 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
 {
     constexpr int kThreads = kWarps * 32, kScan = 4; // chunk maxima of a thread at a time
     __shared__ unsigned long long sl[kWarps][32], pend[kWarps][kChunk + 32];
-    __shared__ int cand[32 * kScan], ncand;
+    __shared__ unsigned long long pool[kWarps * 64];
+    __shared__ int cand[32 * kScan], ncand, npool;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const float *row = a.x + r * a.ld;
     const int mis = row_mis(row);
@@ -271,19 +272,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
     const unsigned long long bound = __shfl_sync(0xFFFFFFFFu, firsts, a.k - 1); // 0: fewer chunks than k
     const float least = bound ? key_value(bound) : -INFINITY;
 
-    // Those chunks' logits that reach the bound are collected and merged 32 at a time.
+    // Those chunks' logits that reach the bound are collected, a chunk per warp at a
+    // time; 32 of a warp's are merged into its list (many equal logits, else rare).
     unsigned long long list = 0;
     int n = 0; // logits collected in pend[w]
-    auto drain = [&](int rest) {
-#pragma unroll 1
-        while (n > rest) {
-            const int q = n < 32 ? n : 32;
-            __syncwarp();
-            list = merge32(list, sort32(lane < q ? pend[w][n - q + lane] : 0ull, lane), lane);
-            n -= q;
-            __syncwarp();
-        }
-    };
+    if (tid == 0)
+        npool = 0;
 #pragma unroll 1
     for (int c0 = 0; c0 < a.nc; c0 += kScan * kThreads) {
         if (a.nc > kScan * kThreads)
@@ -295,45 +289,76 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
         for (int j = 0; j < kScan; ++j) {
             const int c = c0 + j * kThreads + tid;
             if (c < a.nc && make_key(cm[j], c) >= bound)
-                cand[atomicAdd(&ncand, 1)] = c; // in any order: the logits are sorted
+                cand[atomicAdd(&ncand, 1)] = c; // in any order: the logits are ranked
         }
         __syncthreads();
         const int nk = ncand;
+        float v[8]; // the next chunk's
+        int e = 0;
+        auto load = [&](int i) {
+            e = i < nk ? cand[i] * kChunk - mis + lane : a.V;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = e + 32 * j >= 0 && e + 32 * j < a.V ? __ldcs(row + e + 32 * j) : 0.f;
+        };
+        load(w);
 #pragma unroll 1
-        for (int i0 = w; i0 < nk; i0 += kBatch * kWarps) {
-            float v[kBatch][8];
+        for (int i = w; i < nk; i += kWarps) {
+            float x[8];
+            const int ex = e;
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (i0 + b * kWarps < nk)
-                    load_chunk(row, mis, a.V, cand[i0 + b * kWarps], lane, v[b]);
+            for (int j = 0; j < 8; ++j)
+                x[j] = v[j];
+            load(i + kWarps);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (i0 + b * kWarps >= nk)
-                    break;
-                const long long e0 = (long long)cand[i0 + b * kWarps] * kChunk - mis + 4 * lane;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const long long e = e0 + (j >> 2) * 128 + (j & 3);
-                    const bool in = v[b][j] >= least && e >= 0 && e < a.V;
-                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-                    if (in)
-                        pend[w][n + __popc(who & ((1u << lane) - 1u))] = make_key(v[b][j], (uint32_t)e);
-                    n += __popc(who);
-                }
-                drain(31); // at most 31 stay for the next chunk
+            for (int j = 0; j < 8; ++j) {
+                const int at = ex + 32 * j;
+                const bool in = x[j] >= least && at >= 0 && at < a.V;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+                if (in)
+                    pend[w][n + __popc(who & ((1u << lane) - 1u))] = make_key(x[j], (uint32_t)at);
+                n += __popc(who);
+            }
+#pragma unroll 1
+            while (n >= 32) { // at most 31 stay for the next chunk
+                __syncwarp();
+                list = merge32(list, sort32(pend[w][n - 32 + lane], lane), lane);
+                n -= 32;
+                __syncwarp();
             }
         }
         __syncthreads(); // cand has been read
     }
-    drain(0);
-    const unsigned long long best = merge_block(list, sl, lane, w);
-    if (w == 0 && lane < a.k) {
-        const float x = key_value(best);
-        const size_t o = r * a.k + lane;
+    // What the warps have left, at most 63 each: a key's place is the number before it.
+    const uint32_t held = __ballot_sync(0xFFFFFFFFu, list != 0); // the first lanes
+    const int nh = __popc(held);
+    int base = 0;
+    if (lane == 0 && n + nh > 0)
+        base = atomicAdd(&npool, n + nh);
+    base = __shfl_sync(0xFFFFFFFFu, base, 0);
+    if (lane < n)
+        pool[base + lane] = pend[w][lane];
+    if (lane < nh)
+        pool[base + n + lane] = list;
+    __syncthreads();
+    const int np = npool;
+#pragma unroll 1
+    for (int i = tid; i < np || i < a.k; i += kThreads) {
+        const unsigned long long key = i < np ? pool[i] : 0ull; // 0: fewer logits than k
+        int place = i < np ? 0 : i;
+        if (i < np) {
+#pragma unroll 4
+            for (int j = 0; j < np; ++j)
+                place += pool[j] > key;
+        }
+        if (place >= a.k)
+            continue;
+        const float x = key_value(key);
+        const size_t o = r * a.k + place;
         if (a.top_id)
-            a.top_id[o] = bad || best == 0 ? -1 : (int32_t)key_index(best);
+            a.top_id[o] = bad || key == 0 ? -1 : (int32_t)key_index(key);
         if (a.top_logprob)
-            a.top_logprob[o] = bad ? nan : (best == 0 || x == -INFINITY ? -INFINITY : (x - m) - logs);
+            a.top_logprob[o] = bad ? nan : (key == 0 || x == -INFINITY ? -INFINITY : (x - m) - logs);
     }
 }
 
