@@ -613,7 +613,7 @@ int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top
         return W4_ERR_INVALID_ARG;
     if (M < 1 || V < 1 || ld < V || topk < 0)
         return W4_ERR_INVALID_ARG;
-    if (topk > 32)
+    if (topk > 32 || V > 2147483647 - 1024) // chunk ends past the row are 32-bit numbers too
         return W4_ERR_UNSUPPORTED;
     if (!aligned(logits, 4) || (targets && !aligned(targets, 4)) || (logprob && !aligned(logprob, 4)) ||
         (entropy && !aligned(entropy, 4)) || (top_logprob && !aligned(top_logprob, 4)) ||

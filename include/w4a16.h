@@ -364,7 +364,8 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
  *   logits fp32 [M][V], ld >= V floats between rows, 4-byte aligned (-inf: a
  *   token that a constrained decoder masks, probability 0); targets int32 [M];
  *   logprob, entropy fp32 [M]; top_logprob fp32 [M][topk]; top_id int32 [M][topk].
- *   Any output may be NULL (targets too when logprob is); topk in 0..32.
+ *   Any output may be NULL (targets too when logprob is); topk in 0..32; V up to
+ *   2^31 - 1025 (more: W4_ERR_UNSUPPORTED).
  *   A target outside [0, V) gives logprob 0 and, if status is not NULL, stores 1
  *   to *status. Entries past V are -1 and -inf. A row of -inf alone has entropy 0
  *   and log probabilities -inf; a row with a NaN or +inf gives NaN and ids -1.

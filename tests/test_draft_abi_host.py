@@ -67,6 +67,13 @@ def test_logprobs_refusals(lib, kw, rc):
     assert _logprobs(lib, **kw) == rc
 
 
+def test_logprobs_row_of_2_31(lib):
+    # chunk numbers and ends are 32-bit: a row must end 1024 before 2^31
+    V = 2**31 - 1024
+    assert _logprobs(lib, V=V, ld=V) == 2
+    assert _logprobs(lib, V=2**31 - 1, ld=2**31 - 1) == 2
+
+
 def _commit(lib, kc=A, vc=A, kpos=None, kt=A, vt=A, path=A, count=A, pos=A, L=1, B=1, N=8, T=16, W=64, status=None):
     return lib.w4_kv_commit(kc, vc, kpos, kt, vt, path, count, pos, L, B, N, T, W, status, None)
 
