@@ -21,7 +21,7 @@
 //
 // Bound by the read of the logits: 4 V bytes a row. 256 rows of 256003 logits (262 MB)
 // take 49 us with 5 alternatives, 45 us (5.8 TB/s) without: the picks of the rows that
-// finish last are not hidden. One row of 262144: 9.1 us on the GPU, a chain of short
+// finish last are not hidden. One row of 262144: 9.5 us on the GPU, a chain of short
 // steps (read 1.3 us, count of finished blocks 1.3, sums 0.7, bound 2, picks 3).
 #include "common.cuh"
 #include "internal.h"
@@ -276,6 +276,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
     // Those chunks' logits that reach the bound are collected, a chunk per warp at a
     // time; 32 of a warp's are merged into its list (many equal logits, else rare).
     unsigned long long list = 0;
+    unsigned long long reached = 0; // its k-th: equal logits of later chunks stay out
     int n = 0; // logits collected in pend[w]
     if (tid == 0)
         npool = 0;
@@ -314,18 +315,26 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int at = ex + 32 * j;
-                const bool in = x[j] >= least && at >= 0 && at < a.V;
+                const unsigned long long key = make_key(x[j], (uint32_t)at);
+                const bool in = x[j] >= least && key > reached && at >= 0 && at < a.V;
                 const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
                 if (in)
-                    pend[w][n + __popc(who & ((1u << lane) - 1u))] = make_key(x[j], (uint32_t)at);
+                    pend[w][n + __popc(who & ((1u << lane) - 1u))] = key;
                 n += __popc(who);
-            }
+                if (j != 0 && j != 7)
+                    continue;
+                // At most 31 stay for the next chunk. After the first 32 logits too: of
+                // a chunk of equal logits the others then stay out (8 sorts a chunk
+                // against 1: a row of 262144 that a mask leaves three tokens takes 17 us
+                // against 11 with 5 alternatives, 48 against 16 with 32).
 #pragma unroll 1
-            while (n >= 32) { // at most 31 stay for the next chunk
-                __syncwarp();
-                list = merge32(list, sort32(pend[w][n - 32 + lane], lane), lane);
-                n -= 32;
-                __syncwarp();
+                while (n >= 32) {
+                    __syncwarp();
+                    list = merge32(list, sort32(pend[w][n - 32 + lane], lane), lane);
+                    reached = __shfl_sync(0xFFFFFFFFu, list, a.k - 1);
+                    n -= 32;
+                    __syncwarp();
+                }
             }
         }
         __syncthreads(); // cand has been read

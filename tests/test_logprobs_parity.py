@@ -75,6 +75,28 @@ def test_sizes(w4, M, V, k):
     check(w4, logits(V, M, V), rng.integers(0, V, M), k)
 
 
+@pytest.mark.parametrize("M,V,k", [(1, 262145, 32), (2, 300007, 7), (1, 700001, 32), (1, 2000003, 3)])
+def test_rows_of_many_chunks(w4, M, V, k):
+    """More chunk maxima than the finishing block's threads hold at once, and more
+    blocks' worth of chunks than it has threads."""
+    x = logits(V, M, V)
+    check(w4, x, [V - 1] * M, k)
+    x[0] = float("-inf")
+    x[0, ::4096] = 1.0            # the last chunks' too: equal logits, one per 16 chunks
+    x[-1, V - 1] = 50.0
+    check(w4, x, [V - 1] * M, k)
+
+
+@pytest.mark.parametrize("k", [1, 5, 32])
+def test_best_chunks_in_one_thread(w4, k):
+    """The best logits 256 chunks apart: one thread's share holds all of them."""
+    x = logits(12, 1, 600000)
+    x[0, 77:600000:65536] += 100.0
+    check(w4, x, [77], k)
+    x[0, 1024:1024 + 256 * 3] = 90.0   # three chunks of equal logits
+    check(w4, x, [77], k)
+
+
 def test_strided_rows_of_every_alignment(w4):
     import torch
     for off in range(4):
