@@ -42,7 +42,7 @@ kv_commit_kernel(const KvCommitArgs a)
                 node = -1;
                 if (first && a.status)
                     *a.status = 1;
-            } else if (n - j > a.T) {
+            } else if (a.kpos && n - j > a.T) {
                 node = -1; // a later token of the path takes the same slot of a short ring
             } else {
                 slot = (int)(a.kpos ? p % a.T : p);
