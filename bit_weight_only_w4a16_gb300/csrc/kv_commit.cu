@@ -30,30 +30,38 @@ kv_commit_kernel(const KvCommitArgs a)
     const int b = blockIdx.x % a.B, l = blockIdx.x / a.B;
     const bool first = l == 0 && blockIdx.y == 0;
     const int n = min(max(__ldg(a.count + b), 0), a.N);
-    if (threadIdx.x < 64) {
-        // Thread j: token j of the path; -1 = nothing to write.
-        const int j = threadIdx.x;
+    // Thread j: token j of the path; -1 = nothing to write.
+    const int j = threadIdx.x;
+    const long long p = j < n ? (long long)__ldg(a.pos + b) + j : 0;
+    if (j < 64) {
         int node = -1, slot = -1;
         if (j < n) {
             node = __ldg(a.path + (size_t)b * a.N + j);
-            const long long p = (long long)__ldg(a.pos + b) + j;
             const bool ok = node >= 0 && node < a.N && p >= 0 && p <= 0x7FFFFFFFll && (a.kpos || p < a.T);
             if (!ok) {
                 node = -1;
                 if (first && a.status)
                     *a.status = 1;
-            } else if (a.kpos && n - j > a.T) {
-                node = -1; // a later token of the path takes the same slot of a short ring
             } else {
                 slot = (int)(a.kpos ? p % a.T : p);
-                if (first && a.kpos)
-                    a.kpos[(size_t)b * a.T + slot] = (int32_t)p;
             }
         }
         s_node[j] = node;
         s_slot[j] = slot;
     }
     __syncthreads();
+    if (a.kpos && n > a.T) {
+        // A short ring: the last token that is stored to a slot stays in it.
+        bool later = false;
+        for (int i = j + a.T; i < n; i += a.T)
+            later = later || s_node[i] >= 0;
+        __syncthreads();
+        if (later)
+            s_node[j] = -1;
+        __syncthreads();
+    }
+    if (first && a.kpos && j < n && s_node[j] >= 0)
+        a.kpos[(size_t)b * a.T + s_slot[j]] = (int32_t)p;
     const size_t lb = (size_t)l * a.B + b;
     const int w8 = a.W >> 3; // 16-byte pieces of a row
     const uint4 *src = reinterpret_cast<const uint4 *>(blockIdx.y ? a.v_tree : a.k_tree) + lb * a.N * w8;
@@ -67,10 +75,10 @@ kv_commit_kernel(const KvCommitArgs a)
             const long long i = i0 + (long long)q * kThreads;
             to[q] = -1;
             if (i < items) {
-                const int j = (int)(i / w8), c = (int)(i - (long long)j * w8);
-                if (s_node[j] >= 0) {
-                    v[q] = __ldg(src + (size_t)s_node[j] * w8 + c);
-                    to[q] = (long long)s_slot[j] * w8 + c;
+                const int t = (int)(i / w8), c = (int)(i - (long long)t * w8);
+                if (s_node[t] >= 0) {
+                    v[q] = __ldg(src + (size_t)s_node[t] * w8 + c);
+                    to[q] = (long long)s_slot[t] * w8 + c;
                 }
             }
         }

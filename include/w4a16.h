@@ -387,8 +387,9 @@ int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top
  *   pos int32 [B], kpos int32 [B][T] or NULL; 16-byte aligned, int32 4-byte.
  *   N in 1..64, L * B < 2^31. count is taken into [0, N]. A node outside [0, N),
  *   a negative position or one outside a full cache is not stored and sets
- *   *status = 1 (status may be NULL). Of tokens that share a slot of a short ring
- *   the last is stored. pos is not changed. The caches do not overlap the trees.
+ *   *status = 1 (status may be NULL). Of stored tokens that share a slot of a
+ *   short ring the last stays (one that is not stored takes no slot). pos is not
+ *   changed. The caches do not overlap the trees.
  */
 int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint16_t *k_tree,
                  const uint16_t *v_tree, const int32_t *path, const int32_t *count, const int32_t *pos, int L, int B,
