@@ -430,6 +430,11 @@ struct RowMask {
     bool live;                // a row of the output
     int lo, hi;               // kept keys (positions) [lo, hi)
     unsigned long long nodes; // tree: ancestors or self within the window
+
+    // A tree's absent node. Value rows are judged by what the present nodes keep, so its
+    // accumulator may hold 0 * NaN: zeros are selected for it. (Where a prompt's row keeps
+    // nothing, its tile's first row keeps nothing either, and every key is searched.)
+    __device__ __forceinline__ bool absent() const { return nodes == 0; }
 };
 
 template <bool TREE>
@@ -1307,6 +1312,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                     uint32_t o[32];
                     W4_TLD32(o, o_col(t) + lanes + c0);
+                    if (TREE && rm.absent()) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = 0u;
+                    }
                     uint4 y[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -1331,6 +1341,11 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 for (int c0 = half * OC; c0 < half * OC + OC; c0 += 32) {
                     uint32_t o[32];
                     W4_TLD32(o, o_col(t) + lanes + c0);
+                    if (TREE && rm.absent()) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = 0u;
+                    }
                     if (rm.live) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
