@@ -319,19 +319,23 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int s)
     return q;
 }
 
+// First position that a window ending at position `at` holds. Positions below zero keep
+// nothing, so they count as 0: the difference stays within 32 bits for every window.
+__device__ __forceinline__ int window_start(int at, int window) { return max(0, max(at, 0) - window + 1); }
+
 // First key and one past the last that any of the tokens [t0, t0 + nt) keeps.
 template <bool TREE>
 __device__ __forceinline__ void key_range(const Args &a, const Seq &q, int t0, int nt, int &lo, int &hi)
 {
     if (TREE) {
-        lo = a.window > 0 ? max(0, q.off - a.window + 1) : 0; // depth 0 sees furthest back
+        lo = a.window > 0 ? window_start(q.off, a.window) : 0; // depth 0 sees furthest back
         hi = q.lk;
         if (a.kpos) { // any slot may hold any position
             lo = 0;
             hi = a.T;
         }
     } else {
-        lo = a.window > 0 ? max(0, q.off + t0 - a.window + 1) : 0;
+        lo = a.window > 0 ? window_start(q.off + t0, a.window) : 0;
         hi = min(q.lk, q.off + t0 + nt);
     }
     if (hi <= lo) {
@@ -386,7 +390,7 @@ __device__ __forceinline__ bool edge_unit(const Args &a, const Piece &w, int x)
     }
     if (k + kKeys > w.off + w.t0 + 1 || k + kKeys > w.hi || k < w.lo) // past the first row's last key
         return true;
-    return a.window > 0 && k < w.off + w.t0 + w.nt - a.window; // before the last row's first key
+    return a.window > 0 && k < window_start(w.off + w.t0 + w.nt - 1, a.window); // before the last row's first key
 }
 
 // A value row's part in the product: 0 = kept by every row (or zeros already), 1 = by
@@ -420,7 +424,7 @@ __device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, i
         return 2;
     if (k > w.off + w.t0)
         return 1;
-    if (a.window > 0 && k <= w.off + w.t0 + w.nt - 1 - a.window)
+    if (a.window > 0 && k < window_start(w.off + w.t0 + w.nt - 1, a.window))
         return 1;
     return 0;
 }
@@ -464,7 +468,7 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int t
     } else {
         const int at = w.off + w.t0 + tok;
         m.hi = min(at + 1, w.lk);
-        m.lo = a.window > 0 ? max(0, at - a.window + 1) : 0;
+        m.lo = a.window > 0 ? window_start(at, a.window) : 0;
     }
     return m;
 }
