@@ -310,10 +310,11 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int s)
         q.off = max(__ldg(a.pos + s), 0);
         q.lk = min(q.off, a.T);
     } else {
+        // Ends are taken into the tensors first: an end before its start is an empty sequence.
         q.q0 = __ldg(a.cu_q + s);
-        q.lq = q.q0 < 0 ? 0 : max(0, min(__ldg(a.cu_q + s + 1), a.total_q) - q.q0);
+        q.lq = q.q0 < 0 ? 0 : max(0, max(0, min(__ldg(a.cu_q + s + 1), a.total_q)) - q.q0);
         q.k0 = max(0, __ldg(a.cu_k + s));
-        q.lk = max(0, min(__ldg(a.cu_k + s + 1), a.total_k) - q.k0);
+        q.lk = max(0, max(0, min(__ldg(a.cu_k + s + 1), a.total_k)) - q.k0);
         q.off = q.lk - q.lq;
     }
     return q;

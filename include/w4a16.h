@@ -309,7 +309,8 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  *
  *   out, q  bf16 [total_q][Hq][D], ldo / ldq elements between rows
  *   k, v    bf16 [total_k][Hkv][D], ldk / ldv elements between rows
- *   cu_q    int32 [B + 1] device, ascending; cu_k the same, or NULL: cu_q
+ *   cu_q    int32 [B + 1] device, ascending; cu_k the same, or NULL: cu_q (an end
+ *           past the tensor is cut there, an end before its start is an empty sequence)
  *   16-byte aligned pointers, cu_* 4-byte; ld* multiples of 8, at least heads * D.
  *   B in 1..4096, Hq / Hkv a whole number in 1..128, D in {64, 128, 256, 384,
  *   512}, scale > 0 and finite; rows and ld* below 2^31.
