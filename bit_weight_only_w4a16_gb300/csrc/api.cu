@@ -47,6 +47,21 @@ int cuda_fail(cudaError_t e)
     return W4_ERR_CUDA;
 }
 
+// Zeros, in place when the call returns. A stream of its own: a clear on the legacy
+// stream would be ordered with neither the host nor a caller's non-blocking stream.
+cudaError_t clear_now(void *p, size_t bytes)
+{
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess)
+        return e;
+    e = cudaMemsetAsync(p, 0, bytes, s);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(s);
+    const cudaError_t d = cudaStreamDestroy(s);
+    return e == cudaSuccess ? d : e;
+}
+
 // Set up (once) and return the state of the current device.
 int device_state(DeviceState **out)
 {
@@ -80,7 +95,7 @@ int device_state(DeviceState **out)
             return cuda_fail(e);
         st.keys = static_cast<unsigned long long *>(p);
         st.err = reinterpret_cast<int *>(static_cast<char *>(p) + kKeyCapacity * sizeof(unsigned long long));
-        e = cudaMemset(st.err, 0, sizeof(int));
+        e = clear_now(st.err, sizeof(int));
         if (e != cudaSuccess)
             return cuda_fail(e);
         void *w = nullptr;
@@ -90,7 +105,7 @@ int device_state(DeviceState **out)
             return cuda_fail(e);
         st.ws = static_cast<float *>(w);
         st.left = reinterpret_cast<int *>(static_cast<char *>(w) + ws_bytes);
-        e = cudaMemset(st.left, 0, left_bytes);
+        e = clear_now(st.left, left_bytes);
         if (e != cudaSuccess)
             return cuda_fail(e);
         st.num_sms = sms;
@@ -328,7 +343,7 @@ int w4_device_error(int32_t *code)
     if (e == cudaSuccess)
         e = cudaMemcpy(code, st->err, sizeof(int32_t), cudaMemcpyDeviceToHost);
     if (e == cudaSuccess)
-        e = cudaMemset(st->err, 0, sizeof(int32_t));
+        e = clear_now(st->err, sizeof(int32_t));
     return e == cudaSuccess ? W4_OK : cuda_fail(e);
 }
 
