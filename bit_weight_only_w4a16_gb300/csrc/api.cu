@@ -25,13 +25,16 @@ size_t ws_capacity(int num_sms)
     return n > kWsFloats ? n : kWsFloats;
 }
 
+constexpr size_t kLeftBytes = w4::kLogprobRows * sizeof(unsigned long long);
+
 struct DeviceState {
     // Set (release) once the fields below are written; read (acquire) first.
     std::atomic<bool> ready{false};
     int num_sms = 0;
     unsigned long long *keys = nullptr;
     int *err = nullptr; // device error word written by kernels whose bounded waits ran out
-    int *left = nullptr; // log probabilities: blocks of each row that have finished (zeros between calls)
+    // Log probabilities: blocks of each row that have finished (zeros between calls).
+    unsigned long long *left = nullptr;
     float *ws = nullptr; // prefill split-K and attention partials, ws_capacity(num_sms) floats
 };
 
@@ -99,13 +102,13 @@ int device_state(DeviceState **out)
         if (e != cudaSuccess)
             return cuda_fail(e);
         void *w = nullptr;
-        const size_t ws_bytes = ws_capacity(sms) * sizeof(float), left_bytes = w4::kLogprobRows * sizeof(int);
-        e = cudaMalloc(&w, ws_bytes + left_bytes);
+        const size_t ws_bytes = ws_capacity(sms) * sizeof(float); // a multiple of 32
+        e = cudaMalloc(&w, ws_bytes + kLeftBytes);
         if (e != cudaSuccess)
             return cuda_fail(e);
         st.ws = static_cast<float *>(w);
-        st.left = reinterpret_cast<int *>(static_cast<char *>(w) + ws_bytes);
-        e = clear_now(st.left, left_bytes);
+        st.left = reinterpret_cast<unsigned long long *>(static_cast<char *>(w) + ws_bytes);
+        e = clear_now(st.left, kLeftBytes);
         if (e != cudaSuccess)
             return cuda_fail(e);
         st.num_sms = sms;
@@ -344,6 +347,8 @@ int w4_device_error(int32_t *code)
         e = cudaMemcpy(code, st->err, sizeof(int32_t), cudaMemcpyDeviceToHost);
     if (e == cudaSuccess)
         e = clear_now(st->err, sizeof(int32_t));
+    if (e == cudaSuccess)
+        e = clear_now(st->left, kLeftBytes);
     return e == cudaSuccess ? W4_OK : cuda_fail(e);
 }
 

@@ -205,7 +205,8 @@ struct LogprobsArgs {
 };
 // left: kLogprobRows zeros, and zeros again when the call has run.
 constexpr int kLogprobRows = 65535;
-cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int *left, int num_sms, cudaStream_t s);
+cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, unsigned long long *left, int num_sms,
+                         cudaStream_t s);
 
 // Rows path[b][0 .. count[b]) of the trees' keys and values [L][B][N][W] into the
 // slots of positions pos[b], pos[b] + 1, ... of caches [L][B][T][W].

@@ -40,13 +40,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 // masked logit, or finite logits further apart than fp32 reaches) is not 0.
 constexpr float kLeast = -1e30f;
 
+// A row's counter is 0 before and after a call. A count that calls which overlapped (in
+// spite of the rule) have left behind does not stay: every block first raises the counter
+// to its launch's number and a count of 0, which changes nothing once one block has done
+// it. A captured launch keeps the number of its capture: after a newer launch's remainder
+// it is right again once w4_device_error has cleared the counters.
+constexpr int kTagShift = 16; // at most 256 blocks count
+
 struct LogprobArgs {
     const float *x;
     long long ld;
     int V, nc, S; // logits per row, chunks per row, blocks per row
     float *cmax;  // [rows][nc]
     float *part;  // [rows][S][4]: m, s, u
-    int *left;    // [rows] blocks that have finished; 0 before and after a call
+    unsigned long long *left; // [rows] blocks that have finished, above kTagShift bits the call
+    unsigned long long tag;   // this launch's number, larger than earlier ones'
     const int32_t *targets;
     float *logprob, *entropy, *top_logprob;
     int32_t *top_id;
@@ -290,11 +298,14 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t r)
 #pragma unroll
         for (int j = 0; j < kScan; ++j) {
             const int c = c0 + j * kThreads + tid;
-            if (c < a.nc && make_key(cm[j], c) >= bound)
-                cand[atomicAdd(&ncand, 1)] = c; // in any order: the logits are ranked
+            if (c < a.nc && make_key(cm[j], c) >= bound) {
+                const int at = atomicAdd(&ncand, 1); // in any order: the logits are ranked
+                if (at < 32 * kScan) // more only if another call overwrites the maxima meanwhile
+                    cand[at] = c;
+            }
         }
         __syncthreads();
-        const int nk = ncand;
+        const int nk = min(ncand, 32 * kScan);
         float v[8]; // the next chunk's
         int e = 0;
         auto load = [&](int i) {
@@ -382,6 +393,8 @@ logprob_kernel(const LogprobArgs a)
     const int mis = row_mis(row);
     const int c0 = (int)((long long)blockIdx.x * a.nc / a.S), c1 = (int)((long long)(blockIdx.x + 1) * a.nc / a.S);
     float *cmax = a.cmax + (size_t)blockIdx.y * a.nc;
+    if (threadIdx.x == 0) // before this thread's count: the same address, so in this order
+        atomicMax(a.left + blockIdx.y, a.tag << kTagShift);
 
     float m = -INFINITY, s = 0.f, u = 0.f; // m is the same in all lanes
     for (int cb = c0 + w; cb < c1; cb += kBatch * kWarps) {
@@ -440,7 +453,7 @@ logprob_kernel(const LogprobArgs a)
         *reinterpret_cast<float4 *>(a.part + ((size_t)blockIdx.y * a.S + blockIdx.x) * 4) =
             make_float4(st.x, st.y, st.z, 0.f);
         __threadfence();
-        const int n = atomicAdd(a.left + blockIdx.y, 1);
+        const int n = (int)(atomicAdd(a.left + blockIdx.y, 1ull) & ((1ull << kTagShift) - 1));
         s_last = n == a.S - 1;
         if (s_last)
             a.left[blockIdx.y] = 0;
@@ -453,9 +466,10 @@ logprob_kernel(const LogprobArgs a)
 
 } // namespace
 
-cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int *left, int num_sms,
+cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, unsigned long long *left, int num_sms,
                          cudaStream_t s)
 {
+    static std::atomic<unsigned long long> launches{0};
     LogprobArgs a = {};
     a.ld = p.ld;
     a.V = p.V;
@@ -495,6 +509,7 @@ cudaError_t run_logprobs(const LogprobsArgs &p, float *ws, size_t ws_floats, int
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     for (long long r0 = 0; r0 < p.M; r0 += rows) {
         const int n = (int)(p.M - r0 < rows ? p.M - r0 : rows);
+        a.tag = launches.fetch_add(1, std::memory_order_relaxed) + 1;
         a.x = p.logits + (size_t)r0 * p.ld;
         a.part = ws;
         a.cmax = ws + (size_t)n * S * 4;

@@ -67,7 +67,8 @@ int w4_init(void);
 
 /*
  * Reads and clears the device error word of the current device after a
- * cudaDeviceSynchronize. *code is 0 when every kernel finished normally. A set
+ * cudaDeviceSynchronize (and clears what calls that overlapped against their rule have
+ * left in the library's scratch). *code is 0 when every kernel finished normally. A set
  * bit means that a kernel's bounded wait on its own shared-memory pipeline ran
  * out: bit 0 the streaming decode kernel, bit 1 the prefill GEMM, bit 2 the
  * self-test below, bit 3 the prompt and tree attention. That kernel then returned without hanging; its outputs are

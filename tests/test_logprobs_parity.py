@@ -205,3 +205,68 @@ def test_refusals(w4):
     for k in (33, -1):
         with pytest.raises(w4.W4Error):
             w4.w4_logprobs(x, topk=k)
+
+
+def test_captured_calls_between_newer_ones(w4):
+    """A captured call is replayed after many newer calls on the same rows, and they
+    after it."""
+    import torch
+    x = logits(20, 5, 60000).cuda()
+    t = torch.arange(5, dtype=torch.int32, device="cuda")
+    want = w4.w4_logprobs(x, t, 7)
+    out = [torch.zeros_like(y) for y in want]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w4.w4_logprobs(x, t, 7, out=out, stream=s)
+    for n in (1, 3, 2000):  # blocks per row differ with the rows' number and length
+        other = logits(n, n, 300).cuda()
+        for _ in range(4):
+            w4.w4_logprobs(other, topk=3)
+            [y.zero_() for y in out]
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+            got = w4.w4_logprobs(x, t, 7)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_that_overlapped_leave_nothing_behind(w4):
+    """Calls that break the rule and overlap on two streams may give anything (inside
+    their outputs); a call after them is right, and so is a captured one once the
+    device error word has been read."""
+    import torch
+    xs = [logits(21, 4, 262144).cuda(), logits(22, 3, 70001).cuda(), logits(23, 40, 9000).cuda()]
+    want = [w4.w4_logprobs(x, topk=5) for x in xs]
+    outs = [[(Guard((x.shape[0],), torch.float32), Guard((x.shape[0], 5), torch.float32),
+              Guard((x.shape[0], 5), torch.int32)) for x in xs] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    s = torch.cuda.Stream()
+    cap = [torch.zeros_like(y) for y in want[0][1:]]
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w4.w4_logprobs(xs[0], topk=5, out=(None, *cap), stream=s)
+    torch.cuda.synchronize()
+    for turn in range(30):
+        for i in range(6):
+            for j in range(2):
+                n = (i + j + turn) % 3
+                w4.w4_logprobs(xs[n], topk=5, out=(None, *(b.t for b in outs[j][n])), stream=streams[j])
+        torch.cuda.synchronize()
+        for o in outs:
+            for gs in o:
+                for b in gs:
+                    b.check("overlapping calls")
+        for x, w in zip(xs, want):
+            got = w4.w4_logprobs(x, topk=5)
+            assert all(torch.equal(a, b) for a, b in zip(got[1:], w[1:]))
+    for i in range(6):
+        for j in range(2):
+            w4.w4_logprobs(xs[(i + j) % 3], topk=5, out=(None, *(b.t for b in outs[j][(i + j) % 3])), stream=streams[j])
+    assert w4.device_error() == 0
+    [y.zero_() for y in cap]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(cap, want[0][1:]))
