@@ -382,6 +382,7 @@ def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0
     q bf16 [total_q][Hq][D]; k, v bf16 [total_k][Hkv][D] (rows may be strided);
     cu_q, cu_k int32 [B + 1]: the sequences' first rows (cu_k None: as cu_q). A
     sequence's queries are the last of its keys' positions; window 0 = no window.
+    Uses the library's split scratch: no other call that does may overlap in time.
     """
     Sq, Hq, D = q.shape
     Sk, Hkv, _ = k.shape
@@ -405,7 +406,8 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
 
     parents int32 [B][N] (-1 = first level, -2 = absent); pos int32 [B]: the first
     level's position (cached positions below it are kept); kpos int32 [B][T]
-    recorded positions of a ring, or None (slot t holds position t).
+    recorded positions of a ring, or None (slot t holds position t). Uses the
+    library's split scratch: no other call that does may overlap in time.
     """
     B, N, Hq, D = q.shape
     _, T, Hkv, _ = k.shape
@@ -425,7 +427,8 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
 def w4_logprobs(logits, targets=None, topk: int = 0, status=None, out=None, stream=None):
     """(logprob [M] or None, entropy [M], top_logprob [M][topk], top_id [M][topk]) of
     fp32 logits [M][V] (rows may be strided) and int32 targets [M]. out: the four
-    tensors to write instead (None in the place of one that is not wanted)."""
+    tensors to write instead (None in the place of one that is not wanted). Uses the
+    library's split scratch: no other call that does may overlap in time."""
     if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
     M, V = logits.shape

@@ -23,6 +23,13 @@
  *   - Results are bitwise deterministic run to run (no floating-point atomics).
  *   - All calls are safe to capture in a CUDA graph once the library has been
  *     initialised on the device (w4_init, or any earlier call on that device).
+ *   - The library's split scratch is one allocation per device, which w4a16_gemm
+ *     (M > 8), w4a16_gemv_hadamard, w4_attn_decode, w4_attn_decode_devpos,
+ *     w4_attn_prompt, w4_attn_tree and w4_logprobs share. Two of these calls must not
+ *     overlap in time on a device, whichever they are: put them on one stream or
+ *     order their streams with events (judging one step on a side stream while the
+ *     next one's attention runs is such an overlap). Outputs of calls that overlap
+ *     are not valid; calls after them are.
  *   - group is 32, 64, 128, 256 or 512 codes per step along K (32 is the
  *     checkpoint paragraph's format; the "fastgemma-gemma-4-E2B" model card's
  *     file table stores FFN and LM-head weights with group 256, the per-layer
@@ -104,7 +111,8 @@ int w4a16_gemv(float *y, const uint16_t *x, const uint32_t *qweight, const uint1
  * weight multiplies the whole chunk) runs a tensor-core kernel that dequantizes
  * each weight tile to bf16 (round to nearest even) on its way into shared
  * memory and accumulates in fp32 in tensor memory. Same layouts as w4a16_gemv.
- * For M > 8, N must be a multiple of 16 and K a multiple of 64.
+ * For M > 8, N must be a multiple of 16 and K a multiple of 64, and the call uses
+ * the library's split scratch (no overlap with other calls that do, see above).
  */
 int w4a16_gemm(float *y, const uint16_t *x, const uint32_t *qweight, const uint16_t *scales,
                int M, int N, int K, int group, void *stream);
@@ -319,7 +327,7 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  * rounded once. What a row does not keep never reaches it, NaN and infinities
  * included. Lengths are read when the kernels run: one captured call serves
  * every batch with the same total_q and total_k. Uses the library's split
- * scratch (like w4a16_gemm).
+ * scratch: calls that need it must not run concurrently on different streams.
  */
 int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                    const int32_t *cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int D, long long ldq,
@@ -345,7 +353,7 @@ int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const ui
  *   kpos            int32 [B][T] (-1 = empty slot) or NULL; parents int32 [B][N]; pos int32 [B]
  *   16-byte aligned pointers, the int32 ones 4-byte. N in 1..64, B in 1..4096,
  *   B * T and B * N below 2^31; Hq / Hkv, D, scale, precision, masked values and
- *   scratch as w4_attn_prompt. pos, parents and kpos are read when the kernels
+ *   scratch (no concurrent calls) as w4_attn_prompt. pos, parents and kpos are read when the kernels
  *   run. N = 1 is decode attention for any number of key/value heads.
  */
 int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kpos,
@@ -371,7 +379,9 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
  *   A target outside [0, V) gives logprob 0 and, if status is not NULL, stores 1
  *   to *status. Entries past V are -1 and -inf. A row of -inf alone has entropy 0
  *   and log probabilities -inf; a row with a NaN or +inf gives NaN and ids -1.
- * Sums in fp32. Uses the library's split scratch (like w4a16_gemm).
+ * Sums in fp32. Uses the library's split scratch: calls that need it must not run
+ * concurrently on different streams (should they have, a captured call is right again
+ * after w4_device_error, any other at once).
  */
 int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top_id, const float *logits,
                 const int32_t *targets, int M, int V, long long ld, int topk, int32_t *status, void *stream);
