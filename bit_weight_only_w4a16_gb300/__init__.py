@@ -331,12 +331,18 @@ def w4_decode_prologue(token, pos, qtable, scales, group: int = 32, x_next=None,
 # than through Stream objects and c_void_p).
 _BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
 _F32, _I32 = frozenset((torch.float32,)), frozenset((torch.int32,))
+_INT_MIN, _INT_MAX = -2**31, 2**31 - 1
 
 
 def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _past_int(*numbers):
+    """The C calls take int32: a larger number would be cut to its low bits."""
+    return ValueError(f"a size or window does not fit 32 bits: {max(numbers, key=abs)}")
 
 
 def _tensor(t, name, dtypes, shape):
@@ -387,6 +393,8 @@ def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0
     Sq, Hq, D = q.shape
     Sk, Hkv, _ = k.shape
     B = cu_q.numel() - 1
+    if max(Sq, Sk, Hq, Hkv, D, B, window) > _INT_MAX or window < _INT_MIN:
+        raise _past_int(Sq, Sk, Hq, Hkv, D, B, window)
     o = torch.empty((Sq, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
     ldq, ldk, ldv = _rows(q, "q", Sq, Hq, D), _rows(k, "k", Sk, Hkv, D), _rows(v, "v", Sk, Hkv, D)
     ldo = Hq * D if out is None else _rows(o, "out", Sq, Hq, D)
@@ -411,6 +419,8 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
     """
     B, N, Hq, D = q.shape
     _, T, Hkv, _ = k.shape
+    if max(B, N, T, Hq, Hkv, D, window) > _INT_MAX or window < _INT_MIN:
+        raise _past_int(B, N, T, Hq, Hkv, D, window)
     o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
     cache, tree, rows = (B, T, Hkv, D), (B, N, Hkv, D), (B, N, Hq, D)
     rc = _lib.w4_attn_tree(_tensor(o, "out", _BITS16, rows), _tensor(q, "q", _BITS16, rows),
@@ -432,6 +442,8 @@ def w4_logprobs(logits, targets=None, topk: int = 0, status=None, out=None, stre
     if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
     M, V = logits.shape
+    if max(M, V, topk) > _INT_MAX or topk < _INT_MIN:
+        raise _past_int(M, V, topk)
     s0, s1 = logits.stride()
     if s1 != 1 and V > 1:
         raise ValueError("a row of logits must be contiguous")
@@ -463,6 +475,8 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
     (a ring when kpos int32 [B][T] is given: it records the positions)."""
     L, B, T, W = k_cache.shape
     N = k_tree.shape[2]
+    if max(L, B, N, T, W) > _INT_MAX:
+        raise _past_int(L, B, N, T, W)
     cache, tree = (L, B, T, W), (L, B, N, W)
     rc = _lib.w4_kv_commit(_tensor(k_cache, "k_cache", _BITS16, cache), _tensor(v_cache, "v_cache", _BITS16, cache),
                            None if kpos is None else _ints(kpos, "kpos", B * T),
