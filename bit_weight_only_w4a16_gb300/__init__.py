@@ -334,10 +334,29 @@ _F32, _I32 = frozenset((torch.float32,)), frozenset((torch.int32,))
 _INT_MIN, _INT_MAX = -2**31, 2**31 - 1
 
 
-def _raw_stream(stream, t):
+_current_device = torch._C._cuda_getDevice
+
+
+def _device(t, name):
+    """The tensor's device; it has to be the current one, whose scratch and SMs the
+    call uses."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    now = _current_device()
+    if dev != now:
+        raise ValueError(f"{name} is on device {dev}, the current device is {now}")
+    return dev
+
+
+def _raw_stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _elsewhere(name, dev):
+    return ValueError(f"{name} must be a CUDA tensor on device {dev}")
 
 
 def _past_int(*numbers):
@@ -345,10 +364,10 @@ def _past_int(*numbers):
     return ValueError(f"a size or window does not fit 32 bits: {max(numbers, key=abs)}")
 
 
-def _tensor(t, name, dtypes, shape):
-    """A contiguous CUDA tensor of these types and this shape; its address."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _tensor(t, name, dtypes, shape, dev):
+    """A contiguous tensor of these types and this shape on the call's device; its address."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, dev)
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype} is not served")
     if t.shape != shape:
@@ -358,20 +377,20 @@ def _tensor(t, name, dtypes, shape):
     return t.data_ptr()
 
 
-def _ints(t, name, n):
-    """A contiguous CUDA int32 tensor of n elements; its address."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _ints(t, name, n, dev):
+    """A contiguous int32 tensor of n elements on the call's device; its address."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, dev)
     if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 with {n} elements")
     return t.data_ptr()
 
 
-def _rows(t, name, rows, heads, D):
+def _rows(t, name, rows, heads, D, dev):
     """bf16 [rows][heads][D] whose rows may be strided (a view of a wider
     projection): elements between rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise _elsewhere(name, dev)
     if t.dtype not in _BITS16:
         raise TypeError(f"{name} must be bf16 (or its raw 16-bit bits)")
     if t.shape != (rows, heads, D):
@@ -393,14 +412,16 @@ def w4_attn_prompt(q, k, v, cu_q, cu_k=None, window: int = 0, scale: float = 1.0
     Sq, Hq, D = q.shape
     Sk, Hkv, _ = k.shape
     B = cu_q.numel() - 1
-    if max(Sq, Sk, Hq, Hkv, D, B, window) > _INT_MAX or window < _INT_MIN:
+    if (Sq > _INT_MAX or Sk > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX or B > _INT_MAX or
+            window > _INT_MAX or window < _INT_MIN):
         raise _past_int(Sq, Sk, Hq, Hkv, D, B, window)
+    dev = _device(q, "q")
     o = torch.empty((Sq, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    ldq, ldk, ldv = _rows(q, "q", Sq, Hq, D), _rows(k, "k", Sk, Hkv, D), _rows(v, "v", Sk, Hkv, D)
-    ldo = Hq * D if out is None else _rows(o, "out", Sq, Hq, D)
-    rc = _lib.w4_attn_prompt(o.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ints(cu_q, "cu_q", B + 1),
-                             None if cu_k is None else _ints(cu_k, "cu_k", B + 1), B, Sq, Sk, Hq, Hkv, D, ldq, ldk,
-                             ldv, ldo, window, scale, _raw_stream(stream, q))
+    ldq, ldk = _rows(q, "q", Sq, Hq, D, dev), _rows(k, "k", Sk, Hkv, D, dev)
+    ldv, ldo = _rows(v, "v", Sk, Hkv, D, dev), Hq * D if out is None else _rows(o, "out", Sq, Hq, D, dev)
+    rc = _lib.w4_attn_prompt(o.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ints(cu_q, "cu_q", B + 1, dev),
+                             None if cu_k is None else _ints(cu_k, "cu_k", B + 1, dev), B, Sq, Sk, Hq, Hkv, D, ldq,
+                             ldk, ldv, ldo, window, scale, _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_attn_prompt")
     return o
@@ -419,16 +440,18 @@ def w4_attn_tree(q, k, v, k_tree, v_tree, parents, pos, kpos=None, window: int =
     """
     B, N, Hq, D = q.shape
     _, T, Hkv, _ = k.shape
-    if max(B, N, T, Hq, Hkv, D, window) > _INT_MAX or window < _INT_MIN:
+    if (B > _INT_MAX or N > _INT_MAX or T > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX or
+            window > _INT_MAX or window < _INT_MIN):
         raise _past_int(B, N, T, Hq, Hkv, D, window)
+    dev = _device(q, "q")
     o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
     cache, tree, rows = (B, T, Hkv, D), (B, N, Hkv, D), (B, N, Hq, D)
-    rc = _lib.w4_attn_tree(_tensor(o, "out", _BITS16, rows), _tensor(q, "q", _BITS16, rows),
-                           _tensor(k, "k", _BITS16, cache), _tensor(v, "v", _BITS16, cache),
-                           None if kpos is None else _ints(kpos, "kpos", B * T),
-                           _tensor(k_tree, "k_tree", _BITS16, tree), _tensor(v_tree, "v_tree", _BITS16, tree),
-                           _ints(parents, "parents", B * N), _ints(pos, "pos", B), B, N, T, Hq, Hkv, D, window, scale,
-                           _raw_stream(stream, q))
+    rc = _lib.w4_attn_tree(_tensor(o, "out", _BITS16, rows, dev), _tensor(q, "q", _BITS16, rows, dev),
+                           _tensor(k, "k", _BITS16, cache, dev), _tensor(v, "v", _BITS16, cache, dev),
+                           None if kpos is None else _ints(kpos, "kpos", B * T, dev),
+                           _tensor(k_tree, "k_tree", _BITS16, tree, dev),
+                           _tensor(v_tree, "v_tree", _BITS16, tree, dev), _ints(parents, "parents", B * N, dev),
+                           _ints(pos, "pos", B, dev), B, N, T, Hq, Hkv, D, window, scale, _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_attn_tree")
     return o
@@ -442,28 +465,28 @@ def w4_logprobs(logits, targets=None, topk: int = 0, status=None, out=None, stre
     if not logits.is_cuda or logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be a CUDA fp32 [M][V] tensor")
     M, V = logits.shape
-    if max(M, V, topk) > _INT_MAX or topk < _INT_MIN:
+    if M > _INT_MAX or V > _INT_MAX or topk > _INT_MAX or topk < _INT_MIN:
         raise _past_int(M, V, topk)
     s0, s1 = logits.stride()
     if s1 != 1 and V > 1:
         raise ValueError("a row of logits must be contiguous")
-    k, dev = max(int(topk), 0), logits.device
+    k, dev, on = max(int(topk), 0), _device(logits, "logits"), logits.device
     if out is None:
-        lp = None if targets is None else torch.empty((M,), dtype=torch.float32, device=dev)
-        ent = torch.empty((M,), dtype=torch.float32, device=dev)
-        top = torch.empty((M, k), dtype=torch.float32, device=dev)
-        ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+        lp = None if targets is None else torch.empty((M,), dtype=torch.float32, device=on)
+        ent = torch.empty((M,), dtype=torch.float32, device=on)
+        top = torch.empty((M, k), dtype=torch.float32, device=on)
+        ids = torch.empty((M, k), dtype=torch.int32, device=on)
     else:
         lp, ent, top, ids = out
         for t, name, dt, shape in ((lp, "logprob", _F32, (M,)), (ent, "entropy", _F32, (M,)),
                                    (top, "top_logprob", _F32, (M, k)), (ids, "top_id", _I32, (M, k))):
             if t is not None:
-                _tensor(t, name, dt, shape)
+                _tensor(t, name, dt, shape, dev)
     rc = _lib.w4_logprobs(None if lp is None else lp.data_ptr(), None if ent is None else ent.data_ptr(),
                           top.data_ptr() if k and top is not None else None,
                           ids.data_ptr() if k and ids is not None else None, logits.data_ptr(),
-                          None if targets is None else _ints(targets, "targets", M), M, V, s0 if M > 1 else V,
-                          topk, None if status is None else _ints(status, "status", 1), _raw_stream(stream, logits))
+                          None if targets is None else _ints(targets, "targets", M, dev), M, V, s0 if M > 1 else V,
+                          topk, None if status is None else _ints(status, "status", 1, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_logprobs")
     return lp, ent, top, ids
@@ -475,13 +498,16 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
     (a ring when kpos int32 [B][T] is given: it records the positions)."""
     L, B, T, W = k_cache.shape
     N = k_tree.shape[2]
-    if max(L, B, N, T, W) > _INT_MAX:
+    if L > _INT_MAX or B > _INT_MAX or N > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
         raise _past_int(L, B, N, T, W)
+    dev = _device(k_cache, "k_cache")
     cache, tree = (L, B, T, W), (L, B, N, W)
-    rc = _lib.w4_kv_commit(_tensor(k_cache, "k_cache", _BITS16, cache), _tensor(v_cache, "v_cache", _BITS16, cache),
-                           None if kpos is None else _ints(kpos, "kpos", B * T),
-                           _tensor(k_tree, "k_tree", _BITS16, tree), _tensor(v_tree, "v_tree", _BITS16, tree),
-                           _ints(path, "path", B * N), _ints(count, "count", B), _ints(pos, "pos", B), L, B, N, T, W,
-                           None if status is None else _ints(status, "status", 1), _raw_stream(stream, k_cache))
+    rc = _lib.w4_kv_commit(_tensor(k_cache, "k_cache", _BITS16, cache, dev),
+                           _tensor(v_cache, "v_cache", _BITS16, cache, dev),
+                           None if kpos is None else _ints(kpos, "kpos", B * T, dev),
+                           _tensor(k_tree, "k_tree", _BITS16, tree, dev),
+                           _tensor(v_tree, "v_tree", _BITS16, tree, dev), _ints(path, "path", B * N, dev),
+                           _ints(count, "count", B, dev), _ints(pos, "pos", B, dev), L, B, N, T, W,
+                           None if status is None else _ints(status, "status", 1, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_kv_commit")
