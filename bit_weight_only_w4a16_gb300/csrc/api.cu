@@ -141,6 +141,10 @@ int check_attn_args(const float *out, const uint16_t *q, const uint16_t *k, cons
     return W4_OK;
 }
 
+// Rows (or slots, over all sequences) of the tiled attention calls at most: the ends of
+// key tiles that begin below are 32-bit numbers too.
+constexpr long long kAttnRows = 2147483647 - 1024;
+
 // Head layout, width, window and scale of the tiled attention calls.
 int check_heads(int Hq, int Hkv, int D, int window, float scale)
 {
@@ -547,7 +551,7 @@ int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const ui
     int rc = check_heads(Hq, Hkv, D, window, scale);
     if (rc != W4_OK)
         return rc;
-    if (B > 4096)
+    if (B > 4096 || total_q > kAttnRows || total_k > kAttnRows)
         return W4_ERR_UNSUPPORTED;
     const long long wq = (long long)Hq * D, wk = (long long)Hkv * D, most = (1ll << 31) - 1;
     if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || ldq > most || ldk > most || ldv > most || ldo > most)
@@ -598,6 +602,8 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
         return W4_ERR_UNSUPPORTED;
     if ((long long)B * T >= (1ll << 31) || (long long)Hq * D >= (1ll << 31))
         return W4_ERR_INVALID_ARG;
+    if ((long long)B * T > kAttnRows)
+        return W4_ERR_UNSUPPORTED;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_tree, 16) ||
         !aligned(v_tree, 16) || !aligned(parents, 4) || !aligned(pos, 4) || (kpos && !aligned(kpos, 4)))
         return W4_ERR_MISALIGNED;

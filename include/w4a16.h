@@ -322,7 +322,8 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  *           past the tensor is cut there, an end before its start is an empty sequence)
  *   16-byte aligned pointers, cu_* 4-byte; ld* multiples of 8, at least heads * D.
  *   B in 1..4096, Hq / Hkv a whole number in 1..128, D in {64, 128, 256, 384,
- *   512}, scale > 0 and finite; rows and ld* below 2^31.
+ *   512}, scale > 0 and finite; ld* below 2^31, rows up to 2^31 - 1025 (more:
+ *   W4_ERR_UNSUPPORTED).
  * Scores and sums fp32; weights bf16 (relative 2^-8) in the value product, out
  * rounded once. What a row does not keep never reaches it, NaN and infinities
  * included. Lengths are read when the kernels run: one captured call serves
@@ -352,8 +353,9 @@ int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const ui
  *   k_tree, v_tree  bf16 [B][N][Hkv][D]
  *   kpos            int32 [B][T] (-1 = empty slot) or NULL; parents int32 [B][N]; pos int32 [B]
  *   16-byte aligned pointers, the int32 ones 4-byte. N in 1..64, B in 1..4096,
- *   B * T and B * N below 2^31; Hq / Hkv, D, scale, precision, masked values and
- *   scratch (no concurrent calls) as w4_attn_prompt. pos, parents and kpos are read when the kernels
+ *   B * T up to 2^31 - 1025 (more: W4_ERR_UNSUPPORTED, from 2^31 on
+ *   W4_ERR_INVALID_ARG); Hq / Hkv, D, scale, precision, masked values and scratch (no
+ *   concurrent calls) as w4_attn_prompt. pos, parents and kpos are read when the kernels
  *   run. N = 1 is decode attention for any number of key/value heads.
  */
 int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kpos,

@@ -74,6 +74,13 @@ def test_logprobs_row_of_2_31(lib):
     assert _logprobs(lib, V=2**31 - 1, ld=2**31 - 1) == 2
 
 
+@pytest.mark.parametrize("n", [2**31 - 1024, 2**31 - 1])
+def test_attention_rows_next_to_2_31(lib, n):
+    # a key tile's end is a 32-bit number too
+    assert _prompt(lib, Sk=n) == 2 and _prompt(lib, Sq=n) == 2
+    assert _tree(lib, T=n) == 2 and _tree(lib, B=2, T=n // 2 + 1) == (2 if n < 2**31 - 1 else 1)
+
+
 def _commit(lib, kc=A, vc=A, kpos=None, kt=A, vt=A, path=A, count=A, pos=A, L=1, B=1, N=8, T=16, W=64, status=None):
     return lib.w4_kv_commit(kc, vc, kpos, kt, vt, path, count, pos, L, B, N, T, W, status, None)
 
