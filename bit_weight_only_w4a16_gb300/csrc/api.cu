@@ -145,6 +145,12 @@ int check_attn_args(const float *out, const uint16_t *q, const uint16_t *k, cons
 // key tiles that begin below are 32-bit numbers too.
 constexpr long long kAttnRows = 2147483647 - 1024;
 
+// Row tiles of a tiled attention call at most; their numbers are 32-bit.
+bool too_many_tiles(long long rows, int seqs, int Hq, int Hkv, int D)
+{
+    return rows / w4::attn_tile_tokens(Hq / Hkv, D) + seqs > 2147483647 / (w4::attn_slices(D) * (long long)Hkv);
+}
+
 // Head layout, width, window and scale of the tiled attention calls.
 int check_heads(int Hq, int Hkv, int D, int window, float scale)
 {
@@ -551,7 +557,7 @@ int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const ui
     int rc = check_heads(Hq, Hkv, D, window, scale);
     if (rc != W4_OK)
         return rc;
-    if (B > 4096 || total_q > kAttnRows || total_k > kAttnRows)
+    if (B > 4096 || total_q > kAttnRows || total_k > kAttnRows || too_many_tiles(total_q, B, Hq, Hkv, D))
         return W4_ERR_UNSUPPORTED;
     const long long wq = (long long)Hq * D, wk = (long long)Hkv * D, most = (1ll << 31) - 1;
     if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || ldq > most || ldk > most || ldv > most || ldo > most)
@@ -602,7 +608,7 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
         return W4_ERR_UNSUPPORTED;
     if ((long long)B * T >= (1ll << 31) || (long long)Hq * D >= (1ll << 31))
         return W4_ERR_INVALID_ARG;
-    if ((long long)B * T > kAttnRows)
+    if ((long long)B * T > kAttnRows || too_many_tiles((long long)B * N, B, Hq, Hkv, D))
         return W4_ERR_UNSUPPORTED;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_tree, 16) ||
         !aligned(v_tree, 16) || !aligned(parents, 4) || !aligned(pos, 4) || (kpos && !aligned(kpos, 4)))

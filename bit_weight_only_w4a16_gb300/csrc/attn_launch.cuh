@@ -48,6 +48,7 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
                    long long tiles, bool may_cut, float *ws, int num_sms, cudaStream_t s)
 {
     using S = Shape<D>;
+    static_assert(S::TQ == (D <= 128 ? 2 : 1) && S::NV == (D > 256 ? 2 : 1), "as in attn_tile_tokens, attn_slices");
     Maps m;
     if (!encode_rows(&m.q, q.p, q.rows, a.Hq, D, q.ld, a.G, a.tpt) ||
         !encode_rows(&m.k, k.p, k.rows, a.Hkv, D, k.ld, 1, kKeys) ||

@@ -163,6 +163,9 @@ cudaError_t run_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos,
 
 // Tiled attention (attn_tiles.cuh): scratch floats for a device with num_sms SMs.
 size_t attn_ws_floats(int num_sms);
+// Tokens of a row tile with G query heads on one; slices of the value width.
+inline int attn_tile_tokens(int G, int D) { return (D <= 128 ? 2 : 1) * (128 / G); }
+inline int attn_slices(int D) { return D > 256 ? 2 : 1; }
 
 // Causal attention of B packed sequences: query rows cu_q[b] .. cu_q[b + 1) are
 // the last ones of the positions that key rows cu_k[b] .. cu_k[b + 1) hold.

@@ -322,7 +322,8 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  *           past the tensor is cut there, an end before its start is an empty sequence)
  *   16-byte aligned pointers, cu_* 4-byte; ld* multiples of 8, at least heads * D.
  *   B in 1..4096, Hq / Hkv a whole number in 1..128, D in {64, 128, 256, 384,
- *   512}, scale > 0 and finite; ld* below 2^31, rows up to 2^31 - 1025 (more:
+ *   512}, scale > 0 and finite; ld* below 2^31, rows up to 2^31 - 1025, and at most
+ *   2^31 - 1 tiles of 128 or 256 rows over all sequences and key/value heads (more:
  *   W4_ERR_UNSUPPORTED).
  * Scores and sums fp32; weights bf16 (relative 2^-8) in the value product, out
  * rounded once. What a row does not keep never reaches it, NaN and infinities

@@ -81,6 +81,19 @@ def test_attention_rows_next_to_2_31(lib, n):
     assert _tree(lib, T=n) == 2 and _tree(lib, B=2, T=n // 2 + 1) == (2 if n < 2**31 - 1 else 1)
 
 
+@pytest.mark.parametrize("D,rc", [(64, 5), (256, 5), (512, 2)])
+def test_row_tiles_past_2_31(lib, D, rc):
+    # 4096 sequences of one token on 2^18 + 1 heads: 2^30 + 4096 row tiles, two slices at D = 512
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    H = (1 << 18) + 1
+    assert _prompt(lib, B=4095, Sq=4096, Hq=H, Hkv=H, D=D, ldq=H * D, ldk=H * D, ldv=H * D, ldo=H * D) == rc
+    assert _prompt(lib, B=4095, Sq=4096, Hq=2 * H, Hkv=2 * H, D=D, ldq=2 * H * D, ldk=2 * H * D, ldv=2 * H * D,
+                   ldo=2 * H * D) == 2
+    assert _tree(lib, B=4096, N=1, T=1, Hq=H, Hkv=H, D=D) == rc
+
+
 def _commit(lib, kc=A, vc=A, kpos=None, kt=A, vt=A, path=A, count=A, pos=A, L=1, B=1, N=8, T=16, W=64, status=None):
     return lib.w4_kv_commit(kc, vc, kpos, kt, vt, path, count, pos, L, B, N, T, W, status, None)
 
