@@ -575,9 +575,11 @@ __device__ __forceinline__ void swap4(uint4 &a, uint4 &b, int d, bool upper)
 }
 
 template <int THREADS>
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
+__device__ __forceinline__ long long block_scan(int v, int *warp_sums, long long &total)
 {
-    // Inclusive sum over the block; `total` is the sum of all.
+    // Inclusive sum over the block; `total` is the sum of all. A warp's sum fits 32 bits
+    // (a row tile of 2^31 keys has 2^24 units, a call below 2^31 row tiles); the sum of
+    // the units of 384 such tiles does not.
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -590,7 +592,7 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total)
     if (lane == 31)
         warp_sums[w] = x;
     __syncthreads();
-    int before = 0, all = 0;
+    long long before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
         const int t = warp_sums[i];
@@ -616,11 +618,11 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
     for (int s0 = 0; a.B > 1 && s0 < a.B; s0 += S::THREADS) {
         const int s = s0 + (int)threadIdx.x;
         const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
-        int total;
-        const int incl = block_scan<S::THREADS>(nt, sh.warp_sums, total);
+        long long total;
+        const int incl = (int)block_scan<S::THREADS>(nt, sh.warp_sums, total);
         if (s < a.B)
             sbase[s] = R + incl - nt;
-        R += total;
+        R += (int)total; // row tiles of the call: below 2^31
     }
     __syncthreads();
     const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
@@ -643,7 +645,8 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
     };
     // Thread r of the last round of row tiles: its tile's sequence, units, cost and
     // the costs up to it. With one round they serve the second pass as well.
-    int s_r = 0, n_r = 0, cost_r = 0, incl_r = 0, total_r = 0;
+    int s_r = 0, n_r = 0, cost_r = 0;
+    long long incl_r = 0, total_r = 0;
     auto round = [&](int r0) {
         const int r = r0 + (int)threadIdx.x;
         n_r = r < R ? units_of(r, s_r) : 0;
