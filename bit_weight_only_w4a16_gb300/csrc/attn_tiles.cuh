@@ -69,7 +69,10 @@ constexpr int kBlock = 16384;   // 128 rows x 64 dims: a block of Q or K
 constexpr int kSmemBlocks = 14; // Q tiles and ring together
 constexpr int kMaxSlots = 12;   // ring slots
 constexpr int kPieces = 4;      // pieces in flight between the warps
-constexpr int kWaitLimit = 1 << 15;
+// Waits give up after so many tries of 20 us: 0.7 s for what the next unit brings, 40 s
+// for what lies a piece away (a whole row tile: units times 1 to 5 us; the largest keys
+// and values that fit the device take about 25 s). A short wait that gives up ends all others.
+constexpr int kWaitLimit = 1 << 15, kWaitPiece = 1 << 21;
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
 template <int D>
@@ -787,9 +790,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     auto s_col = [&](int b) { return tmem + 128u * (uint32_t)b; };
     auto o_col = [&](int t) { return tmem + 256u + (uint32_t)(t * S::DV); };
 
-    auto wait = [&](unsigned long long &bar, uint32_t parity) -> bool {
+    auto wait = [&](unsigned long long &bar, uint32_t parity, int limit = kWaitLimit) -> bool {
         const uint32_t b = smem_addr(&bar);
-        for (int i = 0; i < kWaitLimit; ++i) {
+        for (int i = 0; i < limit; ++i) {
             if (mbar_try_wait(b, parity, 20000u))
                 return true;
             if (sh.abort)
@@ -801,7 +804,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     };
 
     // Piece p is in sh.piece[p % kPieces] between these two.
-    auto take = [&](uint32_t p) { return wait(bars.pc_full[p % kPieces], (p / kPieces) & 1); };
+    auto take = [&](uint32_t p) { return wait(bars.pc_full[p % kPieces], (p / kPieces) & 1, kWaitPiece); };
     auto done = [&](uint32_t p) { mbar_arrive(smem_addr(&bars.pc_empty[p % kPieces])); };
 
     if (warp == 0) {
@@ -1039,7 +1042,8 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
                         cls |= (uint32_t)key_class<TREE>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
-                    ok = __all_sync(0xFFFFFFFFu, wait(bars.edge[slot], (par >> slot) & 1));
+                    // Units between that are no edges pass without this warp.
+                    ok = __all_sync(0xFFFFFFFFu, wait(bars.edge[slot], (par >> slot) & 1, kWaitPiece));
                     if (!ok)
                         break;
                     par ^= 1u << slot;
@@ -1416,7 +1420,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             w.off = q.off;
             w.nq = S::TQ == 1 ? 1 : (w.nt > a.tpt ? 2 : 1);
             if (piece >= (uint32_t)kPieces)
-                ok = wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1);
+                ok = wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1, kWaitPiece);
             if (!ok)
                 break;
             sh.piece[piece % kPieces] = w;
@@ -1443,7 +1447,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             }
         }
         if (ok && (piece < (uint32_t)kPieces ||
-                   wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1))) {
+                   wait(bars.pc_empty[piece % kPieces], (piece / kPieces - 1) & 1, kWaitPiece))) {
             sh.piece[piece % kPieces].units = 0;
             mbar_arrive(smem_addr(&bars.pc_full[piece % kPieces]));
         }
