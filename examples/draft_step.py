@@ -82,6 +82,9 @@ class Model:
         """The prompt's keys and values into the caches; tokens int32 [n], all but the
         last position (the first step's first node) are read."""
         n = tokens.numel() - 1
+        self.pos.fill_(n)
+        if n == 0:
+            return
         h = self.embed(tokens[:n])
         cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
         for i, layer in enumerate(self.layers):
@@ -95,7 +98,6 @@ class Model:
                 self.kpos[0, p % self.ring] = p.int()
             else:
                 kc[:n], vc[:n] = k[:, 0], v[:, 0]
-        self.pos.fill_(n)
 
     def step(self, tokens, parents):
         """Logits [N][vocab] of a tree of tokens at the current position, and the
