@@ -8,8 +8,11 @@
 // maximum has grown by more than 2^8 (a weight is then at most 256, which bf16
 // holds with the same relative error), so the accumulator in tensor memory is
 // rarely rescaled. Weights are rounded to bf16 (relative 2^-8) for the tensor
-// core's value product: the output is bf16, whose own rounding is as large. The
-// sum of the weights, m and the accumulator are fp32.
+// core's value product: the output is bf16, whose own rounding is as large. (The
+// decode attention of one token carries its weights as two bf16 parts and returns
+// fp32: it is bound by the stream; here a second part would be half as many
+// operations more where they are the bound.) The sum of the weights, m and the
+// accumulator are fp32.
 //
 // Rows. The G query heads of one key/value head share its keys, so a tile's 128
 // rows are (token, head) pairs, 128 / G tokens with all their heads: each key
@@ -41,10 +44,12 @@
 // each commit of the issuing thread leaves the tensor core about 50 and 20 cycles
 // idle, the rest is the chain scores -> weights (about 1200 cycles: tensor-memory
 // reads, the exchange of the maxima, 64 exponentials a thread, the store) -> product
-// when it is longer than the other buffer's work. 16384 tokens, 8 heads on 1, D =
-// 256: 0.66 ms, 1.66 PFLOP/s (0.86 of the measured cuBLAS rate); D = 128: 0.9 PFLOP/s
-// (the chain: with two row tiles a thread has 128 exponentials); D = 512: 0.97
-// PFLOP/s of the operations asked for, 1.46 of those done. A long cache streams at
+// when it is longer than the other buffer's work. 16384 tokens, 8 heads on 1: D =
+// 256 0.68 ms, 1.62 PFLOP/s, when calls lie apart (0.84 of the measured cuBLAS burst), 0.72
+// ms in seconds of calls, when the power cap takes the clock to 1.74 GHz; D = 128 0.44 ms, 1.25
+// PFLOP/s (the chain: with two row tiles a thread has 128 exponentials). 256 tokens after
+// 130000, D = 512: 0.57-0.59 ms apart, 0.93-0.96 PFLOP/s of the operations asked for, 1.4
+// of those done; 0.61 ms in seconds of calls. A long cache streams at
 // 6.1 TB/s; 131072 x 512 with 16 nodes takes 84 us, of which 44 are the stream, 13
 // the merge and the rest start and end.
 //

@@ -9,7 +9,9 @@
 //   s = sum e^(x - m),  u = sum e^(x - m) (x - m)
 // and when m grows to m': s' = f s, u' = f (u + (m - m') s), f = e^(m - m').
 //   log p(t) = (x_t - m) - log s,   entropy = log s - u / s
-// (u in terms of x - m keeps the entropy's two parts small).
+// (u in terms of x - m keeps the entropy's two parts small). All of it is fp32; e^y is the
+// hardware's ex2 of y log2 e, whose error (2^-22 and the rounding of y log2 e) stays below
+// that of the sums: log probabilities come within about 1e-7 (relative) of 64 bits.
 //
 // The k largest logits need no second pass over the row: the streaming blocks keep
 // the maximum of every 256 logits (a chunk). The block that finishes a row last gives

@@ -327,9 +327,11 @@ int w4_decode_prologue(uint16_t *x_next, int32_t *tokens, int32_t *pos, const in
  *   W4_ERR_UNSUPPORTED).
  * Scores and sums fp32; weights bf16 (relative 2^-8) in the value product, out
  * rounded once. What a row does not keep never reaches it, NaN and infinities
- * included. Lengths are read when the kernels run: one captured call serves
- * every batch with the same total_q and total_k. Uses the library's split
- * scratch: calls that need it must not run concurrently on different streams.
+ * included. (w4_attn_decode carries its weights as two bf16 parts, 2^-16, and
+ * returns fp32: it is the more exact call where it serves.) Lengths are read when
+ * the kernels run: one captured call serves every batch with the same total_q and
+ * total_k. Uses the library's split scratch: calls that need it must not run
+ * concurrently on different streams.
  */
 int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                    const int32_t *cu_k, int B, int total_q, int total_k, int Hq, int Hkv, int D, long long ldq,
@@ -357,7 +359,8 @@ int w4_attn_prompt(uint16_t *out, const uint16_t *q, const uint16_t *k, const ui
  *   B * T up to 2^31 - 1025 (more: W4_ERR_UNSUPPORTED, from 2^31 on
  *   W4_ERR_INVALID_ARG); Hq / Hkv, D, scale, precision, masked values and scratch (no
  *   concurrent calls) as w4_attn_prompt. pos, parents and kpos are read when the kernels
- *   run. N = 1 is decode attention for any number of key/value heads.
+ *   run. N = 1 is decode attention for any number of key/value heads, at this
+ *   call's precision.
  */
 int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *kpos,
                  const uint16_t *k_tree, const uint16_t *v_tree, const int32_t *parents, const int32_t *pos, int B,
