@@ -357,8 +357,6 @@ int w4_device_error(int32_t *code)
         e = cudaMemcpy(code, st->err, sizeof(int32_t), cudaMemcpyDeviceToHost);
     if (e == cudaSuccess)
         e = clear_now(st->err, sizeof(int32_t));
-    if (e == cudaSuccess)
-        e = clear_now(st->left, kLeftBytes);
     return e == cudaSuccess ? W4_OK : cuda_fail(e);
 }
 

@@ -46,7 +46,7 @@ constexpr float kLeast = -1e30f;
 // spite of the rule) have left behind does not stay: every block first raises the counter
 // to its launch's number and a count of 0, which changes nothing once one block has done
 // it. A captured launch keeps the number of its capture: after a newer launch's remainder
-// it is right again once w4_device_error has cleared the counters.
+// it is right again once a launch with a newer number has been over its rows.
 constexpr int kTagShift = 16; // at most 256 blocks count
 
 struct LogprobArgs {

@@ -74,8 +74,7 @@ int w4_init(void);
 
 /*
  * Reads and clears the device error word of the current device after a
- * cudaDeviceSynchronize (and clears what calls that overlapped against their rule have
- * left in the library's scratch). *code is 0 when every kernel finished normally. A set
+ * cudaDeviceSynchronize. *code is 0 when every kernel finished normally. A set
  * bit means that a kernel's bounded wait on its own shared-memory pipeline ran
  * out: bit 0 the streaming decode kernel, bit 1 the prefill GEMM, bit 2 the
  * self-test below, bit 3 the prompt and tree attention. That kernel then returned without hanging; its outputs are
@@ -386,8 +385,8 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
  *   to *status. Entries past V are -1 and -inf. A row of -inf alone has entropy 0
  *   and log probabilities -inf; a row with a NaN or +inf gives NaN and ids -1.
  * Sums in fp32. Uses the library's split scratch: calls that need it must not run
- * concurrently on different streams (should they have, a captured call is right again
- * after w4_device_error, any other at once).
+ * concurrently on different streams (should they have, later calls are right at once, a
+ * captured one once a call outside its graph has been made with as many rows).
  */
 int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top_id, const float *logits,
                 const int32_t *targets, int M, int V, long long ld, int topk, int32_t *status, void *stream);

@@ -234,8 +234,7 @@ def test_captured_calls_between_newer_ones(w4):
 
 def test_calls_that_overlapped_leave_nothing_behind(w4):
     """Calls that break the rule and overlap on two streams may give anything (inside
-    their outputs); a call after them is right, and so is a captured one once the
-    device error word has been read."""
+    their outputs); a call after them is right, and after it a captured one."""
     import torch
     xs = [logits(21, 4, 262144).cuda(), logits(22, 3, 70001).cuda(), logits(23, 40, 9000).cuda()]
     want = [w4.w4_logprobs(x, topk=5) for x in xs]
@@ -265,6 +264,9 @@ def test_calls_that_overlapped_leave_nothing_behind(w4):
     for i in range(6):
         for j in range(2):
             w4.w4_logprobs(xs[(i + j) % 3], topk=5, out=(None, *(b.t for b in outs[j][(i + j) % 3])), stream=streams[j])
+    torch.cuda.synchronize()
+    big = logits(24, 40, 500).cuda()  # rows of every call above
+    assert torch.equal(w4.w4_logprobs(big, topk=1)[3][:, 0].long(), big.argmax(1))
     assert w4.device_error() == 0
     [y.zero_() for y in cap]
     g.replay()
