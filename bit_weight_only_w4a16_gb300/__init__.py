@@ -28,7 +28,8 @@ EXPORTS = ("w4_status_string", "w4_last_cuda_error", "w4_init", "w4_device_error
            "w4a16_gemv_argmax", "w4a16_gemv_argmax_noalloc", "w4_embed_gather", "hbm_read_probe",
            "w4_attn_decode", "w4a16_gemv_hadamard", "w4_selftest_wait_timeout", "w4_attn_decode_devpos",
            "w4_kv_append", "w4a16_gemv_argmax_forced", "w4_decode_prologue", "w4_attn_prompt", "w4_attn_tree",
-           "w4_logprobs", "w4_kv_commit")
+           "w4_logprobs", "w4_kv_commit", "w4_qk_norm_rope", "w4_qkv_paged", "w4_attn_paged",
+           "w4_lora")
 
 
 class W4Error(RuntimeError):
@@ -86,6 +87,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4_logprobs.restype = I
     lib.w4_kv_commit.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P]
     lib.w4_kv_commit.restype = I
+    lib.w4_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, L, L, L, L, I, I, F, P]
+    lib.w4_qk_norm_rope.restype = I
+    lib.w4_qkv_paged.argtypes = [P] * 13 + [I] * 9 + [L] * 7 + [I, I, F, P, P]
+    lib.w4_qkv_paged.restype = I
+    lib.w4_attn_paged.argtypes = [P] * 7 + [I] * 8 + [L] * 5 + [I, F, P]
+    lib.w4_attn_paged.restype = I
+    lib.w4_lora.argtypes = [P] * 7 + [I] * 5 + [L] * 3 + [P, P]
+    lib.w4_lora.restype = I
     return lib
 
 
@@ -511,3 +520,190 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
                            None if status is None else _ints(status, "status", 1, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_kv_commit")
+
+
+_ROWS = _BITS16 | _F32
+
+
+def _heads(t, name, shape, dtype, dev):
+    """Rows of heads of one type (fp32, or bf16 or its bits), strided rows: elements between rows."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, dev)
+    if t.dtype != dtype and not (t.dtype in _BITS16 and dtype in _BITS16):
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    rows, heads, D = shape
+    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        raise ValueError(f"{name}: heads and head width must be contiguous")
+    return s0 if rows > 1 else heads * D
+
+
+def _weight(t, name, n, dev):
+    """A contiguous fp32 tensor of n elements or None; its address."""
+    return None if t is None else _tensor(t, name, _F32, (n,), dev)
+
+
+def _pages(k_pages, v_pages, Hkv, D, dev):
+    """Strides of pages, rows and heads (where there is one only, a stride that is in order)."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.get_device() != dev:
+            raise _elsewhere(name, dev)
+        if t.dtype not in _BITS16:
+            raise TypeError(f"{name} must be bf16 (or its raw 16-bit bits)")
+        if t.dim() != 4 or t.shape[2:] != (Hkv, D) or t.shape != k_pages.shape:
+            raise ValueError(f"{name} must be [pages][page][{Hkv}][{D}] (k_pages and v_pages alike), got {list(t.shape)}")
+    n, page = k_pages.shape[:2]
+    sk, sv = k_pages.stride(), v_pages.stride()
+    for a, b, size in zip(sk, sv, k_pages.shape):
+        if a != b and size > 1:
+            raise ValueError("k_pages and v_pages must have the same strides")
+    if sk[3] != 1:
+        raise ValueError("k_pages: the head width must be contiguous")
+    head = sk[2] if Hkv > 1 else D
+    row = sk[1] if page > 1 else D
+    return n, page, sk[0] if n > 1 else max(row * page, head * Hkv), row, head
+
+
+def _batch(table, lens, cu_q, rows, dev):
+    """Sequences, pages of a table's row, and the addresses of table, lens and cu_q."""
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [B][pages of a sequence at most]")
+    B, n = table.shape
+    if cu_q is None and rows != B:
+        raise ValueError(f"without cu_q there is one row of each sequence: {rows} rows, {B} sequences")
+    return (B, n, _ints(table, "table", B * n, dev), _ints(lens, "lens", B, dev),
+            None if cu_q is None else _ints(cu_q, "cu_q", B + 1, dev))
+
+
+def w4_qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, pairs: bool = False, q_out=None,
+                    k_out=None, stream=None):
+    """(q_out bf16 [M][Hq][D], k_out bf16 [M][Hkv][D]): heads normed (where a weight fp32
+    [D] is given) and turned by pos * inv_freq.
+
+    q [M][Hq][D], k [M][Hkv][D] (or None) fp32 or bf16, rows may be strided (views of a
+    fused projection); pos int32 [M]; inv_freq fp32 [R / 2] (or None: no rotation);
+    pairs: neighbouring elements are turned together, else j and j + R / 2. q_out may
+    be q, k_out k, where those are bf16.
+    """
+    M, Hq, D = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if M > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX or R > _INT_MAX:
+        raise _past_int(M, Hq, Hkv, D, R)
+    dev = _device(q, "q")
+    if q.dtype not in _ROWS:
+        raise TypeError(f"q: {q.dtype} is not served")
+    qo = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+    ldq, ldqo = _heads(q, "q", (M, Hq, D), q.dtype, dev), _heads(qo, "q_out", (M, Hq, D), torch.bfloat16, dev)
+    ko, ldk, ldko = None, 0, 0
+    if k is not None:
+        ko = torch.empty((M, Hkv, D), dtype=torch.bfloat16, device=q.device) if k_out is None else k_out
+        ldk, ldko = _heads(k, "k", (M, Hkv, D), q.dtype, dev), _heads(ko, "k_out", (M, Hkv, D), torch.bfloat16, dev)
+    rc = _lib.w4_qk_norm_rope(qo.data_ptr(), None if k is None else ko.data_ptr(), q.data_ptr(),
+                              None if k is None else k.data_ptr(), _weight(q_weight, "q_weight", D, dev),
+                              _weight(k_weight, "k_weight", D, dev), _weight(inv_freq, "inv_freq", R // 2, dev),
+                              _ints(pos, "pos", M, dev), M, Hq, Hkv, D, R, ldq, ldk, ldqo, ldko,
+                              q.dtype == torch.float32, pairs, eps, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "w4_qk_norm_rope")
+    return qo, ko
+
+
+def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_weight=None, k_weight=None, v_weight=None,
+                 eps: float = 1e-6, pairs: bool = False, q_out=None, status=None, stream=None):
+    """q_out bf16 [M][Hq][D] as w4_qk_norm_rope; the keys (normed and turned) and values
+    of the new tokens go to the pages of a cache.
+
+    k_pages, v_pages bf16 [pages][page][Hkv][D] (strided views alike); table int32
+    [B][n]: the pages of each sequence in order; lens int32 [B]: positions of each with
+    its new tokens, which are the last; cu_q int32 [B + 1]: the sequences' first rows,
+    or None: row b is sequence b's. A token without a page sets status (int32 [1]).
+    """
+    M, Hq, D = q.shape
+    Hkv = k.shape[1]
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    dev = _device(q, "q")
+    if q.dtype not in _ROWS:
+        raise TypeError(f"q: {q.dtype} is not served")
+    qo = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+    n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
+    B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
+    if max(M, Hq, Hkv, D, R, n, page, B, tn) > _INT_MAX:
+        raise _past_int(M, Hq, Hkv, D, R, n, page, B, tn)
+    ldq, ldk = _heads(q, "q", (M, Hq, D), q.dtype, dev), _heads(k, "k", (M, Hkv, D), q.dtype, dev)
+    ldv, ldqo = _heads(v, "v", (M, Hkv, D), q.dtype, dev), _heads(qo, "q_out", (M, Hq, D), torch.bfloat16, dev)
+    rc = _lib.w4_qkv_paged(qo.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), q.data_ptr(), k.data_ptr(),
+                           v.data_ptr(), _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev),
+                           _weight(v_weight, "v_weight", D, dev), _weight(inv_freq, "inv_freq", R // 2, dev), tp, lp, cp,
+                           B, M, Hq, Hkv, D, R, n, page, tn, ldq, ldk, ldv, ldqo, ps, rs, hs, q.dtype == torch.float32,
+                           pairs, eps, None if status is None else _ints(status, "status", 1, dev),
+                           _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "w4_qkv_paged")
+    return qo
+
+
+def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, scale: float = 1.0, out=None, stream=None):
+    """bf16 [total_q][Hq][D]: causal attention of new tokens (chunks, or one of each
+    sequence when cu_q is None) over a paged cache that holds their keys already.
+
+    q bf16 [total_q][Hq][D] (rows may be strided); pages, table, lens and cu_q as
+    w4_qkv_paged; window 0 = no window. Uses the library's split scratch: no other call
+    that does may overlap in time.
+    """
+    M, Hq, D = q.shape
+    Hkv = k_pages.shape[2]
+    dev = _device(q, "q")
+    o = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
+    B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
+    if max(M, Hq, Hkv, D, n, page, B, tn, window) > _INT_MAX or window < _INT_MIN:
+        raise _past_int(M, Hq, Hkv, D, n, page, B, tn, window)
+    ldq, ldo = _rows(q, "q", M, Hq, D, dev), Hq * D if out is None else _rows(o, "out", M, Hq, D, dev)
+    rc = _lib.w4_attn_paged(o.data_ptr(), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tp, lp, cp, B, M, Hq, Hkv,
+                            D, n, page, tn, ldq, ldo, ps, rs, hs, window, scale, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "w4_attn_paged")
+    return o
+
+
+def _matrix(t, name, dtypes, shape, dev):
+    """A matrix of these types whose rows may be strided: elements between rows."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, dev)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} is not served")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return s0 if shape[0] > 1 else shape[1]
+
+
+def w4_lora(y, x, a, b, ids, scale=None, out=None, status=None, stream=None):
+    """out fp32 [M][N] = y + scale[i] b[i] (a[i] x) with each row's adapter i = ids[m]
+    (below 0: none, out = y).
+
+    y fp32 [M][N] (a projection of x bf16 [M][K]; rows of both may be strided); a bf16
+    [L][R][K], b bf16 [L][N][R], R <= 128; ids int32 [M]; scale fp32 [L] or None. out
+    may be y. An id of L or more counts as none and sets status (int32 [1]). Uses the
+    library's split scratch: no other call that does may overlap in time.
+    """
+    M, N = y.shape
+    L, R, K = a.shape
+    if max(M, N, K, R, L) > _INT_MAX:
+        raise _past_int(M, N, K, R, L)
+    dev = _device(y, "y")
+    o = torch.empty((M, N), dtype=torch.float32, device=y.device) if out is None else out
+    ldy, ldx = _matrix(y, "y", _F32, (M, N), dev), _matrix(x, "x", _BITS16, (M, K), dev)
+    ldo = N if out is None else _matrix(o, "out", _F32, (M, N), dev)
+    rc = _lib.w4_lora(o.data_ptr(), y.data_ptr(), x.data_ptr(), _tensor(a, "a", _BITS16, (L, R, K), dev),
+                      _tensor(b, "b", _BITS16, (L, N, R), dev), _ints(ids, "ids", M, dev), _weight(scale, "scale", L, dev),
+                      M, N, K, R, L, ldo, ldy, ldx, None if status is None else _ints(status, "status", 1, dev),
+                      _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "w4_lora")
+    return o

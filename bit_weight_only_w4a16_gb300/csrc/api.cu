@@ -636,6 +636,252 @@ int w4_attn_tree(uint16_t *out, const uint16_t *q, const uint16_t *k, const uint
     return e == cudaSuccess ? W4_OK : cuda_fail(e);
 }
 
+namespace {
+
+// Pages of a cache: sizes, and strides that keep rows, heads and pages apart.
+int check_pages(int B, int Hkv, int D, int pages, int page, int table_pages, long long page_stride,
+                long long row_stride, long long head_stride)
+{
+    if (B < 1 || pages < 1 || page < 1 || table_pages < 1)
+        return W4_ERR_INVALID_ARG;
+    if (B > 4096 || page < 16 || page > 1024 || (page & (page - 1)) != 0 || (long long)table_pages * page > kAttnRows)
+        return W4_ERR_UNSUPPORTED;
+    struct {
+        long long stride, n;
+    } d[3] = {{head_stride, Hkv}, {row_stride, page}, {page_stride, pages}};
+    for (int i = 0; i < 3; ++i)
+        if (d[i].stride < D || d[i].stride > (1ll << 38)) // a tensor copy's strides end at 2^40 bytes
+            return W4_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (d[i].stride % 8 != 0)
+            return W4_ERR_MISALIGNED;
+    for (int i = 0; i < 2; ++i) // ascending strides
+        for (int j = 0; j < 2 - i; ++j)
+            if (d[j].stride > d[j + 1].stride || (d[j].stride == d[j + 1].stride && d[j].n > d[j + 1].n)) {
+                const auto t = d[j];
+                d[j] = d[j + 1];
+                d[j + 1] = t;
+            }
+    double extent = D;
+    for (int i = 0; i < 3; ++i) {
+        if (d[i].n > 1 && (double)d[i].stride < extent)
+            return W4_ERR_INVALID_ARG;
+        extent += (double)d[i].stride * (double)(d[i].n - 1);
+    }
+    return extent < 4.6e18 ? W4_OK : W4_ERR_INVALID_ARG;
+}
+
+int log2_of(int n)
+{
+    int r = 0;
+    while ((1 << r) < n)
+        ++r;
+    return r;
+}
+
+// What both norm-and-rotation calls check.
+int check_norm_rope(const w4::NormRopeArgs &a, int ldv_heads)
+{
+    if (a.M < 1 || a.Hq < 1 || a.Hkv < 0 || a.D < 1 || a.R < 0 || !(a.eps >= 0.f) || !(a.eps <= 3.4e38f) ||
+        (long long)a.Hq + 2ll * a.Hkv >= (1ll << 20))
+        return W4_ERR_INVALID_ARG;
+    if (!(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 384 || a.D == 512) || (a.R % 8 != 0 && a.R <= a.D))
+        return W4_ERR_UNSUPPORTED;
+    if (a.R > a.D || (a.R > 0 && !a.inv_freq))
+        return W4_ERR_INVALID_ARG;
+    const long long wq = (long long)a.Hq * a.D, wk = (long long)a.Hkv * a.D, most = (1ll << 31) - 1;
+    if (a.ldq < wq || a.ldqo < wq || a.ldk < wk || a.ldv < (long long)ldv_heads * a.D || a.ldko < wk || a.ldq > most ||
+        a.ldqo > most || a.ldk > most || a.ldv > most || a.ldko > most)
+        return W4_ERR_INVALID_ARG;
+    if (a.ldq % 8 != 0 || a.ldqo % 8 != 0 || a.ldk % 8 != 0 || a.ldv % 8 != 0 || a.ldko % 8 != 0)
+        return W4_ERR_MISALIGNED;
+    if (!aligned(a.q_out, 16) || !aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.k_out, 16) ||
+        !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16) ||
+        !aligned(a.v_weight, 16) || !aligned(a.inv_freq, 4) || !aligned(a.pos, 4) || !aligned(a.table, 4) ||
+        !aligned(a.lens, 4) || !aligned(a.cu_q, 4) || !aligned(a.status, 4))
+        return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+int do_norm_rope(const w4::NormRopeArgs &a, void *stream)
+{
+    DeviceState *st = nullptr;
+    const int rc = device_state(&st);
+    if (rc != W4_OK)
+        return rc;
+    cudaError_t e = w4::run_qk_norm_rope(a, st->num_sms, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported)
+        return W4_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+} // namespace
+
+int w4_lora(float *out, const float *y, const uint16_t *x, const uint16_t *a, const uint16_t *b, const int32_t *ids,
+            const float *scale, int M, int N, int K, int R, int L, long long ldo, long long ldy, long long ldx,
+            int32_t *status, void *stream)
+{
+    if (!out || !y || !x || !a || !b || !ids || M < 1 || N < 1 || K < 1 || R < 1 || L < 1)
+        return W4_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 32 != 0)
+        return W4_ERR_INVALID_ARG;
+    if (R % 8 != 0 || R > 128 || N > 1 << 23)
+        return W4_ERR_UNSUPPORTED;
+    const long long most = (1ll << 31) - 1;
+    if (ldo < N || ldy < N || ldx < K || ldo > most || ldy > most || ldx > most || (out == y && ldo != ldy))
+        return W4_ERR_INVALID_ARG;
+    if (ldo % 4 != 0 || ldy % 4 != 0 || ldx % 8 != 0)
+        return W4_ERR_MISALIGNED;
+    if (!aligned(out, 16) || !aligned(y, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+        !aligned(ids, 4) || !aligned(scale, 4) || !aligned(status, 4))
+        return W4_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    const int rc = device_state(&st);
+    if (rc != W4_OK)
+        return rc;
+    const w4::LoraArgs p = {out, y, x, a, b, ids, scale, M, N, K, R, L, ldo, ldy, ldx, status};
+    cudaError_t e = w4::run_lora(p, st->ws, ws_capacity(st->num_sms), st->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
+int w4_qk_norm_rope(uint16_t *q_out, uint16_t *k_out, const void *q, const void *k, const float *q_weight,
+                    const float *k_weight, const float *inv_freq, const int32_t *pos, int M, int Hq, int Hkv, int D,
+                    int R, long long ldq, long long ldk, long long ldqo, long long ldko, int f32, int pairs, float eps,
+                    void *stream)
+{
+    if (!q_out || !q || !pos || (Hkv != 0 && (!k || !k_out)))
+        return W4_ERR_INVALID_ARG;
+    w4::NormRopeArgs a = {};
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q = q;
+    a.k = k;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.inv_freq = inv_freq;
+    a.pos = pos;
+    a.M = M;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.R = R;
+    a.ldq = ldq;
+    a.ldk = Hkv == 0 ? 0 : ldk;
+    a.ldqo = ldqo;
+    a.ldko = Hkv == 0 ? 0 : ldko;
+    a.eps = eps;
+    a.f32 = f32 != 0;
+    a.pairs = pairs != 0;
+    const int rc = check_norm_rope(a, 0);
+    return rc == W4_OK ? do_norm_rope(a, stream) : rc;
+}
+
+int w4_qkv_paged(uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages, const void *q, const void *k, const void *v,
+                 const float *q_weight, const float *k_weight, const float *v_weight, const float *inv_freq,
+                 const int32_t *table, const int32_t *lens, const int32_t *cu_q, int B, int M, int Hq, int Hkv, int D,
+                 int R, int pages, int page, int table_pages, long long ldq, long long ldk, long long ldv,
+                 long long ldqo, long long page_stride, long long row_stride, long long head_stride, int f32,
+                 int pairs, float eps, int32_t *status, void *stream)
+{
+    if (!q_out || !k_pages || !v_pages || !q || !k || !v || !table || !lens || Hkv < 1 || (!cu_q && M != B))
+        return W4_ERR_INVALID_ARG;
+    w4::NormRopeArgs a = {};
+    a.q_out = q_out;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.v_weight = v_weight;
+    a.inv_freq = inv_freq;
+    a.table = table;
+    a.lens = lens;
+    a.cu_q = cu_q;
+    a.M = M;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.R = R;
+    a.pages = pages;
+    a.table_pages = table_pages;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.ldqo = ldqo;
+    a.ldko = (long long)Hkv * D; // no rows of keys
+    a.page_stride = page_stride;
+    a.row_stride = row_stride;
+    a.head_stride = head_stride;
+    a.eps = eps;
+    a.f32 = f32 != 0;
+    a.pairs = pairs != 0;
+    a.status = status;
+    int rc = check_norm_rope(a, Hkv);
+    if (rc == W4_OK)
+        rc = check_pages(B, Hkv, D, pages, page, table_pages, page_stride, row_stride, head_stride);
+    if (rc != W4_OK)
+        return rc;
+    a.page_log2 = log2_of(page);
+    return do_norm_rope(a, stream);
+}
+
+int w4_attn_paged(uint16_t *out, const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                  const int32_t *table, const int32_t *lens, const int32_t *cu_q, int B, int total_q, int Hq, int Hkv,
+                  int D, int pages, int page, int table_pages, long long ldq, long long ldo, long long page_stride,
+                  long long row_stride, long long head_stride, int window, float scale, void *stream)
+{
+    if (!out || !q || !k_pages || !v_pages || !table || !lens)
+        return W4_ERR_INVALID_ARG;
+    if (total_q < 1 || (!cu_q && total_q != B))
+        return W4_ERR_INVALID_ARG;
+    int rc = check_heads(Hq, Hkv, D, window, scale);
+    if (rc == W4_OK)
+        rc = check_pages(B, Hkv, D, pages, page, table_pages, page_stride, row_stride, head_stride);
+    if (rc != W4_OK)
+        return rc;
+    if (total_q > kAttnRows || too_many_tiles(total_q, B, Hq, Hkv, D))
+        return W4_ERR_UNSUPPORTED;
+    const long long wq = (long long)Hq * D, most = (1ll << 31) - 1;
+    if (ldq < wq || ldo < wq || ldq > most || ldo > most)
+        return W4_ERR_INVALID_ARG;
+    if (ldq % 8 != 0 || ldo % 8 != 0)
+        return W4_ERR_MISALIGNED;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(table, 4) ||
+        !aligned(lens, 4) || !aligned(cu_q, 4))
+        return W4_ERR_MISALIGNED;
+    DeviceState *st = nullptr;
+    if ((rc = device_state(&st)) != W4_OK)
+        return rc;
+    w4::AttnPagedArgs p = {};
+    p.out = out;
+    p.q = q;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.table = table;
+    p.lens = lens;
+    p.cu_q = cu_q;
+    p.B = B;
+    p.total_q = total_q;
+    p.pages = pages;
+    p.page_log2 = log2_of(page);
+    p.table_pages = table_pages;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.page_stride = page_stride;
+    p.row_stride = row_stride;
+    p.head_stride = head_stride;
+    p.window = window;
+    p.scale = scale;
+    cudaError_t e = w4::run_attn_paged(p, st->ws, st->err, st->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4_OK : cuda_fail(e);
+}
+
 int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top_id, const float *logits,
                 const int32_t *targets, int M, int V, long long ld, int topk, int32_t *status, void *stream)
 {

@@ -36,6 +36,22 @@ inline bool encode_rows(CUtensorMap *map, const void *p, long long rows, int hea
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Keys or values in pages: rows of a page, pages and heads lie at the call's strides;
+// boxes of 64 dims x 1 head x `br` rows of a page.
+inline bool encode_pages(CUtensorMap *map, const void *p, const Args &a, int D, int br)
+{
+    auto enc = tmap_encoder();
+    if (!enc)
+        return false;
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)1 << a.page_log2, (cuuint64_t)a.pages};
+    cuuint64_t strides[3] = {(cuuint64_t)a.head_stride * 2, (cuuint64_t)a.row_stride * 2, (cuuint64_t)a.page_stride * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)br, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Rows {
     const uint16_t *p;
     long long rows, ld;
@@ -43,7 +59,7 @@ struct Rows {
 
 // q, k, v (and for a tree the nodes' own kt, vt); a.* but the scratch is set.
 // tiles: row tiles of the call at most, over all heads and value slices.
-template <int D, bool TREE>
+template <int D, Kind KIND>
 cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Rows &kt, const Rows &vt,
                    long long tiles, bool may_cut, float *ws, int num_sms, cudaStream_t s)
 {
@@ -51,9 +67,12 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     static_assert(S::TQ == (D <= 128 ? 2 : 1) && S::NV == (D > 256 ? 2 : 1), "as in attn_tile_tokens, attn_slices");
     Maps m;
     if (!encode_rows(&m.q, q.p, q.rows, a.Hq, D, q.ld, a.G, a.tpt) ||
-        !encode_rows(&m.k, k.p, k.rows, a.Hkv, D, k.ld, 1, kKeys) ||
-        !encode_rows(&m.v, v.p, v.rows, a.Hkv, D, v.ld, 1, S::VKEYS) ||
-        (TREE && (!encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||
+        (KIND == kPaged
+             ? !encode_pages(&m.k, k.p, a, D, min(1 << a.page_log2, kKeys)) ||
+                   !encode_pages(&m.v, v.p, a, D, min(1 << a.page_log2, S::VKEYS))
+             : !encode_rows(&m.k, k.p, k.rows, a.Hkv, D, k.ld, 1, kKeys) ||
+                   !encode_rows(&m.v, v.p, v.rows, a.Hkv, D, v.ld, 1, S::VKEYS)) ||
+        (KIND == kTree && (!encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||
                   !encode_rows(&m.vt, vt.p, vt.rows, a.Hkv, D, vt.ld, 1, S::VKEYS))))
         return cudaErrorInvalidValue;
     a.ws_o = ws;
@@ -61,7 +80,7 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     a.rec = reinterpret_cast<int32_t *>(a.ws_ml + (size_t)2 * num_sms * 256 * 2);
     a.where = a.rec + 2 * num_sms;
 
-    auto kern = attn_kernel<D, TREE>;
+    auto kern = attn_kernel<D, KIND>;
     // Once per device: the attribute belongs to the kernel there.
     static std::atomic<unsigned long long> set{0};
     int dev = 0;

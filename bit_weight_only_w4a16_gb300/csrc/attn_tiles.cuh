@@ -141,11 +141,18 @@ struct Args {
     int tpt; // tokens per MMA row tile: 128 / G
     int window;
     float c; // scale * log2(e)
+    // paged: keys of a sequence through its pages [B][table_pages] of 2^page_log2 rows
+    const int32_t *table, *lens;
+    int table_pages, pages, page_log2, most_k; // most_k: keys that a table holds
+    long long page_stride, row_stride, head_stride;
 };
 
 struct Maps {
     CUtensorMap q, k, v, kt, vt;
 };
+
+// What a query row's keys are.
+enum Kind { kPrompt, kTree, kPaged };
 
 // ------------------------------------------------------------------ PTX ----
 
@@ -196,6 +203,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                       uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
                  : "memory");
 }
 
@@ -307,11 +323,25 @@ struct Seq {
     int off;    // prompt: position of query row 0; tree: position of depth 0
 };
 
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ Seq load_seq(const Args &a, int s)
 {
     Seq q;
-    if (TREE) {
+    if (KIND == kPaged) {
+        // Rows as a prompt's, or one of each sequence; a length past the table keeps its
+        // positions and loses the keys that the table has no page for.
+        if (a.cu_q) {
+            q.q0 = __ldg(a.cu_q + s);
+            q.lq = q.q0 < 0 ? 0 : max(0, max(0, min(__ldg(a.cu_q + s + 1), a.total_q)) - q.q0);
+        } else {
+            q.q0 = s;
+            q.lq = 1;
+        }
+        q.k0 = 0;
+        const int len = max(0, __ldg(a.lens + s));
+        q.lk = min(len, a.most_k);
+        q.off = len - q.lq;
+    } else if (KIND == kTree) {
         q.q0 = s * a.N;
         q.lq = a.N;
         q.k0 = s * a.T;
@@ -333,10 +363,10 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int s)
 __device__ __forceinline__ int window_start(int at, int window) { return max(0, max(at, 0) - window + 1); }
 
 // First key and one past the last that any of the tokens [t0, t0 + nt) keeps.
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ void key_range(const Args &a, const Seq &q, int t0, int nt, int &lo, int &hi)
 {
-    if (TREE) {
+    if (KIND == kTree) {
         lo = a.window > 0 ? window_start(q.off, a.window) : 0; // depth 0 sees furthest back
         hi = q.lk;
         if (a.kpos) { // any slot may hold any position
@@ -355,11 +385,11 @@ __device__ __forceinline__ void key_range(const Args &a, const Seq &q, int t0, i
 
 // Units of a row tile: its key tiles, and in a tree call one more for the tree's
 // own keys; at least one, so that rows without keys are written.
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ int tile_units(int lo, int hi)
 {
     const int n = hi > lo ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
-    return TREE ? n + 1 : max(n, 1);
+    return KIND == kTree ? n + 1 : max(n, 1);
 }
 
 // A piece: units [u, u1) of one row tile, as all warps see it.
@@ -379,21 +409,21 @@ struct Piece {
 
 // Key tile of unit x of the row tile; in a tree call the tree's own keys follow
 // the cache's.
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ bool tree_unit(const Piece &w, int x)
 {
-    return TREE && x == w.n - 1;
+    return KIND == kTree && x == w.n - 1;
 }
 __device__ __forceinline__ int key0(const Piece &w, int x) { return (w.lo / kKeys + x) * kKeys; }
 
 // A unit whose value rows need repair: keys outside [lo, hi), keys that only
 // some rows keep, recorded positions, the tree's own keys.
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ bool edge_unit(const Args &a, const Piece &w, int x)
 {
     const int k = key0(w, x);
-    if (TREE) {
-        if (tree_unit<TREE>(w, x) || a.kpos)
+    if (KIND == kTree) {
+        if (tree_unit<KIND>(w, x) || a.kpos)
             return true;
         return k + kKeys > w.hi || k < w.lo || (a.window > 0 && k < w.lo + 64);
     }
@@ -404,13 +434,13 @@ __device__ __forceinline__ bool edge_unit(const Args &a, const Piece &w, int x)
 
 // A value row's part in the product: 0 = kept by every row (or zeros already), 1 = by
 // some, 2 = by none.
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, int j)
 {
-    if (TREE) {
+    if (KIND == kTree) {
         // Rows past the last sequence's are past the tensor: copied as zeros.
         const int past = w.s == a.B - 1 ? 0 : 2;
-        if (tree_unit<TREE>(w, x))
+        if (tree_unit<KIND>(w, x))
             return j < a.N ? 1 : past;
         const int k = key0(w, x) + j;
         if (k >= a.T)
@@ -427,7 +457,7 @@ __device__ __forceinline__ int key_class(const Args &a, const Piece &w, int x, i
         return 0;
     }
     const int k = key0(w, x) + j;
-    if (k >= a.total_k - w.k0)
+    if (KIND == kPrompt && k >= a.total_k - w.k0)
         return 0; // past the tensor
     if (k >= w.hi || k < w.lo)
         return 2;
@@ -450,7 +480,7 @@ struct RowMask {
     __device__ __forceinline__ bool absent() const { return nodes == 0; }
 };
 
-template <bool TREE>
+template <Kind KIND>
 __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int tok, bool live)
 {
     RowMask m;
@@ -459,7 +489,7 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int t
     m.nodes = 0;
     if (!live)
         return m;
-    if (TREE) {
+    if (KIND == kTree) {
         const int32_t *par = a.parents + (size_t)w.s * a.N;
         int j = w.t0 + tok, d = 0, p = __ldg(par + j);
         if (p == -2) // an absent node
@@ -484,18 +514,18 @@ __device__ __forceinline__ RowMask row_mask(const Args &a, const Piece &w, int t
 
 // Adds to a stored output row (or partial) the NaN and infinite values of the
 // keys that warp 2 took out of the product and that this row keeps.
-template <int D, bool TREE, typename Add>
+template <int D, Kind KIND, typename Add>
 __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, const RowMask &m, int kvh,
                                              int dv0, int d0, int d1, Add add)
 {
 #pragma unroll 1
     for (int x = w.u; x < w.u1; ++x) {
-        if (!edge_unit<TREE>(a, w, x))
+        if (!edge_unit<KIND>(a, w, x))
             continue;
-        const bool tree = tree_unit<TREE>(w, x);
+        const bool tree = tree_unit<KIND>(w, x);
 #pragma unroll 1
         for (int j = 0; j < kKeys; ++j) {
-            if (key_class<TREE>(a, w, x, j) != 1)
+            if (key_class<KIND>(a, w, x, j) != 1)
                 continue;
             const int k = key0(w, x) + j;
             bool kept;
@@ -504,9 +534,16 @@ __device__ __forceinline__ void add_specials(const Args &a, const Piece &w, cons
                 kept = (m.nodes >> j) & 1;
                 row = a.vt + ((size_t)(w.s * (long long)a.N + j) * a.Hkv + kvh) * D;
             } else {
-                const int p = TREE && a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
+                const int p = KIND == kTree && a.kpos ? __ldg(a.kpos + (size_t)w.s * a.T + k) : k;
                 kept = p >= m.lo && p < m.hi;
-                row = a.v + (size_t)((long long)w.k0 + k) * a.ldv + (size_t)kvh * D;
+                if (KIND == kPaged) {
+                    const int pg = kept ? __ldg(a.table + (size_t)w.s * a.table_pages + (k >> a.page_log2)) : -1;
+                    kept = pg >= 0 && pg < a.pages;
+                    row = a.v + (size_t)(kept ? pg : 0) * a.page_stride +
+                          (size_t)(k & ((1 << a.page_log2) - 1)) * a.row_stride + (size_t)kvh * a.head_stride;
+                } else {
+                    row = a.v + (size_t)((long long)w.k0 + k) * a.ldv + (size_t)kvh * D;
+                }
             }
             if (!kept)
                 continue;
@@ -537,6 +574,9 @@ struct Shared {
     int xok[2][8];         // and whether their waits ended well ([parity][softmax warp])
     int cut[2][4], tiles;
     int special[4];        // piece whose value rows had NaN or infinities
+    // paged: unit's keys whose page is none of the pool, a bit for 16 keys. Keys of a unit
+    // are copied at most 8 units ahead of the softmax (half the ring's slots, and two).
+    uint32_t absent[16];
     int warp_sums[16];
     uint32_t tmem;
     volatile int abort;
@@ -615,17 +655,17 @@ __device__ __forceinline__ long long block_scan(int v, int *warp_sums, long long
 // units and TILE_COST each, at equal costs: sh.cut[e] is where this CTA's run begins
 // (e = 0) and ends (e = 1): tile index over all heads, sequence, tile within the
 // sequence, unit. sbase: space for the first row tile of each sequence.
-template <typename S, bool TREE>
+template <typename S, Kind KIND>
 __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, int tt, int HS, int &R)
 {
     if (a.B == 1) {
-        R = (load_seq<TREE>(a, 0).lq + tt - 1) / tt;
+        R = (load_seq<KIND>(a, 0).lq + tt - 1) / tt;
         if (threadIdx.x == 0)
             sbase[0] = 0;
     }
     for (int s0 = 0; a.B > 1 && s0 < a.B; s0 += S::THREADS) {
         const int s = s0 + (int)threadIdx.x;
-        const int nt = s < a.B ? (load_seq<TREE>(a, s).lq + tt - 1) / tt : 0;
+        const int nt = s < a.B ? (load_seq<KIND>(a, s).lq + tt - 1) / tt : 0;
         long long total;
         const int incl = (int)block_scan<S::THREADS>(nt, sh.warp_sums, total);
         if (s < a.B)
@@ -645,11 +685,11 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
                 y = m - 1;
         }
         s = x;
-        const Seq q = load_seq<TREE>(a, s);
+        const Seq q = load_seq<KIND>(a, s);
         const int t0 = (r - sbase[s]) * tt;
         int lo, hi;
-        key_range<TREE>(a, q, t0, min(tt, q.lq - t0), lo, hi);
-        return tile_units<TREE>(lo, hi);
+        key_range<KIND>(a, q, t0, min(tt, q.lq - t0), lo, hi);
+        return tile_units<KIND>(lo, hi);
     };
     // Thread r of the last round of row tiles: its tile's sequence, units, cost and
     // the costs up to it. With one round they serve the second pass as well.
@@ -702,11 +742,12 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
     }
 }
 
-template <int D, bool TREE>
+template <int D, Kind KIND>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
 attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using S = Shape<D>;
+    constexpr bool TREE = KIND == kTree;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t q_base = smem_addr(smem);
     const uint32_t ring = q_base + S::QBYTES;
@@ -765,12 +806,12 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         if (TREE && a.B == 1) {
             // One tree: its row tiles have the same units.
             if (threadIdx.x < 2) {
-                const Seq q = load_seq<TREE>(a, 0);
+                const Seq q = load_seq<KIND>(a, 0);
                 int lo, hi;
-                key_range<TREE>(a, q, 0, q.lq, lo, hi);
+                key_range<KIND>(a, q, 0, q.lq, lo, hi);
                 R = (q.lq + tt - 1) / tt;
                 const int extra = (long long)R * HS >= (long long)gridDim.x ? S::TILE_COST : 0;
-                const long long cost = tile_units<TREE>(lo, hi) + extra, all = cost * R * HS;
+                const long long cost = tile_units<KIND>(lo, hi) + extra, all = cost * R * HS;
                 const long long ctas = min((long long)gridDim.x, all); // a unit each at least
                 const long long x = all * min((long long)blockIdx.x + threadIdx.x, ctas) / ctas;
                 const int tile = (int)(x / cost);
@@ -780,7 +821,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 sh.cut[threadIdx.x][3] = (int)max(0ll, x - tile * cost - extra);
             }
         } else {
-            plan_run<S, TREE>(a, sh, reinterpret_cast<int *>(smem), tt, HS, R);
+            plan_run<S, KIND>(a, sh, reinterpret_cast<int *>(smem), tt, HS, R);
         }
         if (threadIdx.x == 0)
             sh.tiles = R;
@@ -812,7 +853,132 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
     auto take = [&](uint32_t p) { return wait(bars.pc_full[p % kPieces], (p / kPieces) & 1, kWaitPiece); };
     auto done = [&](uint32_t p) { mbar_arrive(smem_addr(&bars.pc_empty[p % kPieces])); };
 
-    if (warp == 0) {
+    if (KIND == kPaged && warp == 0) {
+        // ------------------------------------- copies through a page table
+        // Lane i reads the page of the i-th copy of a unit, two units ahead; one lane
+        // copies. A copy is a page's rows, or 128 keys (a value stage's) of a longer page.
+        // A page that is none of the pool, or holds no kept key, is not read: its copies
+        // lie past the pool's end and land as zeros.
+        const int clog = min(a.page_log2, 7), copies = kKeys >> clog;
+        const int vlog = min(a.page_log2, S::VKEYS == 128 ? 7 : (S::VKEYS == 64 ? 6 : 5));
+        const int in_page = (1 << a.page_log2) - 1;
+        uint32_t g = 0, piece = 0, unit = 0; // stages, pieces, units so far
+        uint32_t par = 0, onedge = 0;
+        bool ok = true;
+        auto all_wait = [&](unsigned long long &bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0;
+        };
+        for (; ok; ++piece) {
+            if (!(ok = __all_sync(0xFFFFFFFFu, take(piece))))
+                break;
+            const Piece w = sh.piece[piece % kPieces];
+            __syncwarp();
+            if (lane == 0)
+                done(piece);
+            if (w.units == 0)
+                break;
+            if (piece > 0 && !(ok = all_wait(bars.q_empty, (piece - 1) & 1)))
+                break;
+            const int kvh = w.hs / S::NV, dv0 = (w.hs % S::NV) * S::DV;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(smem_addr(&bars.q_full), (uint32_t)(w.nq * S::QB * a.tpt * a.G * 128));
+                for (int t = 0; t < w.nq; ++t)
+                    for (int c = 0; c < S::QB; ++c)
+                        tma_3d(q_base + (t * S::QB + c) * kBlock, &maps.q, 64 * c, kvh * a.G,
+                               w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
+            }
+            __syncwarp();
+            const int32_t *table = a.table + (size_t)w.s * a.table_pages;
+            auto entry = [&](int j) {
+                const int k = key0(w, w.u + j) + (lane << clog);
+                int t = -1;
+                if (j < w.units && lane < copies && k < w.hi && k + (1 << clog) > w.lo)
+                    t = __ldg(table + (k >> a.page_log2));
+                return t;
+            };
+            auto page = [&](int t) { return t >= 0 && t < a.pages ? t : a.pages; };
+            auto keys = [&](int j, int t) {
+                const int row = key0(w, w.u + j) & in_page;
+                const int mine = page(t);
+                const uint32_t out = __ballot_sync(0xFFFFFFFFu, __shfl_sync(0xFFFFFFFFu, mine, (lane & 7) >> (clog - 4)) ==
+                                                                    a.pages);
+                for (int c = 0; c < S::KC; ++c, ++g) {
+                    const uint32_t slot = g % S::NS, use = g / S::NS;
+                    if (use > 0 && !all_wait(bars.empty[slot], (use - 1) & 1))
+                        return false;
+                    const uint32_t bar = smem_addr(&bars.full[slot]);
+                    onedge &= ~(1u << slot);
+                    if (lane == 0) {
+                        if (c == 0)
+                            sh.absent[unit & 15] = out & 0xFFu;
+                        mbar_arrive_expect_tx(bar, S::STAGE);
+                    }
+                    __syncwarp();
+                    for (int i = 0; i < copies; ++i) {
+                        const int pg = __shfl_sync(0xFFFFFFFFu, mine, i);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int b = 0; b < S::KB; ++b)
+                                tma_4d(ring + slot * S::STAGE + b * kBlock + ((i << clog) * 128), &maps.k,
+                                       64 * (c * S::KB + b), kvh, row, pg, bar);
+                        }
+                        __syncwarp();
+                    }
+                }
+                ++unit;
+                return true;
+            };
+            auto values = [&](int j, int t) {
+                const bool edge = edge_unit<KIND>(a, w, w.u + j);
+                const int k0 = key0(w, w.u + j), mine = page(t);
+                for (int c = 0; c < S::VC; ++c, ++g) {
+                    const uint32_t slot = g % S::NS, use = g / S::NS;
+                    if (use > 0 && !all_wait(bars.empty[slot], (use - 1) & 1))
+                        return false;
+                    const uint32_t bar = smem_addr(edge ? &bars.edge[slot] : &bars.full[slot]);
+                    onedge = edge ? onedge | (1u << slot) : onedge & ~(1u << slot);
+                    par ^= edge ? 1u << slot : 0u;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, S::VBYTES);
+                    __syncwarp();
+                    for (int i = 0; i < (S::VKEYS >> vlog); ++i) {
+                        const int r = c * S::VKEYS + (i << vlog); // first row within the unit
+                        const int pg = __shfl_sync(0xFFFFFFFFu, mine, r >> clog);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int b = 0; b < S::DV / 64; ++b)
+                                tma_4d(ring + slot * S::STAGE + b * (S::VKEYS * 128) + ((i << vlog) * 128), &maps.v,
+                                       dv0 + 64 * b, kvh, (k0 + r) & in_page, pg, bar);
+                        }
+                        __syncwarp();
+                    }
+                }
+                return true;
+            };
+            int cur = entry(0), nxt = entry(1);
+            ok = keys(0, cur);
+            for (int j = 0; ok && j < w.units; ++j) {
+                const bool more = j + 1 < w.units;
+                const int after = entry(j + 2);
+                ok = S::PAIR ? (!more || keys(j + 1, nxt)) && values(j, cur) : values(j, cur) && (!more || keys(j + 1, nxt));
+                cur = nxt;
+                nxt = after;
+            }
+        }
+        if (!ok && lane == 0) {
+            // Copies in flight write this CTA's shared memory: let them land.
+            for (int i = 0; i < S::NS; ++i) {
+                const uint32_t uses = (g + S::NS - 1 - i) / S::NS;
+                if ((onedge >> i) & 1)
+                    mbar_wait_bounded(smem_addr(&bars.edge[i]), ((par >> i) & 1) ^ 1, 64);
+                else if (uses > 0)
+                    mbar_wait_bounded(smem_addr(&bars.full[i]), (uses - 1) & 1, 64);
+            }
+            if (piece > 0)
+                mbar_wait_bounded(smem_addr(&bars.q_full), (piece - 1) & 1, 64);
+        }
+        __syncwarp();
+    } else if (warp == 0) {
         // ---------------------------------------------------- copies
         if (elect_one()) {
             uint32_t g = 0, piece = 0;    // stages, pieces so far
@@ -835,7 +1001,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                                w.q0 + w.t0 + t * a.tpt, smem_addr(&bars.q_full));
                 auto keys = [&](int j) {
                     const int x = w.u + j;
-                    const bool tr = tree_unit<TREE>(w, x);
+                    const bool tr = tree_unit<KIND>(w, x);
                     const CUtensorMap *m = tr ? &maps.kt : &maps.k;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::KC; ++c, ++g) {
@@ -853,7 +1019,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 };
                 auto values = [&](int j) {
                     const int x = w.u + j;
-                    const bool tr = tree_unit<TREE>(w, x), edge = edge_unit<TREE>(a, w, x);
+                    const bool tr = tree_unit<KIND>(w, x), edge = edge_unit<KIND>(a, w, x);
                     const CUtensorMap *m = tr ? &maps.vt : &maps.v;
                     const int row = tr ? w.s * a.N : w.k0 + key0(w, x);
                     for (int c = 0; c < S::VC; ++c, ++g) {
@@ -1036,7 +1202,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 break;
             for (int j = 0; ok && j < units; ++j) {
                 const int x = w.u + j;
-                if (!edge_unit<TREE>(a, w, x))
+                if (!edge_unit<KIND>(a, w, x))
                     continue;
                 const uint32_t gv = base + (uint32_t)(j * (S::KC + S::VC) + S::KC) +
                                     (S::PAIR && j + 1 < units ? S::KC : 0);
@@ -1046,7 +1212,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     uint32_t cls = 0;
 #pragma unroll
                     for (int h = 0; h < S::VKEYS / 32; ++h)
-                        cls |= (uint32_t)key_class<TREE>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
+                        cls |= (uint32_t)key_class<KIND>(a, w, x, c * S::VKEYS + 32 * h + lane) << (2 * h);
                     // Units between that are no edges pass without this warp.
                     ok = __all_sync(0xFFFFFFFFu, wait(bars.edge[slot], (par >> slot) & 1, kWaitPiece));
                     if (!ok)
@@ -1116,6 +1282,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         const int tok_in = row / a.G, head = row - tok_in * a.G;
         constexpr int OC = S::PAIR ? S::DV / 2 : S::DV; // accumulator columns of this thread
         uint32_t it = 0, mine = 0, piece = 0; // units, pieces of this row tile; pieces of the run
+        uint32_t passed = 0;        // paged: units of the run before this piece
         uint32_t xs = 0;            // exchanges so far
         bool ok = true;
         // The row's two threads exchange a value, and whether their waits ended well:
@@ -1140,17 +1307,18 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             if (units == 0)
                 break;
             if (t >= w.nq) {
+                passed += units;
                 __syncwarp();
                 if (lane == 0)
                     done(piece);
                 continue;
             }
             const int tok = t * a.tpt + tok_in;
-            const RowMask rm = row_mask<TREE>(a, w, tok, tok_in < a.tpt && tok < w.nt);
+            const RowMask rm = row_mask<KIND>(a, w, tok, tok_in < a.tpt && tok < w.nt);
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < units; ++j, ++it) {
                 const int x = w.u + j, kb = key0(w, x);
-                const bool tr = tree_unit<TREE>(w, x);
+                const bool tr = tree_unit<KIND>(w, x);
                 const uint32_t b = S::PAIR ? (it & 1) : (uint32_t)t;
                 const uint32_t ph = S::PAIR ? (it >> 1) & 1 : it & 1;
                 // Kept keys of this row, one bit each; `all`: the warp keeps every key.
@@ -1192,6 +1360,16 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 if (!S::PAIR && !ok)
                     break;
                 tc_fence_after();
+                if (KIND == kPaged) {
+                    const uint32_t absent = sh.absent[(passed + j) & 15];
+                    if (absent) {
+                        all = false;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            km[h] &= ((absent >> (2 * h)) & 1u ? 0u : 0xFFFFu) |
+                                     ((absent >> (2 * h + 1)) & 1u ? 0u : 0xFFFF0000u);
+                    }
+                }
                 const uint32_t sa = s_col(b) + lanes;
                 uint32_t v[64];
                 auto mask = [&](uint32_t k0, uint32_t k1) {
@@ -1298,6 +1476,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             if (!S::PAIR && !ok)
                 break;
             // ------------------------------------------------- epilogue
+            passed += units;
             ok = ok && __all_sync(0xFFFFFFFFu, wait(bars.o_last[t], mine & 1));
             ++mine;
             if (S::PAIR)
@@ -1385,7 +1564,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             if (special)
                 __syncwarp(); // a row's output may come from its neighbour lanes
             if (special && rm.live)
-                add_specials<D, TREE>(a, w, rm, kvh, dv0, half * OC, half * OC + OC, [&](int d, float f) {
+                add_specials<D, KIND>(a, w, rm, kvh, dv0, half * OC, half * OC + OC, [&](int d, float f) {
                     if (whole) {
                         const float o = __uint_as_float((uint32_t)orow[d] << 16) + f;
                         orow[d] = (uint16_t)(pack2(o, 0.f) & 0xFFFFu);
@@ -1407,15 +1586,15 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         bool ok = true;
         Seq q = {};
         if (tile < end || (tile == end && u < end_u))
-            q = load_seq<TREE>(a, s);
+            q = load_seq<KIND>(a, s);
         while (ok && (tile < end || (tile == end && u < end_u))) {
             Piece w;
             w.hs = tile / sh.tiles;
             w.s = s;
             w.t0 = i * tt;
             w.nt = min(tt, q.lq - w.t0);
-            key_range<TREE>(a, q, w.t0, w.nt, w.lo, w.hi);
-            w.n = tile_units<TREE>(w.lo, w.hi);
+            key_range<KIND>(a, q, w.t0, w.nt, w.lo, w.hi);
+            w.n = tile_units<KIND>(w.lo, w.hi);
             w.u = u;
             w.u1 = tile == end ? end_u : w.n;
             w.units = w.u1 - w.u;
@@ -1448,7 +1627,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             while (i * tt >= q.lq) { // ends: there is another row tile
                 i = 0;
                 s = s + 1 < a.B ? s + 1 : 0;
-                q = load_seq<TREE>(a, s);
+                q = load_seq<KIND>(a, s);
             }
         }
         if (ok && (piece < (uint32_t)kPieces ||

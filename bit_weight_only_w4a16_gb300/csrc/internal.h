@@ -194,6 +194,49 @@ struct AttnTreeArgs {
 };
 cudaError_t run_attn_tree(const AttnTreeArgs &p, float *ws, int *err, int num_sms, cudaStream_t s);
 
+// Causal attention of B sequences' new tokens over caches in pages of 2^page_log2 rows:
+// key t of sequence b is row t mod 2^page_log2 of page table[b][t >> page_log2]. The
+// queries are the last of lens[b] positions. cu_q null: one token of each sequence.
+struct AttnPagedArgs {
+    uint16_t *out;
+    const uint16_t *q, *k_pages, *v_pages;
+    const int32_t *table, *lens, *cu_q;
+    int B, total_q, pages, page_log2, table_pages, Hq, Hkv, D;
+    long long ldq, ldo, page_stride, row_stride, head_stride;
+    int window;
+    float scale;
+};
+cudaError_t run_attn_paged(const AttnPagedArgs &p, float *ws, int *err, int num_sms, cudaStream_t s);
+
+// Norms of query and key heads, the rotation, and in a paged call (k_pages set) the
+// store of keys and values; see qk_norm_rope.cu. f32: q, k, v are fp32, else bf16.
+struct NormRopeArgs {
+    uint16_t *q_out, *k_out, *k_pages, *v_pages;
+    const void *q, *k, *v;
+    const float *q_weight, *k_weight, *v_weight, *inv_freq;
+    const int32_t *pos;                  // rows
+    const int32_t *table, *lens, *cu_q;  // pages
+    int M, B, Hq, Hkv, D, R, pages, page_log2, table_pages;
+    long long ldq, ldk, ldv, ldqo, ldko, page_stride, row_stride, head_stride;
+    float eps;
+    bool f32, pairs;
+    int32_t *status;
+};
+cudaError_t run_qk_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t s);
+
+// out = y + scale[i] b[i] (a[i] x) for each row's adapter i = ids[m]; see lora.cu.
+struct LoraArgs {
+    float *out;
+    const float *y;
+    const uint16_t *x, *a, *b;
+    const int32_t *ids;
+    const float *scale;
+    int M, N, K, R, L;
+    long long ldo, ldy, ldx;
+    int32_t *status;
+};
+cudaError_t run_lora(const LoraArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s);
+
 // Log probability of targets[m], entropy and the k <= 32 largest logits of M rows
 // of V fp32 logits, ld elements apart. Any output may be null.
 struct LogprobsArgs {

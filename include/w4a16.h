@@ -25,7 +25,7 @@
  *     initialised on the device (w4_init, or any earlier call on that device).
  *   - The library's split scratch is one allocation per device, which w4a16_gemm
  *     (M > 8), w4a16_gemv_hadamard, w4_attn_decode, w4_attn_decode_devpos,
- *     w4_attn_prompt, w4_attn_tree and w4_logprobs share. Two of these calls must not
+ *     w4_attn_prompt, w4_attn_tree, w4_attn_paged, w4_lora and w4_logprobs share. Two of these calls must not
  *     overlap in time on a device, whichever they are: put them on one stream or
  *     order their streams with events (judging one step on a side stream while the
  *     next one's attention runs is such an overlap). Outputs of calls that overlap
@@ -77,7 +77,7 @@ int w4_init(void);
  * cudaDeviceSynchronize. *code is 0 when every kernel finished normally. A set
  * bit means that a kernel's bounded wait on its own shared-memory pipeline ran
  * out: bit 0 the streaming decode kernel, bit 1 the prefill GEMM, bit 2 the
- * self-test below, bit 3 the prompt and tree attention. That kernel then returned without hanging; its outputs are
+ * self-test below, bit 3 the prompt, tree and paged attention. That kernel then returned without hanging; its outputs are
  * not valid, and the context stays usable.
  */
 int w4_device_error(int32_t *code);
@@ -411,6 +411,103 @@ int w4_logprobs(float *logprob, float *entropy, float *top_logprob, int32_t *top
 int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint16_t *k_tree,
                  const uint16_t *v_tree, const int32_t *path, const int32_t *count, const int32_t *pos, int L, int B,
                  int N, int T, int W, int32_t *status, void *stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (y of w4a16_gemv or
+ * w4a16_gemm, x its input): every row has an adapter of its own, or none.
+ *
+ *   out[m][n] = y[m][n] + scale[i] sum_r b[i][n][r] (sum_k a[i][r][k] x[m][k]),  i = ids[m]
+ *
+ *   An id below 0 is no adapter: out[m] = y[m]. So is one of L or more, which sets
+ *   *status = 1 (status may be NULL).
+ *
+ *   out, y  fp32 [M][N], ldo / ldy elements between rows (out may be y at the same stride)
+ *   x       bf16 [M][K], ldx elements between rows
+ *   a       bf16 [L][R][K]; b bf16 [L][N][R]; scale fp32 [L] or NULL (1); ids int32 [M]
+ *   R a multiple of 8 in 8..128 (adapters of lower rank have rows of zeros), K a multiple
+ *   of 32, N of 8 and at most 2^23; M, L >= 1; ldx a multiple of 8, ldo and ldy of 4.
+ *   16-byte aligned pointers, ids, scale and status 4-byte.
+ * Sums in fp32; a x is carried to the second product as two bf16 parts (2^-18). Any
+ * order of ids is served; past 512 rows those of one request should lie together (a
+ * tile of 64 rows takes its adapters in turn). Uses the library's split scratch:
+ * calls that need it must not run concurrently on different streams.
+ */
+int w4_lora(float *out, const float *y, const uint16_t *x, const uint16_t *a, const uint16_t *b, const int32_t *ids,
+            const float *scale, int M, int N, int K, int R, int L, long long ldo, long long ldy, long long ldx,
+            int32_t *status, void *stream);
+
+/*
+ * Norms of the query and key heads and the position rotation, one pass: from a
+ * layer's projections (w4a16_gemv, w4a16_gemm) to its attention (w4_attn_prompt,
+ * w4_attn_tree, w4_attn_decode with w4_kv_append).
+ *
+ *   u = x * weight / sqrt(mean x^2 + eps)   over a head's D elements (NULL weight: u = x)
+ *   (a, b) = (u[j], u[j + R/2]), or (u[2j], u[2j + 1]) with pairs != 0, j < R / 2:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos[m] * inv_freq[j]
+ *   elements from R on are not turned
+ *
+ *   q [M][Hq][D], k [M][Hkv][D], fp32 (f32 != 0) or bf16, ldq / ldk elements between
+ *   rows; q_out, k_out bf16, ldqo / ldko elements between rows (q_out may be q, and
+ *   k_out k, where both are bf16 at the same strides). Hkv = 0: no keys (k, k_out NULL).
+ *   q_weight, k_weight fp32 [D] or NULL; inv_freq fp32 [R / 2], radians per position
+ *   (finite, below 2^24; scaled frequencies as the caller makes them); pos int32 [M].
+ *   D in {64, 128, 256, 384, 512}; R a multiple of 8 in 0..D (0: no rotation, inv_freq
+ *   may be NULL); eps >= 0. 16-byte aligned pointers (int32 and inv_freq 4-byte), ld*
+ *   multiples of 8.
+ * Norm and turn in fp32, one rounding to bf16. The angle is exact to 2^-32 of a turn
+ * for the fp32 inv_freq at every position (whole turns are dropped in integers).
+ */
+int w4_qk_norm_rope(uint16_t *q_out, uint16_t *k_out, const void *q, const void *k, const float *q_weight,
+                    const float *k_weight, const float *inv_freq, const int32_t *pos, int M, int Hq, int Hkv, int D,
+                    int R, long long ldq, long long ldk, long long ldqo, long long ldko, int f32, int pairs, float eps,
+                    void *stream);
+
+/*
+ * The same for new tokens of B sequences whose keys and values go to a paged cache
+ * (the keys normed and turned, the values normed where v_weight is given).
+ *
+ *   Sequence b has rows cu_q[b] .. cu_q[b + 1] of q, k and v (cu_q NULL: row b, M = B)
+ *   and lens[b] positions with them: its rows are the last of those positions. Position
+ *   p is row p mod page of page table[b][p / page] of k_pages and v_pages.
+ *   A position below 0 or past the table, and one whose page lies outside [0, pages), is
+ *   not stored and sets *status = 1 (status may be NULL). Rows of no sequence (a padded
+ *   batch's last ones) are left as they are in q_out and store nothing.
+ *
+ *   k_pages, v_pages bf16 [pages][page][Hkv][D] with page_stride, row_stride and
+ *   head_stride elements between them (multiples of 8; any order of the three in
+ *   memory, no overlap); page a power of two in 16..1024; table int32 [B][table_pages];
+ *   lens int32 [B]; cu_q int32 [B + 1], ascending; B in 1..4096; table_pages * page up to
+ *   2^31 - 1025. v as k, with ldv; v_weight as k_weight. Otherwise as w4_qk_norm_rope.
+ * table, lens and cu_q are read when the kernel runs. Two tokens stored to the same place
+ * (two sequences that share their last page) leave either's row.
+ */
+int w4_qkv_paged(uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages, const void *q, const void *k, const void *v,
+                 const float *q_weight, const float *k_weight, const float *v_weight, const float *inv_freq,
+                 const int32_t *table, const int32_t *lens, const int32_t *cu_q, int B, int M, int Hq, int Hkv, int D,
+                 int R, int pages, int page, int table_pages, long long ldq, long long ldk, long long ldv,
+                 long long ldqo, long long page_stride, long long row_stride, long long head_stride, int f32,
+                 int pairs, float eps, int32_t *status, void *stream);
+
+/*
+ * Attention of new tokens (one of each sequence, or chunks of prompts, packed) over a
+ * paged cache that holds them already (w4_qkv_paged): w4_attn_prompt with keys and
+ * values found through a page table.
+ *
+ *   Rows, positions, pages, their strides and limits as w4_qkv_paged; the row at
+ *   position p keeps key positions t <= p and, when window > 0, t > p - window.
+ *   Keys past the table and those whose page lies outside [0, pages) are kept by no row.
+ *   The table's entries of pages that hold no kept position are not read from (a window's
+ *   past pages may serve others). A row that keeps no key gives zeros; a row of out that
+ *   belongs to no sequence is not written.
+ *
+ *   out, q bf16 [total_q][Hq][D], ldq / ldo elements between rows; cu_q NULL: total_q = B.
+ *   Hq / Hkv, D, scale, precision, masked values, tiles and scratch (no concurrent calls)
+ *   as w4_attn_prompt.
+ */
+int w4_attn_paged(uint16_t *out, const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                  const int32_t *table, const int32_t *lens, const int32_t *cu_q, int B, int total_q, int Hq, int Hkv,
+                  int D, int pages, int page, int table_pages, long long ldq, long long ldo, long long page_stride,
+                  long long row_stride, long long head_stride, int window, float scale, void *stream);
 
 #ifdef __cplusplus
 }
