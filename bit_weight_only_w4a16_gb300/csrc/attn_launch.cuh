@@ -52,6 +52,79 @@ inline bool encode_pages(CUtensorMap *map, const void *p, const Args &a, int D, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Partial sums' places in the scratch.
+inline void set_scratch(Args &a, float *ws, int num_sms)
+{
+    a.ws_o = ws;
+    a.ws_ml = ws + (size_t)2 * num_sms * kSlotFloats;
+    a.rec = reinterpret_cast<int32_t *>(a.ws_ml + (size_t)2 * num_sms * 256 * 2);
+    a.where = a.rec + 2 * num_sms;
+}
+
+// A kernel's dynamic shared memory, once per device: the attribute belongs to the kernel there.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<unsigned long long> &set)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !((set.load(std::memory_order_relaxed) >> dev) & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+}
+
+// What the merge takes from a call's arguments (rows_per_tile and DV are the kernel's).
+inline MergeArgs merge_args(const Args &a, int num_sms)
+{
+    MergeArgs g = {};
+    g.out = a.out;
+    g.ldo = a.ldo;
+    g.ws_o = a.ws_o;
+    g.ws_ml = a.ws_ml;
+    g.rec = a.rec;
+    g.where = a.where;
+    g.ctas = num_sms;
+    g.D = a.D;
+    g.G = a.G;
+    g.tpt = a.tpt;
+    return g;
+}
+
+// A paged call's arguments but its queries and the scratch.
+inline Args paged_args(const AttnPagedArgs &p)
+{
+    Args a = {};
+    a.out = p.out;
+    a.ldo = p.ldo;
+    a.cu_q = p.cu_q;
+    a.v = p.v_pages;
+    a.B = p.B;
+    a.total_q = p.total_q;
+    a.Hq = p.Hq;
+    a.Hkv = p.Hkv;
+    a.G = p.Hq / p.Hkv;
+    a.D = p.D;
+    a.tpt = kRowsQ / a.G;
+    a.window = p.window;
+    a.c = p.scale * 1.4426950408889634f;
+    a.table = p.table;
+    a.lens = p.lens;
+    a.table_pages = p.table_pages;
+    a.pages = p.pages;
+    a.page_log2 = p.page_log2;
+    a.most_k = p.table_pages << p.page_log2;
+    a.page_stride = p.page_stride;
+    a.row_stride = p.row_stride;
+    a.head_stride = p.head_stride;
+    return a;
+}
+
 struct Rows {
     const uint16_t *p;
     long long rows, ld;
@@ -75,25 +148,13 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
         (KIND == kTree && (!encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||
                   !encode_rows(&m.vt, vt.p, vt.rows, a.Hkv, D, vt.ld, 1, S::VKEYS))))
         return cudaErrorInvalidValue;
-    a.ws_o = ws;
-    a.ws_ml = ws + (size_t)2 * num_sms * kSlotFloats;
-    a.rec = reinterpret_cast<int32_t *>(a.ws_ml + (size_t)2 * num_sms * 256 * 2);
-    a.where = a.rec + 2 * num_sms;
+    set_scratch(a, ws, num_sms);
 
     auto kern = attn_kernel<D, KIND>;
-    // Once per device: the attribute belongs to the kernel there.
     static std::atomic<unsigned long long> set{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = allow_smem(kern, S::SMEM, set);
     if (e != cudaSuccess)
         return e;
-    if (dev >= 64 || !((set.load(std::memory_order_relaxed) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
-        if (e != cudaSuccess)
-            return e;
-        if (dev < 64)
-            set.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -107,19 +168,9 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     e = cudaLaunchKernelEx(&cfg, kern, a, m);
     if (e != cudaSuccess || !may_cut)
         return e;
-    MergeArgs g;
-    g.out = a.out;
-    g.ldo = a.ldo;
-    g.ws_o = a.ws_o;
-    g.ws_ml = a.ws_ml;
-    g.rec = a.rec;
-    g.where = a.where;
-    g.ctas = num_sms;
+    MergeArgs g = merge_args(a, num_sms);
     g.rows_per_tile = S::ROWS;
-    g.D = D;
     g.DV = S::DV;
-    g.G = a.G;
-    g.tpt = a.tpt;
     return run_merge(g, (int)(tiles < num_sms ? tiles : num_sms), s);
 }
 

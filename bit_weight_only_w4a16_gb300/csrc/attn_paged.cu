@@ -10,30 +10,11 @@ namespace w4 {
 
 cudaError_t run_attn_paged(const AttnPagedArgs &p, float *ws, int *err, int num_sms, cudaStream_t s)
 {
-    attn::Args a = {};
-    a.out = p.out;
-    a.ldo = p.ldo;
-    a.cu_q = p.cu_q;
-    a.v = p.v_pages;
+    // One token of each sequence whose heads fit a warp's products (attn_step.cu).
+    if (!p.cu_q && step_serves(p.Hq / p.Hkv, p.D))
+        return run_attn_step(p, ws, num_sms, s);
+    attn::Args a = attn::paged_args(p);
     a.err = err;
-    a.B = p.B;
-    a.total_q = p.total_q;
-    a.Hq = p.Hq;
-    a.Hkv = p.Hkv;
-    a.G = p.Hq / p.Hkv;
-    a.D = p.D;
-    a.tpt = attn::kRowsQ / a.G;
-    a.window = p.window;
-    a.c = p.scale * 1.4426950408889634f;
-    a.table = p.table;
-    a.lens = p.lens;
-    a.table_pages = p.table_pages;
-    a.pages = p.pages;
-    a.page_log2 = p.page_log2;
-    a.most_k = p.table_pages << p.page_log2;
-    a.page_stride = p.page_stride;
-    a.row_stride = p.row_stride;
-    a.head_stride = p.head_stride;
     const attn::Rows q = {p.q, p.total_q, p.ldq}, k = {p.k_pages, 0, 0}, v = {p.v_pages, 0, 0};
     auto run = [&](auto shape) {
         using S = decltype(shape);

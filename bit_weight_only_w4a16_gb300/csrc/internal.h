@@ -206,6 +206,9 @@ struct AttnPagedArgs {
     int window;
     float scale;
 };
+// One token of each sequence: served for these heads per key/value head and widths.
+bool step_serves(int G, int D);
+cudaError_t run_attn_step(const AttnPagedArgs &p, float *ws, int num_sms, cudaStream_t s);
 cudaError_t run_attn_paged(const AttnPagedArgs &p, float *ws, int *err, int num_sms, cudaStream_t s);
 
 // Norms of query and key heads, the rotation, and in a paged call (k_pages set) the

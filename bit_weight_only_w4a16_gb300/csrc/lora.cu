@@ -4,9 +4,9 @@
 //   h[m][r] = scale[i] sum_k a[i][r][k] x[m][k]            r < R <= 128
 //   out[m][n] = y[m][n] + sum_r b[i][n][r] h[m][r]
 // Two kernels: the first forms h, the second reads y and adds. h goes to the second
-// one's tensor-core product as two bf16 parts (hi = bf16(h), lo = bf16(h - hi):
-// within 2^-18 of h), because y and out are fp32 and one part (2^-9) would be
-// their largest error. Sums are fp32.
+// one's tensor-core product as three bf16 parts, each the rounding of what those before
+// it leave (within 2^-25 of h, as fp32 is): y and out are fp32, and two parts (2^-17)
+// were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32.
 //
 // Rows. A product tile is 16 rows of one adapter. Up to kGrouped rows (a decode
 // batch, every request its own adapter) a block finds its tile by ranking all rows
@@ -41,7 +41,7 @@ constexpr int kGrouped = 512; // rows that a block ranks (two of each thread)
 
 struct Args {
     LoraArgs p;
-    uint16_t *hi, *lo; // [rows of this pass][R]
+    uint16_t *h;       // [3 parts][rows of this pass][R]
     int m0, M;         // first row and rows of this pass
     int parts;         // blocks of a cluster
 };
@@ -267,11 +267,13 @@ lora_down_kernel(const Args a)
             }
             v.x *= scale;
             v.y *= scale;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-            const __nv_bfloat162 r2 = __floats2bfloat162_rn(v.x - __low2float(h), v.y - __high2float(h));
-            const size_t o = (size_t)s.row[i] * p.R + r;
-            *reinterpret_cast<__nv_bfloat162 *>(a.hi + o) = h;
-            *reinterpret_cast<__nv_bfloat162 *>(a.lo + o) = r2;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+                v.x -= __low2float(h);
+                v.y -= __high2float(h);
+                *reinterpret_cast<__nv_bfloat162 *>(a.h + ((size_t)k * a.M + s.row[i]) * p.R + r) = h;
+            }
         }
         if (a.parts > 1)
             cluster_sync(); // before another block's reads of this one's part go stale
@@ -348,19 +350,20 @@ lora_up_kernel(const Args a)
 #pragma unroll
                     for (int k = 0; k < NS; ++k) {
                         const int r = 32 * k + 8 * tq;
-                        uint4 h[2], lo[2];
+                        uint4 h[3][2];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const size_t o = row[u][q] * p.R + r;
-                            const bool have = ok[u][q] && r < p.R;
-                            h[q] = have ? __ldcg(reinterpret_cast<const uint4 *>(a.hi + o)) : make_uint4(0, 0, 0, 0);
-                            lo[q] = have ? __ldcg(reinterpret_cast<const uint4 *>(a.lo + o)) : make_uint4(0, 0, 0, 0);
-                        }
+                        for (int t = 0; t < 3; ++t)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            mma32(c[u][j], lo[0], lo[1], b[k][j]);
-                            mma32(c[u][j], h[0], h[1], b[k][j]);
-                        }
+                            for (int q = 0; q < 2; ++q)
+                                h[t][q] = ok[u][q] && r < p.R
+                                              ? __ldcg(reinterpret_cast<const uint4 *>(
+                                                    a.h + ((size_t)t * a.M + row[u][q]) * p.R + r))
+                                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int t = 2; t >= 0; --t) // small parts first
+                                mma32(c[u][j], h[t][0], h[t][1], b[k][j]);
                     }
             }
 #pragma unroll
@@ -463,15 +466,14 @@ cudaError_t pass(const Args &a, int down_tiles, int up_tiles, int num_sms, cudaS
 
 cudaError_t run_lora(const LoraArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s)
 {
-    // Rows whose h fits the scratch go in one pass (65536 at R = 128).
-    const long long most = (long long)(ws_floats / (size_t)p.R) / 64 * 64;
+    // Rows whose h fits the scratch go in one pass (53000 or so at R = 128).
+    const long long most = (long long)(ws_floats * 4 / (6 * (size_t)p.R)) / 64 * 64;
     for (long long m0 = 0; m0 < p.M; m0 += most) {
         Args a = {};
         a.p = p;
         a.m0 = (int)m0;
         a.M = (int)(p.M - m0 < most ? p.M - m0 : most);
-        a.hi = reinterpret_cast<uint16_t *>(ws);
-        a.lo = a.hi + (size_t)a.M * p.R;
+        a.h = reinterpret_cast<uint16_t *>(ws);
         cudaError_t e;
         if (a.M <= kGrouped) {
             // Each adapter has at most one tile that is not full.

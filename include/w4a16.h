@@ -427,7 +427,7 @@ int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint
  *   R a multiple of 8 in 8..128 (adapters of lower rank have rows of zeros), K a multiple
  *   of 32, N of 8 and at most 2^23; M, L >= 1; ldx a multiple of 8, ldo and ldy of 4.
  *   16-byte aligned pointers, ids, scale and status 4-byte.
- * Sums in fp32; a x is carried to the second product as two bf16 parts (2^-18). Any
+ * Sums in fp32; a x is carried to the second product as three bf16 parts (2^-25). Any
  * order of ids is served; past 512 rows those of one request should lie together (a
  * tile of 64 rows takes its adapters in turn). Uses the library's split scratch:
  * calls that need it must not run concurrently on different streams.
