@@ -652,9 +652,10 @@ int check_pages(int B, int Hkv, int D, int pages, int page, int table_pages, lon
     for (int i = 0; i < 3; ++i)
         if (d[i].stride < D || d[i].stride > (1ll << 38)) // a tensor copy's strides end at 2^40 bytes
             return W4_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i)
-        if (d[i].stride % 8 != 0)
-            return W4_ERR_MISALIGNED;
+    if (head_stride % 64 != 0 || row_stride % 8 != 0 || page_stride % 8 != 0)
+        return W4_ERR_MISALIGNED;
+    if (head_stride / 64 * Hkv >= (1ll << 31)) // a tensor copy's coordinates
+        return W4_ERR_UNSUPPORTED;
     for (int i = 0; i < 2; ++i) // ascending strides
         for (int j = 0; j < 2 - i; ++j)
             if (d[j].stride > d[j + 1].stride || (d[j].stride == d[j + 1].stride && d[j].n > d[j + 1].n)) {

@@ -36,18 +36,21 @@ inline bool encode_rows(CUtensorMap *map, const void *p, long long rows, int hea
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Keys or values in pages: rows of a page, pages and heads lie at the call's strides;
-// boxes of 64 dims x 1 head x `br` rows of a page.
-inline bool encode_pages(CUtensorMap *map, const void *p, const Args &a, int D, int br)
+// Keys or values in pages: rows of a page, pages and heads lie at the call's strides.
+// A box is `br` rows of a page (a multiple of 8) and `blocks` blocks of 64 dims; heads are
+// so many blocks apart, which leaves the other dimensions to rows (in eights) and pages.
+inline bool encode_pages(CUtensorMap *map, const void *p, const Args &a, int D, int br, int blocks)
 {
     auto enc = tmap_encoder();
     if (!enc)
         return false;
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)1 << a.page_log2, (cuuint64_t)a.pages};
-    cuuint64_t strides[3] = {(cuuint64_t)a.head_stride * 2, (cuuint64_t)a.row_stride * 2, (cuuint64_t)a.page_stride * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)br, 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+    cuuint64_t dims[5] = {64, 8, (cuuint64_t)(a.Hkv - 1) * a.head_blocks + D / 64, (cuuint64_t)1 << (a.page_log2 - 3),
+                          (cuuint64_t)a.pages};
+    cuuint64_t strides[4] = {(cuuint64_t)a.row_stride * 2, 128, (cuuint64_t)a.row_stride * 16,
+                             (cuuint64_t)a.page_stride * 2};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)blocks, (cuuint32_t)br / 8, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(p), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -122,6 +125,7 @@ inline Args paged_args(const AttnPagedArgs &p)
     a.page_stride = p.page_stride;
     a.row_stride = p.row_stride;
     a.head_stride = p.head_stride;
+    a.head_blocks = (int)(p.head_stride / 64);
     return a;
 }
 
@@ -141,8 +145,8 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
     Maps m;
     if (!encode_rows(&m.q, q.p, q.rows, a.Hq, D, q.ld, a.G, a.tpt) ||
         (KIND == kPaged
-             ? !encode_pages(&m.k, k.p, a, D, min(1 << a.page_log2, kKeys)) ||
-                   !encode_pages(&m.v, v.p, a, D, min(1 << a.page_log2, S::VKEYS))
+             ? !encode_pages(&m.k, k.p, a, D, min(1 << a.page_log2, kKeys), S::KB) ||
+                   !encode_pages(&m.v, v.p, a, D, min(1 << a.page_log2, S::VKEYS), S::DV / 64)
              : !encode_rows(&m.k, k.p, k.rows, a.Hkv, D, k.ld, 1, kKeys) ||
                    !encode_rows(&m.v, v.p, v.rows, a.Hkv, D, v.ld, 1, S::VKEYS)) ||
         (KIND == kTree && (!encode_rows(&m.kt, kt.p, kt.rows, a.Hkv, D, kt.ld, 1, kKeys) ||

@@ -23,7 +23,7 @@
 //     tile only: what is not kept is never read.
 // Work: the tiles of all (sequence, key/value head) segments, in order, cut into equal
 // runs, one per block; a block's warps take turns and join their sums at a segment's end.
-// A segment that was cut leaves partial sums, merged in key order by attn_merge.cu.
+// A segment that was cut leaves partial sums, which a second kernel joins in a fixed order.
 #include "attn_launch.cuh"
 
 namespace w4 {
@@ -36,15 +36,17 @@ constexpr int kTile = 16;
 // HT: groups of 8 heads.
 template <int D, int HT>
 struct StepShape {
-    static constexpr int W = D <= 128 ? 8 : (D == 256 ? 4 : 2);                     // warps
-    static constexpr int ST = HT == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 6 : (D == 384 ? 4 : 3)); // tiles of a warp's ring
-    static constexpr int HALF = kTile * D * 2;   // keys (or values) of a tile
-    static constexpr int RING = ST * 2 * HALF;   // of a warp
+    static constexpr int W = D <= 128 || (D == 256 && HT == 1) ? 8 : 4; // warps
+    static constexpr int HALF = kTile * D * 2;   // keys (or values) of a tile: a copy
     static constexpr int HS = D + 4;             // floats between heads of the joined sums (no bank twice)
     static constexpr int HEADS = 8 * HT;
-    static constexpr size_t JOIN = (size_t)W * HEADS * HS * 4;
-    static constexpr size_t SMEM = (size_t)W * RING + JOIN + (size_t)W * HEADS * 8;
-    static_assert(SMEM <= 232448 - 1024, "shared memory");
+    static constexpr size_t JOIN = (size_t)(W / 2) * HEADS * (HS * 4 + 8);
+    // Copies in a warp's ring: what shared memory holds (3 to 12).
+    static constexpr int FIT = (int)((230400 - JOIN) / ((size_t)W * HALF));
+    static constexpr int ST = FIT > 12 ? 12 : FIT;
+    static constexpr int RING = ST * HALF;
+    static constexpr size_t SMEM = (size_t)W * RING + JOIN;
+    static_assert(ST >= 3 && SMEM <= 230400, "shared memory");
 };
 
 struct StepArgs {
@@ -154,7 +156,7 @@ step_kernel(const StepArgs p)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
     const uint32_t ring = smem_addr(smem) + w * S::RING;
     float *join = reinterpret_cast<float *>(smem + (size_t)S::W * S::RING);
-    float2 *join_ml = reinterpret_cast<float2 *>(smem + (size_t)S::W * S::RING + S::JOIN); // [W][HEADS]
+    float2 *join_ml = reinterpret_cast<float2 *>(join + (size_t)(S::W / 2) * S::HEADS * S::HS); // [W / 2][HEADS]
     pdl_launch_dependents();
     pdl_wait();
 
@@ -191,7 +193,7 @@ step_kernel(const StepArgs p)
             break;
     }
     __syncthreads();
-    int cont = 0, begins = 0; // as in attn_tiles.cuh
+    int begins = 0, begins_b = 0, begins_h = 0; // parts of the cut segment that this run begins, if any
     if (x0 < x1) {
         Walk c;
         c.b = s_seq;
@@ -202,7 +204,7 @@ step_kernel(const StepArgs p)
         Walk f = c; // what is copied next
         long long xf = x0 + w;
 
-        // Tile xf into ring slot `slot`, then on to the warp's next tile.
+        // The next tile's page, a tile ahead of its copies.
         auto page_of = [&]() {
             int pg = -1;
             if (xf < x1) {
@@ -214,34 +216,59 @@ step_kernel(const StepArgs p)
             return pg;
         };
         int pg = page_of();
-        uint32_t paged = 0; // whether the tiles copied last have a page, the newest in bit 0
-        auto issue = [&](int slot) {
-            paged <<= 1;
-            if (xf < x1) {
-                const int key = (f.t0 + (int)(xf - f.base)) * kTile;
-                const bool have = pg >= 0 && pg < a.pages;
-                paged |= have ? 1u : 0u;
-                const int r0 = have ? f.lo - key : kTile, r1 = have ? f.len - key : 0; // kept rows
-                const size_t at = (size_t)(have ? pg : 0) * a.page_stride +
-                                  (size_t)(key & ((1 << a.page_log2) - 1)) * a.row_stride + (size_t)f.h * a.head_stride;
-                const uint32_t to = ring + slot * 2 * S::HALF;
+        uint32_t paged = 0;   // whether the tiles copied last have a page, the newest in bit 0
+        size_t at = 0;        // the tile being copied: its first row, its kept rows
+        int r0 = 0, r1 = 0;
+        auto rows = [&](const uint16_t *p, int slot) {
+            const uint32_t to = ring + slot * S::HALF;
 #pragma unroll
-                for (int i = 0; i < kTile * CH / 32; ++i) {
-                    const int e = lane + 32 * i, r = e / CH, j = e - r * CH;
-                    const bool kept = r >= r0 && r < r1;
-                    const size_t from = at + (kept ? (size_t)r * a.row_stride : 0) + 8 * j;
-                    const uint32_t so = to + r * (D * 2) + ((j ^ (r & 7)) << 4);
-                    copy16(so, p.k + from, kept);
-                    copy16(so + S::HALF, a.v + from, kept);
-                }
-                xf += S::W;
-                pg = page_of();
+            for (int i = 0; i < kTile * CH / 32; ++i) {
+                const int e = lane + 32 * i, r = e / CH, j = e - r * CH;
+                const bool kept = r >= r0 && r < r1;
+                copy16(to + r * (D * 2) + ((j ^ (r & 7)) << 4), p + at + (kept ? (size_t)r * a.row_stride : 0) + 8 * j,
+                       kept);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        bool copying = false;
+        // Keys of tile xf, then its values.
+        auto issue_keys = [&](int slot) {
+            paged <<= 1;
+            copying = xf < x1;
+            if (copying) {
+                const int key = (f.t0 + (int)(xf - f.base)) * kTile;
+                const bool have = pg >= 0 && pg < a.pages;
+                paged |= have ? 1u : 0u;
+                r0 = have ? f.lo - key : kTile;
+                r1 = have ? f.len - key : 0;
+                at = (size_t)(have ? pg : 0) * a.page_stride +
+                     (size_t)(key & ((1 << a.page_log2) - 1)) * a.row_stride + (size_t)f.h * a.head_stride;
+                rows(p.k, slot);
+                xf += S::W;
+                pg = page_of();
+            } else {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        };
+        auto issue_values = [&](int slot) {
+            if (copying)
+                rows(a.v, slot);
+            else
+                asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
         for (int i = 0; i < S::ST - 1; ++i)
-            issue(i);
+            (i & 1) ? issue_values(i) : issue_keys(i);
+        // Copy number n + ST - 1 while copy n is worked on: the same half when ST is odd.
+        auto ahead = [&](bool keys, int slot) {
+            const int to = slot == 0 ? S::ST - 1 : slot - 1;
+            if (keys == (S::ST % 2 == 1))
+                issue_keys(to);
+            else
+                issue_values(to);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::ST - 1) : "memory");
+            __syncwarp(); // every lane's copies are in place
+        };
 
         int slot = 0;
         long long x = x0 + w;
@@ -272,10 +299,8 @@ step_kernel(const StepArgs p)
             }
 #pragma unroll 1
             for (; x < end; x += S::W) {
-                issue(slot == 0 ? S::ST - 1 : slot - 1);
-                asm volatile("cp.async.wait_group %0;" ::"n"(S::ST - 1) : "memory");
-                __syncwarp(); // every lane's copies of the tile are in place
-                const uint32_t kb = ring + slot * 2 * S::HALF, vb = kb + S::HALF;
+                ahead(true, slot);
+                const uint32_t kb = ring + slot * S::HALF;
                 slot = slot == S::ST - 1 ? 0 : slot + 1;
                 float sc[HT][2][4];
 #pragma unroll
@@ -297,7 +322,7 @@ step_kernel(const StepArgs p)
                 }
                 // Kept keys: rows g and g + 8 of the tile. A page that is none left zeros.
                 const int key = (c.t0 + (int)(x - c.base)) * kTile;
-                const bool have = (paged >> (S::ST - 1)) & 1u;
+                const bool have = (paged >> ((S::ST - 1) / 2)) & 1u;
                 const bool k0 = have && key + g >= c.lo && key + g < c.len;
                 const bool k1 = have && key + g + 8 >= c.lo && key + g + 8 < c.len;
                 uint32_t hi[HT][2], lw[HT][2];
@@ -343,9 +368,12 @@ step_kernel(const StepArgs p)
                             o[t][s][3] *= al[t][1];
                         }
                 }
+                __syncwarp(); // all lanes have read the keys, whose slot the next copies go to
+                ahead(false, slot);
                 {
                     const int row = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
-                    const uint32_t ra = vb + row * (D * 2);
+                    const uint32_t ra = ring + slot * S::HALF + row * (D * 2);
+                    slot = slot == S::ST - 1 ? 0 : slot + 1;
 #pragma unroll
                     for (int s = 0; s < KS; ++s) {
                         uint32_t r[4];
@@ -357,28 +385,64 @@ step_kernel(const StepArgs p)
                         }
                     }
                 }
-                __syncwarp(); // all lanes have read the slot that the next copies go to
+                __syncwarp(); // and the values
             }
             // ------------------------------------- the warps' sums joined
+            // The upper half of the warps leave theirs, the lower half add them and leave the sums.
 #pragma unroll
-            for (int t = 0; t < HT; ++t) {
+            for (int t = 0; t < HT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float s = l[t][i];
-                    s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
-                    s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
-                    s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
-                    if (g == 0)
-                        join_ml[w * S::HEADS + 8 * t + 2 * tq + i] = make_float2(m[t][i], s);
+                    l[t][i] += __shfl_xor_sync(0xFFFFFFFFu, l[t][i], 4);
+                    l[t][i] += __shfl_xor_sync(0xFFFFFFFFu, l[t][i], 8);
+                    l[t][i] += __shfl_xor_sync(0xFFFFFFFFu, l[t][i], 16);
                 }
-                float *to = join + (size_t)(w * S::HEADS + 8 * t + 2 * tq) * S::HS + g;
+            const int u = w & (S::W / 2 - 1);
+            float *mine = join + (size_t)(u * S::HEADS + 2 * tq) * S::HS + g;
+            auto leave = [&]() {
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    to[16 * s] = o[t][s][0];
-                    to[16 * s + S::HS] = o[t][s][1];
-                    to[16 * s + 8] = o[t][s][2];
-                    to[16 * s + 8 + S::HS] = o[t][s][3];
+                for (int t = 0; t < HT; ++t) {
+                    float *to = mine + (size_t)8 * t * S::HS;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        to[16 * s] = o[t][s][0];
+                        to[16 * s + S::HS] = o[t][s][1];
+                        to[16 * s + 8] = o[t][s][2];
+                        to[16 * s + 8 + S::HS] = o[t][s][3];
+                    }
+                    if (g == 0) {
+                        join_ml[u * S::HEADS + 8 * t + 2 * tq] = make_float2(m[t][0], l[t][0]);
+                        join_ml[u * S::HEADS + 8 * t + 2 * tq + 1] = make_float2(m[t][1], l[t][1]);
+                    }
                 }
+            };
+            if (w >= S::W / 2)
+                leave();
+            __syncthreads();
+            if (w < S::W / 2) {
+#pragma unroll
+                for (int t = 0; t < HT; ++t) {
+                    const float *from = mine + (size_t)8 * t * S::HS;
+                    float fa[2], fb[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 ml = join_ml[u * S::HEADS + 8 * t + 2 * tq + i];
+                        const float M = fmaxf(m[t][i], ml.x);
+                        fa[i] = m[t][i] == -INFINITY ? 0.f : ex2(m[t][i] - M);
+                        fb[i] = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                        m[t][i] = M;
+                        l[t][i] = l[t][i] * fa[i] + ml.y * fb[i];
+                    }
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        o[t][s][0] = o[t][s][0] * fa[0] + from[16 * s] * fb[0];
+                        o[t][s][1] = o[t][s][1] * fa[1] + from[16 * s + S::HS] * fb[1];
+                        o[t][s][2] = o[t][s][2] * fa[0] + from[16 * s + 8] * fb[0];
+                        o[t][s][3] = o[t][s][3] * fa[1] + from[16 * s + 8 + S::HS] * fb[1];
+                    }
+                }
+                __syncwarp(); // the lanes' heads' sums have been read
+                leave();
             }
             __syncthreads();
             const bool first = xs == c.base, last = end == c.base + c.n, whole = first && last;
@@ -387,20 +451,20 @@ step_kernel(const StepArgs p)
                 const int h = e / (D / 4), d4 = e - h * (D / 4);
                 float M = -INFINITY;
 #pragma unroll
-                for (int u = 0; u < S::W; ++u)
-                    M = fmaxf(M, join_ml[u * S::HEADS + h].x);
+                for (int v = 0; v < S::W / 2; ++v)
+                    M = fmaxf(M, join_ml[v * S::HEADS + h].x);
                 float L = 0.f;
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int u = 0; u < S::W; ++u) {
-                    const float2 ml = join_ml[u * S::HEADS + h];
+                for (int v = 0; v < S::W / 2; ++v) {
+                    const float2 ml = join_ml[v * S::HEADS + h];
                     const float fu = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-                    const float4 v = *reinterpret_cast<const float4 *>(join + (size_t)(u * S::HEADS + h) * S::HS + 4 * d4);
+                    const float4 z = *reinterpret_cast<const float4 *>(join + (size_t)(v * S::HEADS + h) * S::HS + 4 * d4);
                     L = fmaf(fu, ml.y, L);
-                    y.x = fmaf(fu, v.x, y.x);
-                    y.y = fmaf(fu, v.y, y.y);
-                    y.z = fmaf(fu, v.z, y.z);
-                    y.w = fmaf(fu, v.w, y.w);
+                    y.x = fmaf(fu, z.x, y.x);
+                    y.y = fmaf(fu, z.y, y.y);
+                    y.z = fmaf(fu, z.z, y.z);
+                    y.w = fmaf(fu, z.w, y.w);
                 }
                 if (whole) {
                     const float inv = L == 0.f ? 0.f : 1.f / L; // nothing kept: zeros
@@ -409,22 +473,16 @@ step_kernel(const StepArgs p)
                     b.y = pack2(y.z * inv, y.w * inv);
                     *reinterpret_cast<uint2 *>(a.out + (size_t)c.b * a.ldo + (size_t)(c.h * a.G + h) * D + 4 * d4) = b;
                 } else {
-                    *reinterpret_cast<float4 *>(a.ws_o + (size_t)part * kSlotFloats + ((size_t)d4 * S::HEADS + h) * 4) = y;
+                    *reinterpret_cast<float4 *>(a.ws_o + (size_t)part * kSlotFloats + (size_t)h * D + 4 * d4) = y;
                     if (d4 == 0)
                         *reinterpret_cast<float2 *>(a.ws_ml + ((size_t)part * 256 + h) * 2) = make_float2(M, L);
                 }
             }
             if (!whole && first) {
-                begins = 1;
-                if (tid == 0) {
-                    int32_t *at = a.where + 4 * blockIdx.x;
-                    at[0] = c.b;
-                    at[1] = 1;
-                    at[2] = c.h;
-                    at[3] = 0;
-                }
-            } else if (!whole) {
-                cont = last ? 3 : 1;
+                // The block that has the segment's last tile: the largest one whose run begins at or before it.
+                begins = (int)(((c.base + c.n) * blocks - 1) / tot) - (int)blockIdx.x + 1;
+                begins_b = c.b;
+                begins_h = c.h;
             }
             xs = end;
             if (xs < x1)
@@ -433,7 +491,112 @@ step_kernel(const StepArgs p)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     if (tid == 0)
-        *reinterpret_cast<int2 *>(a.rec + 2 * blockIdx.x) = make_int2(cont, begins);
+        *reinterpret_cast<int4 *>(a.rec + 4 * blockIdx.x) = make_int4(begins, begins_b, begins_h, 0);
+}
+
+// Joins the parts of the cut segments: part p of one that block c begins is slot 2 c + 1 for p = 0,
+// else 2 (c + p). Block (x, y): the x-th cut segment, one head, 128 of its dims; 8 threads share a
+// float4, each with every eighth part, added in the order of the threads.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
+step_join_kernel(const Args a, int blocks)
+{
+    constexpr int NW = kJoinThreads / 32, BATCH = 8;
+    __shared__ int s_warp[NW], s_pick[4];
+    __shared__ float s_max[NW], s_sum[NW], s_f[kJoinThreads];
+    __shared__ float4 s_y[NW][32];
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    int4 rec = tid < blocks ? __ldcg(reinterpret_cast<const int4 *>(a.rec + 4 * tid)) : make_int4(0, 0, 0, 0);
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, rec.x > 0);
+    if (lane == 0)
+        s_warp[w] = __popc(v);
+    if (tid == 0)
+        s_pick[0] = 0;
+    __syncthreads();
+    int before = __popc(v & ((1u << lane) - 1u));
+    for (int i = 0; i < NW; ++i)
+        before += i < w ? s_warp[i] : 0;
+    if (rec.x > 0 && before == (int)blockIdx.x) {
+        s_pick[0] = rec.x;
+        s_pick[1] = tid;
+        s_pick[2] = rec.y;
+        s_pick[3] = rec.z;
+    }
+    __syncthreads();
+    const int n = s_pick[0], c = s_pick[1];
+    if (n == 0)
+        return;
+    const int per = (a.D + 127) / 128, h = (int)blockIdx.y / per, d = ((int)blockIdx.y % per) * 128 + 4 * lane;
+    auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)); };
+    auto load = [&](int p) {
+        return p < n && d < a.D ? __ldcg(reinterpret_cast<const float4 *>(a.ws_o + slot(p) * kSlotFloats + (size_t)h * a.D + d))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 x[BATCH]; // the first parts are asked for before the weights
+#pragma unroll
+    for (int q = 0; q < BATCH; ++q)
+        x[q] = load(w + q * NW);
+    const float2 ml = tid < n ? __ldcg(reinterpret_cast<const float2 *>(a.ws_ml + (slot(tid) * 256 + h) * 2))
+                              : make_float2(-INFINITY, 0.f);
+    float M = ml.x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+    if (lane == 0)
+        s_max[w] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+        M = fmaxf(M, s_max[i]);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    s_f[tid] = f;
+    float L = f * ml.y;
+#pragma unroll
+    for (int k = 16; k; k >>= 1)
+        L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
+    if (lane == 0)
+        s_sum[w] = L;
+    __syncthreads();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = w;; p0 += BATCH * NW) {
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+            const int p = p0 + q * NW;
+            const float e = p < n ? s_f[p] : 0.f;
+            y.x = fmaf(x[q].x, e, y.x);
+            y.y = fmaf(x[q].y, e, y.y);
+            y.z = fmaf(x[q].z, e, y.z);
+            y.w = fmaf(x[q].w, e, y.w);
+        }
+        if (p0 + BATCH * NW >= n)
+            break;
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q)
+            x[q] = load(p0 + (BATCH + q) * NW);
+    }
+    s_y[w][lane] = y;
+    __syncthreads();
+    if (w == 0 && d < a.D) {
+        L = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            L += s_sum[i];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) {
+            const float4 z = s_y[i][lane];
+            y.x += z.x;
+            y.y += z.y;
+            y.z += z.z;
+            y.w += z.w;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint2 b;
+        b.x = pack2(y.x * inv, y.y * inv);
+        b.y = pack2(y.z * inv, y.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + (size_t)s_pick[2] * a.ldo + (size_t)(s_pick[3] * a.G + h) * a.D + d) = b;
+    }
 }
 
 template <int D, int HT>
@@ -460,10 +623,12 @@ cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t
     const long long segments = (long long)p.a.B * p.a.Hkv;
     if (e != cudaSuccess || p.a.most_k <= kTile) // a segment of one tile is never cut
         return e;
-    MergeArgs g = merge_args(p.a, num_sms);
-    g.rows_per_tile = S::HEADS;
-    g.DV = D;
-    return run_merge(g, (int)(segments < num_sms ? segments : num_sms), s);
+    if (num_sms > kJoinThreads) // a thread for each block's record and part
+        return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)(segments < num_sms ? segments : num_sms), (unsigned)(p.a.G * ((D + 127) / 128)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, step_join_kernel, p.a, num_sms);
 }
 
 } // namespace

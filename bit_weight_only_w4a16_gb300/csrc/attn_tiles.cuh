@@ -145,6 +145,7 @@ struct Args {
     const int32_t *table, *lens;
     int table_pages, pages, page_log2, most_k; // most_k: keys that a table holds
     long long page_stride, row_stride, head_stride;
+    int head_blocks; // blocks of 64 elements between heads
 };
 
 struct Maps {
@@ -156,23 +157,24 @@ enum Kind { kPrompt, kTree, kPaged };
 
 // ------------------------------------------------------------------ PTX ----
 
-__device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr)
+// `rows8`: bytes between groups of 8 rows (x 128 B).
+__device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr, uint32_t rows8 = 1024)
 {
     uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
     d |= (uint64_t)1 << 16;
-    d |= (uint64_t)(1024 >> 4) << 32; // 8 rows x 128 B
+    d |= (uint64_t)(rows8 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61; // 128-byte swizzle
     return d;
 }
 
 // The same swizzle with the other dimension contiguous: 64 dims per 128-byte
-// row, `group` bytes between blocks of 64 dims, 1024 between blocks of 8 keys.
-__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t group)
+// row, `group` bytes between blocks of 64 dims, `rows8` between blocks of 8 keys.
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, uint32_t group, uint32_t rows8 = 1024)
 {
     uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
     d |= (uint64_t)(group >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)(rows8 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
@@ -206,12 +208,11 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
                  : "memory");
 }
 
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                       uint32_t bar)
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, int c2, int c3, int c4, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(0), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
                  : "memory");
 }
 
@@ -748,6 +749,9 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
     using S = Shape<D>;
     constexpr bool TREE = KIND == kTree;
+    // Stages of keys and values: [block of 64 dims][row][128 B], or for pages [group of 8
+    // rows][block][row][128 B].
+    constexpr bool ROWS8 = KIND == kPaged;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t q_base = smem_addr(smem);
     const uint32_t ring = q_base + S::QBYTES;
@@ -855,13 +859,15 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 
     if (KIND == kPaged && warp == 0) {
         // ------------------------------------- copies through a page table
-        // Lane i reads the page of the i-th copy of a unit, two units ahead; one lane
-        // copies. A copy is a page's rows, or 128 keys (a value stage's) of a longer page.
-        // A page that is none of the pool, or holds no kept key, is not read: its copies
-        // lie past the pool's end and land as zeros.
+        // A copy is a page's rows, or 128 keys (a value stage's) of a longer page, with all
+        // blocks of 64 dims of the stage (groups of 8 rows lie outside the blocks: ROWS8).
+        // Lane i has the page of a unit's i-th copy, read two units ahead, and makes that
+        // copy: one thread that made all of them needed 250 cycles for each. A page that is
+        // none of the pool, or holds no kept key, is not read: its copies lie past the pool's
+        // end and land as zeros.
         const int clog = min(a.page_log2, 7), copies = kKeys >> clog;
         const int vlog = min(a.page_log2, S::VKEYS == 128 ? 7 : (S::VKEYS == 64 ? 6 : 5));
-        const int in_page = (1 << a.page_log2) - 1;
+        const int vcopies = S::VKEYS >> vlog, in_page = (1 << a.page_log2) - 1;
         uint32_t g = 0, piece = 0, unit = 0; // stages, pieces, units so far
         uint32_t par = 0, onedge = 0;
         bool ok = true;
@@ -889,6 +895,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             }
             __syncwarp();
             const int32_t *table = a.table + (size_t)w.s * a.table_pages;
+            const int kblock = kvh * a.head_blocks, vblock = kblock + dv0 / 64;
             auto entry = [&](int j) {
                 const int k = key0(w, w.u + j) + (lane << clog);
                 int t = -1;
@@ -898,41 +905,35 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             };
             auto page = [&](int t) { return t >= 0 && t < a.pages ? t : a.pages; };
             auto keys = [&](int j, int t) {
-                const int row = key0(w, w.u + j) & in_page;
-                const int mine = page(t);
+                const int row = (key0(w, w.u + j) & in_page) >> 3, mine = page(t);
                 const uint32_t out = __ballot_sync(0xFFFFFFFFu, __shfl_sync(0xFFFFFFFFu, mine, (lane & 7) >> (clog - 4)) ==
                                                                     a.pages);
+                if (lane == 0)
+                    sh.absent[unit & 15] = out & 0xFFu;
+                ++unit;
                 for (int c = 0; c < S::KC; ++c, ++g) {
                     const uint32_t slot = g % S::NS, use = g / S::NS;
                     if (use > 0 && !all_wait(bars.empty[slot], (use - 1) & 1))
                         return false;
                     const uint32_t bar = smem_addr(&bars.full[slot]);
                     onedge &= ~(1u << slot);
-                    if (lane == 0) {
-                        if (c == 0)
-                            sh.absent[unit & 15] = out & 0xFFu;
+                    if (lane == 0)
                         mbar_arrive_expect_tx(bar, S::STAGE);
-                    }
                     __syncwarp();
-                    for (int i = 0; i < copies; ++i) {
-                        const int pg = __shfl_sync(0xFFFFFFFFu, mine, i);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int b = 0; b < S::KB; ++b)
-                                tma_4d(ring + slot * S::STAGE + b * kBlock + ((i << clog) * 128), &maps.k,
-                                       64 * (c * S::KB + b), kvh, row, pg, bar);
-                        }
-                        __syncwarp();
-                    }
+                    if (lane < copies)
+                        tma_5d(ring + slot * S::STAGE + (lane << clog) * (S::KB * 128), &maps.k, kblock + c * S::KB, row,
+                               mine, bar);
+                    __syncwarp();
                 }
-                ++unit;
                 return true;
             };
             auto values = [&](int j, int t) {
                 const bool edge = edge_unit<KIND>(a, w, w.u + j);
-                const int k0 = key0(w, w.u + j), mine = page(t);
+                const int row = key0(w, w.u + j) & in_page, mine = page(t);
                 for (int c = 0; c < S::VC; ++c, ++g) {
                     const uint32_t slot = g % S::NS, use = g / S::NS;
+                    const int r = c * S::VKEYS + (lane << vlog); // this lane's first row of the unit
+                    const int pg = __shfl_sync(0xFFFFFFFFu, mine, (r >> clog) & 7);
                     if (use > 0 && !all_wait(bars.empty[slot], (use - 1) & 1))
                         return false;
                     const uint32_t bar = smem_addr(edge ? &bars.edge[slot] : &bars.full[slot]);
@@ -941,17 +942,10 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                     if (lane == 0)
                         mbar_arrive_expect_tx(bar, S::VBYTES);
                     __syncwarp();
-                    for (int i = 0; i < (S::VKEYS >> vlog); ++i) {
-                        const int r = c * S::VKEYS + (i << vlog); // first row within the unit
-                        const int pg = __shfl_sync(0xFFFFFFFFu, mine, r >> clog);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int b = 0; b < S::DV / 64; ++b)
-                                tma_4d(ring + slot * S::STAGE + b * (S::VKEYS * 128) + ((i << vlog) * 128), &maps.v,
-                                       dv0 + 64 * b, kvh, (k0 + r) & in_page, pg, bar);
-                        }
-                        __syncwarp();
-                    }
+                    if (lane < vcopies)
+                        tma_5d(ring + slot * S::STAGE + (lane << vlog) * (S::DV * 2), &maps.v, vblock,
+                               ((row + r) & in_page) >> 3, pg, bar);
+                    __syncwarp();
                 }
                 return true;
             };
@@ -1074,13 +1068,14 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                 for (int c = 0; c < S::KC; ++c, ++i) {
                     const uint32_t slot = i % S::NS;
                     const uint64_t ad = sdesc_kmajor(q_base + (t * S::QB + c * S::KB) * kBlock);
-                    const uint64_t bd = sdesc_kmajor(ring + slot * S::STAGE);
+                    const uint64_t bd = sdesc_kmajor(ring + slot * S::STAGE, ROWS8 ? S::KB * 1024 : 1024);
 #pragma unroll
                     for (int k = 0; k < 4 * S::KB; ++k) {
                         if (k == 2 * S::KB && !(c + 1 < S::KC ? !see || ready(i + 1) : next()))
                             return false;
                         const uint32_t step = (k >> 2) * (kBlock >> 4) + 2u * (k & 3);
-                        mma_ss(s_col(b), ad + step, bd + step, id_s, (c > 0 || k > 0) ? 1u : 0u);
+                        const uint32_t bstep = ROWS8 ? (k >> 2) * (1024 >> 4) + 2u * (k & 3) : step;
+                        mma_ss(s_col(b), ad + step, bd + bstep, id_s, (c > 0 || k > 0) ? 1u : 0u);
                     }
                     if (free)
                         mma_commit(smem_addr(&bars.empty[slot]));
@@ -1093,12 +1088,13 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 #pragma unroll
                 for (int c = 0; c < S::VC; ++c, ++i) {
                     const uint32_t slot = i % S::NS;
-                    const uint64_t bd = sdesc_mnmajor(ring + slot * S::STAGE, S::VKEYS * 128);
+                    const uint64_t bd = ROWS8 ? sdesc_mnmajor(ring + slot * S::STAGE, 1024, S::DV * 16)
+                                              : sdesc_mnmajor(ring + slot * S::STAGE, S::VKEYS * 128);
 #pragma unroll
                     for (int k = 0; k < S::VKEYS / 16; ++k) {
                         if (k == S::VKEYS / 32 && !(c + 1 < S::VC ? !see || ready(i + 1) : next()))
                             return false;
-                        mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + 128u * k, id_o,
+                        mma_ts(o_col(t), s_col(b) + (uint32_t)(c * S::VKEYS / 2 + 8 * k), bd + (ROWS8 ? S::DV * 2u : 128u) * k, id_o,
                                c > 0 || k > 0 ? 1u : acc);
                     }
                     if (free)
@@ -1231,16 +1227,19 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                             if ((((some | none) >> r4) & 0xFu) == 0)
                                 continue;
                             const int rr = r4 + (lane >> 3);
-                            const uint32_t p = vb + (32 * h + rr) * 128 + (lane & 7) * 16;
+                            constexpr uint32_t NEXT = ROWS8 ? 1024 : S::VKEYS * 128; // the row's next block
+                            const uint32_t p = vb + (lane & 7) * 16 +
+                                               (ROWS8 ? ((32 * h + rr) >> 3) * (S::DV * 16) + (rr & 7) * 128
+                                                      : (32 * h + rr) * 128);
                             if ((none >> rr) & 1u) {
 #pragma unroll
                                 for (int b = 0; b < S::DV / 64; ++b)
-                                    sts128(p + b * (S::VKEYS * 128), make_uint4(0, 0, 0, 0));
+                                    sts128(p + b * NEXT, make_uint4(0, 0, 0, 0));
                             } else if ((some >> rr) & 1u) {
                                 uint4 v[S::DV / 64];
 #pragma unroll
                                 for (int b = 0; b < S::DV / 64; ++b)
-                                    v[b] = lds128(p + b * (S::VKEYS * 128));
+                                    v[b] = lds128(p + b * NEXT);
 #pragma unroll
                                 for (int b = 0; b < S::DV / 64; ++b) {
                                     uint32_t *e = reinterpret_cast<uint32_t *>(&v[b]);
@@ -1254,7 +1253,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                                     }
                                     if (bad) {
                                         found = true;
-                                        sts128(p + b * (S::VKEYS * 128), v[b]);
+                                        sts128(p + b * NEXT, v[b]);
                                     }
                                 }
                             }

@@ -474,8 +474,8 @@ int w4_qk_norm_rope(uint16_t *q_out, uint16_t *k_out, const void *q, const void 
  *   batch's last ones) are left as they are in q_out and store nothing.
  *
  *   k_pages, v_pages bf16 [pages][page][Hkv][D] with page_stride, row_stride and
- *   head_stride elements between them (multiples of 8; any order of the three in
- *   memory, no overlap); page a power of two in 16..1024; table int32 [B][table_pages];
+ *   head_stride elements between them (multiples of 8, the heads' of 64; any order of the
+ *   three in memory, no overlap); page a power of two in 16..1024; table int32 [B][table_pages];
  *   lens int32 [B]; cu_q int32 [B + 1], ascending; B in 1..4096; table_pages * page up to
  *   2^31 - 1025. v as k, with ldv; v_weight as k_weight. Otherwise as w4_qk_norm_rope.
  * table, lens and cu_q are read when the kernel runs. Two tokens stored to the same place
