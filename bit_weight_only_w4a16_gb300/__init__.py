@@ -522,14 +522,18 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
         _check(rc, "w4_kv_commit")
 
 
+# These calls serve single tokens of many requests, where the call's host time is most of
+# its time: what is usual is tested in one expression per tensor, and what is not goes
+# through the helpers above, which say what is wrong.
 _ROWS = _BITS16 | _F32
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _heads(t, name, shape, dtype, dev):
     """Rows of heads of one type (fp32, or bf16 or its bits), strided rows: elements between rows."""
     if t.get_device() != dev:
         raise _elsewhere(name, dev)
-    if t.dtype != dtype and not (t.dtype in _BITS16 and dtype in _BITS16):
+    if t.dtype is not dtype and not (t.dtype in _BITS16 and dtype in _BITS16):
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -542,11 +546,36 @@ def _heads(t, name, shape, dtype, dev):
 
 def _weight(t, name, n, dev):
     """A contiguous fp32 tensor of n elements or None; its address."""
-    return None if t is None else _tensor(t, name, _F32, (n,), dev)
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not _f32 or t.shape != (n,) or not t.is_contiguous():
+        _tensor(t, name, _F32, (n,), dev)
+    return t.data_ptr()
+
+
+def _words(t, name, n, dev):
+    """A contiguous int32 tensor of n elements; its address."""
+    if t.get_device() != dev or t.dtype is not _i32 or t.numel() != n or not t.is_contiguous():
+        _ints(t, name, n, dev)
+    return t.data_ptr()
 
 
 def _pages(k_pages, v_pages, Hkv, D, dev):
-    """Strides of pages, rows and heads (where there is one only, a stride that is in order)."""
+    """Pages, rows of one, and the strides of pages, rows and heads (where there is one
+    only, a stride that is in order)."""
+    shape, sk = k_pages.shape, k_pages.stride()
+    if (k_pages.get_device() != dev or v_pages.get_device() != dev or k_pages.dtype is not _bf16 or
+            v_pages.dtype is not _bf16 or len(shape) != 4 or shape[3] != D or shape[2] != Hkv or v_pages.shape != shape or
+            v_pages.stride() != sk or sk[3] != 1):
+        _pages_unusual(k_pages, v_pages, Hkv, D, dev)
+    n, page = shape[0], shape[1]
+    head = sk[2] if Hkv > 1 else D
+    row = sk[1] if page > 1 else D
+    return n, page, sk[0] if n > 1 else max(row * page, head * Hkv), row, head
+
+
+def _pages_unusual(k_pages, v_pages, Hkv, D, dev):
+    """Raises what is wrong with two pools, or returns: raw bits and strides that do not count are served."""
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if t.get_device() != dev:
             raise _elsewhere(name, dev)
@@ -554,16 +583,11 @@ def _pages(k_pages, v_pages, Hkv, D, dev):
             raise TypeError(f"{name} must be bf16 (or its raw 16-bit bits)")
         if t.dim() != 4 or t.shape[2:] != (Hkv, D) or t.shape != k_pages.shape:
             raise ValueError(f"{name} must be [pages][page][{Hkv}][{D}] (k_pages and v_pages alike), got {list(t.shape)}")
-    n, page = k_pages.shape[:2]
-    sk, sv = k_pages.stride(), v_pages.stride()
-    for a, b, size in zip(sk, sv, k_pages.shape):
+    for a, b, size in zip(k_pages.stride(), v_pages.stride(), k_pages.shape):
         if a != b and size > 1:
             raise ValueError("k_pages and v_pages must have the same strides")
-    if sk[3] != 1:
+    if k_pages.stride(3) != 1:
         raise ValueError("k_pages: the head width must be contiguous")
-    head = sk[2] if Hkv > 1 else D
-    row = sk[1] if page > 1 else D
-    return n, page, sk[0] if n > 1 else max(row * page, head * Hkv), row, head
 
 
 def _batch(table, lens, cu_q, rows, dev):
@@ -571,10 +595,13 @@ def _batch(table, lens, cu_q, rows, dev):
     if table.dim() != 2:
         raise ValueError("table must be int32 [B][pages of a sequence at most]")
     B, n = table.shape
-    if cu_q is None and rows != B:
-        raise ValueError(f"without cu_q there is one row of each sequence: {rows} rows, {B} sequences")
-    return (B, n, _ints(table, "table", B * n, dev), _ints(lens, "lens", B, dev),
-            None if cu_q is None else _ints(cu_q, "cu_q", B + 1, dev))
+    if cu_q is None:
+        if rows != B:
+            raise ValueError(f"without cu_q there is one row of each sequence: {rows} rows, {B} sequences")
+        cu = None
+    else:
+        cu = _words(cu_q, "cu_q", B + 1, dev)
+    return B, n, _words(table, "table", B * n, dev), _words(lens, "lens", B, dev), cu
 
 
 def w4_qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, pairs: bool = False, q_out=None,
@@ -587,28 +614,36 @@ def w4_qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: floa
     pairs: neighbouring elements are turned together, else j and j + R / 2. q_out may
     be q, k_out k, where those are bf16.
     """
-    M, Hq, D = q.shape
-    Hkv = 0 if k is None else k.shape[1]
+    M, Hq, D = shape = q.shape
+    dt, dev = q.dtype, _device(q, "q")
+    if dt not in _ROWS:
+        raise TypeError(f"q: {dt} is not served")
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if M > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX or R > _INT_MAX:
-        raise _past_int(M, Hq, Hkv, D, R)
-    dev = _device(q, "q")
-    if q.dtype not in _ROWS:
-        raise TypeError(f"q: {q.dtype} is not served")
-    qo = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
-    ldq, ldqo = _heads(q, "q", (M, Hq, D), q.dtype, dev), _heads(qo, "q_out", (M, Hq, D), torch.bfloat16, dev)
-    ko, ldk, ldko = None, 0, 0
+    Hkv, kp, kop, ldk, ldko, ko = 0, None, None, 0, 0, None
     if k is not None:
-        ko = torch.empty((M, Hkv, D), dtype=torch.bfloat16, device=q.device) if k_out is None else k_out
-        ldk, ldko = _heads(k, "k", (M, Hkv, D), q.dtype, dev), _heads(ko, "k_out", (M, Hkv, D), torch.bfloat16, dev)
-    rc = _lib.w4_qk_norm_rope(qo.data_ptr(), None if k is None else ko.data_ptr(), q.data_ptr(),
-                              None if k is None else k.data_ptr(), _weight(q_weight, "q_weight", D, dev),
+        Hkv = k.shape[1]
+        ks = (M, Hkv, D)
+        ldk, ldko, kp = _heads(k, "k", ks, dt, dev), Hkv * D, k.data_ptr()
+        if k_out is None:
+            ko = torch.empty(ks, dtype=_bf16, device=k.device)
+        else:
+            ko = k_out
+            ldko = _heads(ko, "k_out", ks, _bf16, dev)
+        kop = ko.data_ptr()
+    if max(M, Hq, Hkv, D, R) > _INT_MAX:
+        raise _past_int(M, Hq, Hkv, D, R)
+    ldq, ldqo = _heads(q, "q", shape, dt, dev), Hq * D
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+    else:
+        ldqo = _heads(q_out, "q_out", shape, _bf16, dev)
+    rc = _lib.w4_qk_norm_rope(q_out.data_ptr(), kop, q.data_ptr(), kp, _weight(q_weight, "q_weight", D, dev),
                               _weight(k_weight, "k_weight", D, dev), _weight(inv_freq, "inv_freq", R // 2, dev),
-                              _ints(pos, "pos", M, dev), M, Hq, Hkv, D, R, ldq, ldk, ldqo, ldko,
-                              q.dtype == torch.float32, pairs, eps, _raw_stream(stream, dev))
+                              _words(pos, "pos", M, dev), M, Hq, Hkv, D, R, ldq, ldk, ldqo, ldko, dt is _f32, pairs, eps,
+                              _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_qk_norm_rope")
-    return qo, ko
+    return q_out, ko
 
 
 def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_weight=None, k_weight=None, v_weight=None,
@@ -621,28 +656,31 @@ def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_
     its new tokens, which are the last; cu_q int32 [B + 1]: the sequences' first rows,
     or None: row b is sequence b's. A token without a page sets status (int32 [1]).
     """
-    M, Hq, D = q.shape
+    M, Hq, D = shape = q.shape
+    dt, dev = q.dtype, _device(q, "q")
+    if dt not in _ROWS:
+        raise TypeError(f"q: {dt} is not served")
     Hkv = k.shape[1]
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
-    dev = _device(q, "q")
-    if q.dtype not in _ROWS:
-        raise TypeError(f"q: {q.dtype} is not served")
-    qo = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
     n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
     B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
     if max(M, Hq, Hkv, D, R, n, page, B, tn) > _INT_MAX:
         raise _past_int(M, Hq, Hkv, D, R, n, page, B, tn)
-    ldq, ldk = _heads(q, "q", (M, Hq, D), q.dtype, dev), _heads(k, "k", (M, Hkv, D), q.dtype, dev)
-    ldv, ldqo = _heads(v, "v", (M, Hkv, D), q.dtype, dev), _heads(qo, "q_out", (M, Hq, D), torch.bfloat16, dev)
-    rc = _lib.w4_qkv_paged(qo.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), q.data_ptr(), k.data_ptr(),
+    kv = (M, Hkv, D)
+    ldq, ldk, ldv = _heads(q, "q", shape, dt, dev), _heads(k, "k", kv, dt, dev), _heads(v, "v", kv, dt, dev)
+    ldqo = Hq * D
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+    else:
+        ldqo = _heads(q_out, "q_out", shape, _bf16, dev)
+    rc = _lib.w4_qkv_paged(q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), q.data_ptr(), k.data_ptr(),
                            v.data_ptr(), _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev),
                            _weight(v_weight, "v_weight", D, dev), _weight(inv_freq, "inv_freq", R // 2, dev), tp, lp, cp,
-                           B, M, Hq, Hkv, D, R, n, page, tn, ldq, ldk, ldv, ldqo, ps, rs, hs, q.dtype == torch.float32,
-                           pairs, eps, None if status is None else _ints(status, "status", 1, dev),
-                           _raw_stream(stream, dev))
+                           B, M, Hq, Hkv, D, R, n, page, tn, ldq, ldk, ldv, ldqo, ps, rs, hs, dt is _f32, pairs, eps,
+                           None if status is None else _words(status, "status", 1, dev), _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_qkv_paged")
-    return qo
+    return q_out
 
 
 def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, scale: float = 1.0, out=None, stream=None):
@@ -653,20 +691,23 @@ def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, 
     w4_qkv_paged; window 0 = no window. Uses the library's split scratch: no other call
     that does may overlap in time.
     """
-    M, Hq, D = q.shape
+    M, Hq, D = shape = q.shape
     Hkv = k_pages.shape[2]
     dev = _device(q, "q")
-    o = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
     n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
     B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
     if max(M, Hq, Hkv, D, n, page, B, tn, window) > _INT_MAX or window < _INT_MIN:
         raise _past_int(M, Hq, Hkv, D, n, page, B, tn, window)
-    ldq, ldo = _rows(q, "q", M, Hq, D, dev), Hq * D if out is None else _rows(o, "out", M, Hq, D, dev)
-    rc = _lib.w4_attn_paged(o.data_ptr(), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tp, lp, cp, B, M, Hq, Hkv,
+    ldq, ldo = _heads(q, "q", shape, _bf16, dev), Hq * D
+    if out is None:
+        out = torch.empty(shape, dtype=_bf16, device=q.device)
+    else:
+        ldo = _heads(out, "out", shape, _bf16, dev)
+    rc = _lib.w4_attn_paged(out.data_ptr(), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), tp, lp, cp, B, M, Hq, Hkv,
                             D, n, page, tn, ldq, ldo, ps, rs, hs, window, scale, _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_attn_paged")
-    return o
+    return out
 
 
 def _matrix(t, name, dtypes, shape, dev):
@@ -692,18 +733,20 @@ def w4_lora(y, x, a, b, ids, scale=None, out=None, status=None, stream=None):
     may be y. An id of L or more counts as none and sets status (int32 [1]). Uses the
     library's split scratch: no other call that does may overlap in time.
     """
-    M, N = y.shape
+    M, N = shape = y.shape
     L, R, K = a.shape
     if max(M, N, K, R, L) > _INT_MAX:
         raise _past_int(M, N, K, R, L)
     dev = _device(y, "y")
-    o = torch.empty((M, N), dtype=torch.float32, device=y.device) if out is None else out
-    ldy, ldx = _matrix(y, "y", _F32, (M, N), dev), _matrix(x, "x", _BITS16, (M, K), dev)
-    ldo = N if out is None else _matrix(o, "out", _F32, (M, N), dev)
-    rc = _lib.w4_lora(o.data_ptr(), y.data_ptr(), x.data_ptr(), _tensor(a, "a", _BITS16, (L, R, K), dev),
-                      _tensor(b, "b", _BITS16, (L, N, R), dev), _ints(ids, "ids", M, dev), _weight(scale, "scale", L, dev),
-                      M, N, K, R, L, ldo, ldy, ldx, None if status is None else _ints(status, "status", 1, dev),
+    ldy, ldx, ldo = _matrix(y, "y", _F32, shape, dev), _matrix(x, "x", _BITS16, (M, K), dev), N
+    if out is None:
+        out = torch.empty(shape, dtype=_f32, device=y.device)
+    else:
+        ldo = _matrix(out, "out", _F32, shape, dev)
+    rc = _lib.w4_lora(out.data_ptr(), y.data_ptr(), x.data_ptr(), _tensor(a, "a", _BITS16, (L, R, K), dev),
+                      _tensor(b, "b", _BITS16, (L, N, R), dev), _words(ids, "ids", M, dev), _weight(scale, "scale", L, dev),
+                      M, N, K, R, L, ldo, ldy, ldx, None if status is None else _words(status, "status", 1, dev),
                       _raw_stream(stream, dev))
     if rc:
         _check(rc, "w4_lora")
-    return o
+    return out
