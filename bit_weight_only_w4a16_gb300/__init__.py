@@ -595,6 +595,8 @@ def _batch(table, lens, cu_q, rows, dev):
     if table.dim() != 2:
         raise ValueError("table must be int32 [B][pages of a sequence at most]")
     B, n = table.shape
+    if max(rows, B, n) > _INT_MAX:
+        raise _past_int(rows, B, n)
     if cu_q is None:
         if rows != B:
             raise ValueError(f"without cu_q there is one row of each sequence: {rows} rows, {B} sequences")
@@ -623,6 +625,8 @@ def w4_qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: floa
     if k is not None:
         Hkv = k.shape[1]
         ks = (M, Hkv, D)
+        if max(M, Hkv, D) > _INT_MAX:
+            raise _past_int(M, Hkv, D)
         ldk, ldko, kp = _heads(k, "k", ks, dt, dev), Hkv * D, k.data_ptr()
         if k_out is None:
             ko = torch.empty(ks, dtype=_bf16, device=k.device)
@@ -664,8 +668,8 @@ def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
     n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
     B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
-    if max(M, Hq, Hkv, D, R, n, page, B, tn) > _INT_MAX:
-        raise _past_int(M, Hq, Hkv, D, R, n, page, B, tn)
+    if max(Hq, Hkv, D, R, n, page) > _INT_MAX:
+        raise _past_int(Hq, Hkv, D, R, n, page)
     kv = (M, Hkv, D)
     ldq, ldk, ldv = _heads(q, "q", shape, dt, dev), _heads(k, "k", kv, dt, dev), _heads(v, "v", kv, dt, dev)
     ldqo = Hq * D
@@ -696,8 +700,8 @@ def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, 
     dev = _device(q, "q")
     n, page, ps, rs, hs = _pages(k_pages, v_pages, Hkv, D, dev)
     B, tn, tp, lp, cp = _batch(table, lens, cu_q, M, dev)
-    if max(M, Hq, Hkv, D, n, page, B, tn, window) > _INT_MAX or window < _INT_MIN:
-        raise _past_int(M, Hq, Hkv, D, n, page, B, tn, window)
+    if max(Hq, Hkv, D, n, page, window) > _INT_MAX or window < _INT_MIN:
+        raise _past_int(Hq, Hkv, D, n, page, window)
     ldq, ldo = _heads(q, "q", shape, _bf16, dev), Hq * D
     if out is None:
         out = torch.empty(shape, dtype=_bf16, device=q.device)

@@ -107,6 +107,8 @@ qk_norm_rope_kernel(const NormRopeArgs a, const int hp, const int split)
     int o0[CPL], o1[CPL];
     bool has[CPL], rot[CPL];
     unsigned long long turn[CPL][4];
+    pdl_launch_dependents();
+    pdl_wait();
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
         const int c = sub + LPH * i;
@@ -115,13 +117,10 @@ qk_norm_rope_kernel(const NormRopeArgs a, const int hp, const int split)
         const bool half = rot[i] && !PAIRS;
         o0[i] = half ? 4 * c : 8 * c;
         o1[i] = half ? 4 * c + a.R / 2 : 8 * c + 4;
-        // Frequencies are the caller's constants: read ahead of the preceding kernel's end.
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             turn[i][j] = rot[i] ? turn_of(__ldg(a.inv_freq + 4 * c + j)) : 0ull;
     }
-    pdl_launch_dependents();
-    pdl_wait();
 
     const long long items = (long long)a.M * split;
     // All lanes of a warp go round together (their sums are exchanged).
