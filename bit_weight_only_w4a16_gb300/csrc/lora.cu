@@ -22,11 +22,13 @@
 // of which the second launch was 3, and 18 for 61 rows of 12288 columns.)
 //
 // Above that (prompts, whose rows lie together) a tile is 64 rows in order. First kernel: x
-// and a through a ring in shared memory, K split over the blocks of a cluster, h to the
-// scratch. A tile's adapters are shared by kTurns blocks, which take every kTurns-th (a tile
+// and a through a ring in shared memory, K split over blocks that leave partial sums of h in
+// the scratch (joined by a cluster instead, 4 blocks took 19 us for 4001 x 6144 where the
+// stream takes 7). A tile's adapters are shared by kTurns blocks, which take every kTurns-th (a tile
 // where one prompt ends and the next begins took a block two passes, and with it the
 // call; most tiles leave all turns but the first idle). Second kernel: y and b, 256
-// columns a block; y of all rows is asked for at once, before their adapters are known.
+// columns a block; y of all rows is asked for at once, and the partial sums are added and
+// split once per block, through shared memory.
 //
 // Bound by y and out (8 bytes per element) for prompts, by the adapters for mixed
 // batches, by latency for one token.
@@ -46,9 +48,9 @@ constexpr int kGrouped = 512; // rows that a block ranks (two of each thread)
 
 struct Args {
     LoraArgs p;
-    uint16_t *h;       // [3 parts][rows of this pass][R]
+    float *h;          // prompts: partial sums [parts][rows of this pass][R]
     int m0, M;         // first row and rows of this pass
-    int parts;         // blocks of a cluster
+    int parts;         // blocks that share a tile's K
 };
 
 struct Tile {
@@ -394,7 +396,7 @@ lora_group_kernel(const Args a, const int groups)
 // Copies of 16 bytes to shared memory, zeros where !ok.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -405,25 +407,25 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
                  : "memory");
 }
 
-// h of a tile of 64 rows in order. A stage is 64 elements of K: 64 rows of x and 8 NT of a, 128 bytes
+// h of a tile of 64 rows in order. A stage is 128 elements of K: 64 rows of x and 8 NT of a, 256 bytes
 // each, the 16-byte piece c of row r at c ^ (r & 7). Warp w has rows 16 (w / 2) .. and half w % 2 of a stage.
 template <int NT>
 struct DownShape {
     static constexpr int RS = 8 * NT;
-    static constexpr int STAGE = (64 + RS) * 128;
-    static constexpr int ST = NT <= 4 ? 6 : (NT == 8 ? 6 : 4);
-    static constexpr int PART = 2 * 64 * RS * 4; // over the ring's space, when it is drained
+    static constexpr int STAGE = (64 + RS) * 256;
+    static constexpr int ST = NT <= 4 ? 4 : (NT == 8 ? 3 : 4); // two blocks an SM (one at NT = 16)
+    static constexpr int PART = 64 * RS * 4; // over the ring's space, when it is drained
     static constexpr int SMEM = ST * STAGE > PART ? ST * STAGE : PART;
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1)
 lora_down_kernel(const Args a)
 {
     using S = DownShape<NT>;
     constexpr int TR = 64, RS = S::RS, ST = S::ST;
     extern __shared__ __align__(128) unsigned char ring_[];
-    float *part = reinterpret_cast<float *>(ring_); // [2][TR][RS]
+    float *part = reinterpret_cast<float *>(ring_); // [TR][RS]
     const LoraArgs &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
     const int tiles = (a.M + TR - 1) / TR, part_no = (int)(blockIdx.x % a.parts);
@@ -432,32 +434,34 @@ lora_down_kernel(const Args a)
     pdl_wait();
     pdl_launch_dependents(); // what the next kernel reads early is complete
     Adapters ad(a, tile, turn, false);
-    const int steps = (p.K + 63) / 64; // the last one may be half
+    const int steps = (p.K + 127) / 128; // the last one may be short
     const int s0 = (int)((long long)steps * part_no / a.parts), s1 = (int)((long long)steps * (part_no + 1) / a.parts);
     const int wr = w >> 1, half = w & 1;
-    // A thread copies piece tid % 8 of rows tid / 8, 32 further on, ...: two of x, then those of a.
-    const int cr = tid >> 3, cc = tid & 7;
-    const uint32_t to0 = ring + cr * 128 + ((cc ^ (cr & 7)) << 4);
-    const uint16_t *px = p.x + (size_t)(a.m0 + tile * TR + cr) * p.ldx + s0 * 64 + cc * 8;
-    const bool okx[2] = {tile * TR + cr < a.M, tile * TR + cr + 32 < a.M};
+    // A thread copies piece tid % 16 of rows tid / 16, 16 further on, ...: four of x, then those of a.
+    const int cr = tid >> 4, cc = tid & 15, left = a.M - (tile * TR + cr);
+    const uint32_t to0 = ring + cr * 256 + ((cc ^ (cr & 7)) << 4);
+    const uint16_t *px = p.x + (size_t)(a.m0 + tile * TR + cr) * p.ldx + s0 * 128 + cc * 8;
 
     while (ad.left) {
         unsigned long long rows;
         const int id = ad.next(rows);
-        const uint16_t *pa = p.a + ((size_t)id * p.R + cr) * p.K + s0 * 64 + cc * 8;
+        const uint16_t *pa = p.a + ((size_t)id * p.R + cr) * p.K + s0 * 128 + cc * 8;
         auto issue = [&](int i) { // stage i of this block's
             if (i < s1 - s0) {
                 const uint32_t to = to0 + (i % ST) * S::STAGE;
-                const bool in = (s0 + i) * 64 + cc * 8 < p.K;
-                const uint16_t *x = px + i * 64, *y = pa + i * 64;
-                copy16(to, in && okx[0] ? x : p.x, in && okx[0]);
-                copy16(to + 32 * 128, in && okx[1] ? x + 32 * p.ldx : p.x, in && okx[1]);
+                const bool in = (s0 + i) * 128 + cc * 8 < p.K;
+                const uint16_t *x = px + i * 128, *y = pa + i * 128;
 #pragma unroll
-                for (int q = 0; q < (RS + 31) / 32; ++q) {
-                    const int r = 32 * q + cr;
-                    if (RS % 32 == 0 || r < RS) {
+                for (int q = 0; q < 4; ++q) {
+                    const bool ok = in && 16 * q < left;
+                    copy16(to + 16 * q * 256, ok ? x + (size_t)16 * q * p.ldx : p.x, ok);
+                }
+#pragma unroll
+                for (int q = 0; q < (RS + 15) / 16; ++q) {
+                    const int r = 16 * q + cr;
+                    if (RS % 16 == 0 || r < RS) {
                         const bool ok = in && r < p.R;
-                        copy16(to + (64 + 32 * q) * 128, ok ? y + (size_t)32 * q * p.K : p.a, ok);
+                        copy16(to + (64 + 16 * q) * 256, ok ? y + (size_t)16 * q * p.K : p.a, ok);
                     }
                 }
             }
@@ -475,26 +479,26 @@ lora_down_kernel(const Args a)
             asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
             __syncthreads(); // the stage is in place, and the one before it has been read
             issue(st + ST - 1);
-            const uint32_t xb = ring + (st % ST) * S::STAGE, ab = xb + 64 * 128;
+            const uint32_t xb = ring + (st % ST) * S::STAGE, ab = xb + 64 * 256;
             const int row = (lane & 7) + ((lane >> 3) & 1) * 8, up = lane >> 4; // x: rows, then halves of 16
             const int arow = (lane & 7) + (lane >> 4) * 8, aup = (lane >> 3) & 1; // a: halves of 16, then rows
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c0 = 4 * half + 2 * k;
+            for (int k = 0; k < 4; ++k) {
+                const int c0 = 8 * half + 2 * k;
                 uint32_t x4[4];
-                ldsm4(xb + (16 * wr + row) * 128 + (((c0 + up) ^ (row & 7)) << 4), x4);
+                ldsm4(xb + (16 * wr + row) * 256 + (((c0 + up) ^ (row & 7)) << 4), x4);
                 if (NT == 1) {
                     uint32_t b0, b1;
                     asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
                                  : "=r"(b0), "=r"(b1)
-                                 : "r"(ab + (lane & 7) * 128 + (((c0 + aup) ^ (lane & 7)) << 4))
+                                 : "r"(ab + (lane & 7) * 256 + (((c0 + aup) ^ (lane & 7)) << 4))
                                  : "memory");
                     mma_16816(c[0], x4[0], x4[1], x4[2], x4[3], b0, b1);
                 } else {
 #pragma unroll
                     for (int n = 0; n + 1 < NT; n += 2) {
                         uint32_t b4[4];
-                        ldsm4(ab + (8 * n + arow) * 128 + (((c0 + aup) ^ (arow & 7)) << 4), b4);
+                        ldsm4(ab + (8 * n + arow) * 256 + (((c0 + aup) ^ (arow & 7)) << 4), b4);
                         mma_16816(c[n], x4[0], x4[1], x4[2], x4[3], b4[0], b4[1]);
                         mma_16816(c[n + 1], x4[0], x4[1], x4[2], x4[3], b4[2], b4[3]);
                     }
@@ -504,41 +508,29 @@ lora_down_kernel(const Args a)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads(); // the ring's space is the parts' now
         const int i0 = 16 * wr + g, i1 = i0 + 8;
-        float *to = part + (size_t)half * TR * RS;
+        if (half) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2 *>(to + i0 * RS + 8 * n + 2 * tq) = make_float2(c[n][0], c[n][1]);
-            *reinterpret_cast<float2 *>(to + i1 * RS + 8 * n + 2 * tq) = make_float2(c[n][2], c[n][3]);
-        }
-        if (a.parts > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        const float scale = p.scale ? __ldg(p.scale + id) : 1.f;
-        for (int e = part_no * kThreads + tid; e < TR * RS / 2; e += kThreads * a.parts) {
-            const int i = e / (RS / 2), r = 2 * (e - i * (RS / 2));
-            if (!((rows >> i) & 1) || r >= p.R)
-                continue;
-            float2 v = make_float2(0.f, 0.f);
-            const uint32_t at = smem_addr(part) + (uint32_t)e * 8;
-            for (int k = 0; k < a.parts; ++k) {
-                const uint32_t q = map_rank(at, k);
-                const float2 v0 = ld_cluster_f32x2(q), v1 = ld_cluster_f32x2(q + TR * RS * 4);
-                v.x += v0.x + v1.x;
-                v.y += v0.y + v1.y;
+            for (int n = 0; n < NT; ++n) {
+                *reinterpret_cast<float2 *>(part + i0 * RS + 8 * n + 2 * tq) = make_float2(c[n][0], c[n][1]);
+                *reinterpret_cast<float2 *>(part + i1 * RS + 8 * n + 2 * tq) = make_float2(c[n][2], c[n][3]);
             }
-            v.x *= scale;
-            v.y *= scale;
-            __nv_bfloat162 h[3];
-            split3(v, h);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<__nv_bfloat162 *>(a.h + ((size_t)k * a.M + tile * TR + i) * p.R + r) = h[k];
         }
-        if (a.parts > 1)
-            cluster_sync(); // before another block's reads of this one's part go stale
-        else
-            __syncthreads();
+        __syncthreads();
+        if (!half) {
+            float *to = a.h + ((size_t)part_no * a.M + (size_t)tile * TR) * p.R + 2 * tq;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 v0 = *reinterpret_cast<float2 *>(part + i0 * RS + 8 * n + 2 * tq);
+                const float2 v1 = *reinterpret_cast<float2 *>(part + i1 * RS + 8 * n + 2 * tq);
+                if (8 * n < p.R) {
+                    if ((rows >> i0) & 1)
+                        *reinterpret_cast<float2 *>(to + (size_t)i0 * p.R + 8 * n) = make_float2(c[n][0] + v0.x, c[n][1] + v0.y);
+                    if ((rows >> i1) & 1)
+                        *reinterpret_cast<float2 *>(to + (size_t)i1 * p.R + 8 * n) = make_float2(c[n][2] + v1.x, c[n][3] + v1.y);
+                }
+            }
+        }
+        __syncthreads(); // the space is the ring's again
     }
 }
 
@@ -548,6 +540,9 @@ __global__ void __launch_bounds__(kThreads, NS <= 2 ? 2 : 1)
 lora_up_kernel(const Args a)
 {
     constexpr int TR = 64, RB = TR / 16, RU = NS == 1 ? 4 : 2; // row blocks; in flight
+    constexpr int HP = 32 * NS + 8;                            // elements between rows of h
+    extern __shared__ __align__(16) __nv_bfloat16 hs_[];       // [3][TR][HP]
+    __shared__ int s_id[TR];
     const LoraArgs &p = a.p;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3;
     pdl_launch_dependents();
@@ -556,16 +551,54 @@ lora_up_kernel(const Args a)
     const int m = tile * TR + g, rows = a.M - m; // this thread's first row of the pass; rows from it on
     const float *yp = p.y + (size_t)(a.m0 + m) * p.ldy + n0 + 4 * tq;
     float *op = p.out + (size_t)(a.m0 + m) * p.ldo + n0 + 4 * tq;
-    const uint16_t *hp = a.h + (size_t)m * p.R + 8 * tq;
     int ids[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = tile * TR + 32 * i + lane;
         ids[i] = r < a.M ? adapter_of(p, a.m0 + r) : -2;
+        if (w == 0)
+            s_id[32 * i + lane] = ids[i];
     }
     int have = -2; // the adapter whose b is held
     uint4 b[NS][4];
-    bool waited = false;
+    // h of the tile, once the first kernel has left it: partial sums added in order, scaled, in three parts.
+    auto stage = [&]() {
+        __syncthreads(); // the rows' adapters
+        pdl_wait();
+#pragma unroll 2
+        for (int q = 0; q < TR * 8 * NS / kThreads; ++q) { // four elements of a row each
+            const int e = q * kThreads + (int)threadIdx.x, i = e / (8 * NS), r = 4 * (e - i * 8 * NS), id = s_id[i];
+            const bool ok = id >= 0 && r < p.R;
+            const float *from = a.h + ((size_t)tile * TR + i) * p.R + r;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < a.parts; k0 += 4) {
+                float4 x[4]; // in flight together
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = ok && k0 + k < a.parts
+                               ? __ldcg(reinterpret_cast<const float4 *>(from + (size_t)(k0 + k) * a.M * p.R))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v.x += x[k].x;
+                    v.y += x[k].y;
+                    v.z += x[k].z;
+                    v.w += x[k].w;
+                }
+            }
+            const float f = ok && p.scale ? __ldg(p.scale + id) : 1.f;
+            __nv_bfloat162 lo[3], hi[3];
+            split3(make_float2(v.x * f, v.y * f), lo);
+            split3(make_float2(v.z * f, v.w * f), hi);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                __nv_bfloat16 *to = hs_ + (size_t)(t * TR + i) * HP + r;
+                *reinterpret_cast<__nv_bfloat162 *>(to) = lo[t];
+                *reinterpret_cast<__nv_bfloat162 *>(to + 2) = hi[t];
+            }
+        }
+        __syncthreads();
+    };
 #pragma unroll
     for (int rb = 0; rb < RB; rb += RU) {
         float c[RU][4][4];
@@ -576,6 +609,14 @@ lora_up_kernel(const Args a)
                 const int i = (rb + u) * 16 + 8 * q;
                 load_y(c[u], q, yp + (size_t)i * p.ldy, in0 && i < rows, in1 && i < rows);
             }
+        if (rb == 0) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids[0], 0);
+            if (id >= 0) { // as a rule that of all rows
+                load_b<NS>(b, p, id, n0);
+                have = id;
+            }
+            stage();
+        }
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             const int i = (rb + u) * 16, from = 16 * ((rb + u) & 1);
@@ -590,10 +631,6 @@ lora_up_kernel(const Args a)
                     load_b<NS>(b, p, mine, n0);
                     have = mine;
                 }
-                if (!waited) {
-                    pdl_wait();
-                    waited = true;
-                }
                 float d[4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -607,10 +644,7 @@ lora_up_kernel(const Args a)
                     for (int t = 0; t < 3; ++t)
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            h[t][q] = 32 * k + 8 * tq < p.R && i + 8 * q < rows
-                                          ? __ldcg(reinterpret_cast<const uint4 *>(
-                                                hp + ((size_t)t * a.M + i + 8 * q) * p.R + 32 * k))
-                                          : make_uint4(0, 0, 0, 0);
+                            h[t][q] = lds128(smem_addr(hs_ + (size_t)(t * TR + i + 8 * q + g) * HP + 32 * k + 8 * tq));
 #pragma unroll
                     for (int t = 2; t >= 0; --t) // small parts first
 #pragma unroll
@@ -630,8 +664,6 @@ lora_up_kernel(const Args a)
                 store_out(op + (size_t)(i + 8 * q) * p.ldo, c[u], q, in0 && i + 8 * q < rows, in1 && i + 8 * q < rows);
         }
     }
-    if (!waited)
-        pdl_wait();
 }
 
 // Dynamic shared memory of a kernel, once per device.
@@ -678,39 +710,34 @@ cudaError_t grouped(const Args &a, int tiles, int num_sms, cudaStream_t s)
 }
 
 template <int NT>
-cudaError_t down(Args a, int num_sms, cudaStream_t s)
+cudaError_t down(const Args &a, cudaStream_t s)
 {
     static std::atomic<unsigned long long> set{0};
     cudaError_t e = allow(lora_down_kernel<NT>, DownShape<NT>::SMEM, set);
     if (e != cudaSuccess)
         return e;
-    // Blocks that share a tile: up to 8 (a portable cluster), while they fit the SMs at once and
-    // each has a few stages.
-    const int tiles = (a.M + 63) / 64;
-    a.parts = 1;
-    while (a.parts < 8 && (long long)tiles * a.parts * 2 <= 3ll * num_sms && a.parts * 256 < a.p.K)
-        a.parts *= 2;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)a.parts;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * kTurns * a.parts));
+    cfg.gridDim = dim3((unsigned)((a.M + 63) / 64 * kTurns * a.parts));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = DownShape<NT>::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, lora_down_kernel<NT>, a);
 }
 
 template <int NT>
-cudaError_t prompt(const Args &a, int num_sms, cudaStream_t s)
+cudaError_t prompt(const Args &a, cudaStream_t s)
 {
-    const cudaError_t e = down<NT>(a, num_sms, s);
+    constexpr int NS = (NT + 3) / 4, SMEM = 3 * 64 * (32 * NS + 8) * 2;
+    cudaError_t e = down<NT>(a, s);
+    if (e != cudaSuccess)
+        return e;
+    static std::atomic<unsigned long long> set{0};
+    e = allow(lora_up_kernel<NS>, SMEM, set);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[1];
@@ -722,14 +749,15 @@ cudaError_t prompt(const Args &a, int num_sms, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_up_kernel<(NT + 3) / 4>, a);
+    cfg.dynamicSmemBytes = SMEM;
+    return cudaLaunchKernelEx(&cfg, lora_up_kernel<NS>, a);
 }
 
 template <int NT>
 cudaError_t pass(const Args &a, int num_sms, cudaStream_t s)
 {
     if (a.M > kGrouped)
-        return prompt<NT>(a, num_sms, s);
+        return prompt<NT>(a, s);
     // Each adapter (and the rows without one) has at most one tile that is not full.
     const long long ids = (long long)a.p.L + 1, n = a.M / 16 + (ids < a.M ? ids : a.M);
     return grouped<NT>(a, (int)(n < a.M ? n : a.M), num_sms, s);
@@ -739,14 +767,20 @@ cudaError_t pass(const Args &a, int num_sms, cudaStream_t s)
 
 cudaError_t run_lora(const LoraArgs &p, float *ws, size_t ws_floats, int num_sms, cudaStream_t s)
 {
-    // Rows whose h fits the scratch go in one pass (53000 or so at R = 128).
-    const long long most = (long long)(ws_floats * 4 / (6 * (size_t)p.R)) / 64 * 64;
+    // Blocks that share a tile's K, while they fit the SMs and each has a few stages.
+    const long long all = ((long long)p.M + 63) / 64;
+    int parts = 1;
+    while (parts < 8 && all * parts * 2 <= 2ll * num_sms && parts * 512 < p.K)
+        parts *= 2;
+    // Rows whose partial sums fit the scratch go in one pass (82000 at R = 128).
+    const long long most = (long long)(ws_floats / ((size_t)p.R * parts)) / 64 * 64;
     for (long long m0 = 0; m0 < p.M; m0 += most) {
         Args a = {};
         a.p = p;
         a.m0 = (int)m0;
         a.M = (int)(p.M - m0 < most ? p.M - m0 : most);
-        a.h = reinterpret_cast<uint16_t *>(ws);
+        a.h = ws;
+        a.parts = parts;
         const cudaError_t e = p.R <= 8    ? pass<1>(a, num_sms, s)
                               : p.R <= 16 ? pass<2>(a, num_sms, s)
                               : p.R <= 32 ? pass<4>(a, num_sms, s)
