@@ -24,6 +24,8 @@
 // Work: the tiles of all (sequence, key/value head) segments, in order, cut into equal
 // runs, one per block; a block's warps take turns and join their sums at a segment's end.
 // A segment that was cut leaves partial sums, which a second kernel joins in a fixed order.
+// Where a window or a short table keeps segments to a few tiles a warp, runs are whole
+// segments and the second kernel is left out.
 #include "attn_launch.cuh"
 
 namespace w4 {
@@ -53,6 +55,7 @@ struct StepArgs {
     Args a;
     const uint16_t *q, *k;
     long long ldq;
+    int whole; // runs of whole segments
 };
 
 // A run's place: a segment and its kept keys.
@@ -150,7 +153,7 @@ step_kernel(const StepArgs p)
     using S = StepShape<D, HT>;
     constexpr int THREADS = S::W * 32, KS = D / 16, CH = D / 8; // 16-byte pieces of a row
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_base, s_scan[S::W];
+    __shared__ long long s_base, s_run[2], s_scan[S::W];
     __shared__ int s_seq, s_h;
     const Args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
@@ -171,11 +174,14 @@ step_kernel(const StepArgs p)
         run_sum<S::W>(n, s_scan, total);
         all += total;
     }
-    const long long tot = all * a.Hkv;
-    // A tile for each warp of a block at least.
-    const long long blocks = max(1ll, min((long long)gridDim.x, tot / S::W));
-    const long long x0 = tot * min((long long)blockIdx.x, blocks) / blocks;
-    const long long x1 = tot * min((long long)blockIdx.x + 1, blocks) / blocks;
+    const long long tot = all * a.Hkv, segments = (long long)a.B * a.Hkv;
+    // Runs of tiles: one for each warp of a block at least. Or of segments.
+    const long long blocks = max(1ll, min((long long)gridDim.x, p.whole ? segments : tot / S::W));
+    const long long per = p.whole ? segments : tot;
+    const long long u0 = per * min((long long)blockIdx.x, blocks) / blocks;
+    const long long u1 = per * min((long long)blockIdx.x + 1, blocks) / blocks;
+    if (tid < 2)
+        s_run[tid] = tot; // the end of the last run, until a sequence claims the place
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += THREADS) {
         int lo, len, n = 0;
@@ -183,16 +189,25 @@ step_kernel(const StepArgs p)
             keys_of(a, b0 + tid, lo, len, n);
         long long total;
         const long long incl = before + run_sum<S::W>(n, s_scan, total);
-        if (n > 0 && x0 < incl * a.Hkv && x0 >= (incl - n) * a.Hkv) {
-            s_seq = b0 + tid;
-            s_h = (int)((x0 - (incl - n) * a.Hkv) / n);
-            s_base = (incl - n) * a.Hkv + (long long)s_h * n;
+        const long long first = (incl - n) * a.Hkv, seg0 = (long long)(b0 + tid) * a.Hkv; // of this sequence
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long u = e ? u1 : u0;
+            if (n > 0 && (p.whole ? u >= seg0 && u < seg0 + a.Hkv : u >= first && u < incl * a.Hkv)) {
+                const int h = (int)(p.whole ? u - seg0 : (u - first) / n);
+                const long long base = first + (long long)h * n;
+                s_run[e] = p.whole ? base : u;
+                if (e == 0) {
+                    s_seq = b0 + tid;
+                    s_h = h;
+                    s_base = base;
+                }
+            }
         }
         before += total;
-        if (before * a.Hkv > x0)
-            break;
     }
     __syncthreads();
+    const long long x0 = s_run[0], x1 = s_run[1];
     int begins = 0, begins_b = 0, begins_h = 0; // parts of the cut segment that this run begins, if any
     if (x0 < x1) {
         Walk c;
@@ -605,6 +620,12 @@ cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t
     using S = StepShape<D, HT>;
     StepArgs p = p0;
     set_scratch(p.a, ws, num_sms);
+    // Keys of a segment at most, in tiles (a window may begin and end within one). Windows of 512, 8 heads,
+    // D = 256 (5 tiles a warp): 3 tokens 10.4 us whole and 9.8 cut and joined (but one launch, where calls
+    // are bound by those), 61 on two heads of 128 8.3 and 14.4, 152 tokens 11.5 and 27. At D = 512 a tile is
+    // 2 us for a warp: 5 of them 14.6 and 10.7.
+    const long long keys = p.a.window > 0 && p.a.window < p.a.most_k ? p.a.window : p.a.most_k;
+    p.whole = (keys + kTile - 1) / kTile + 1 <= (D <= 256 ? 6 : 2) * S::W;
     static std::atomic<unsigned long long> set{0};
     cudaError_t e = allow_smem(step_kernel<D, HT>, S::SMEM, set);
     if (e != cudaSuccess)
@@ -621,7 +642,7 @@ cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, step_kernel<D, HT>, p);
     const long long segments = (long long)p.a.B * p.a.Hkv;
-    if (e != cudaSuccess || p.a.most_k <= kTile) // a segment of one tile is never cut
+    if (e != cudaSuccess || p.whole)
         return e;
     if (num_sms > kJoinThreads) // a thread for each block's record and part
         return cudaErrorInvalidValue;

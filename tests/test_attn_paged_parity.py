@@ -290,6 +290,25 @@ def test_sharp_and_growing_scores(w4):
         b.check(w4, scale=0.5)
         b = Batch(24, [1, 1], [900, 200], 4, 1, D, 16)
         b.check(w4, scale=1.0, step=True)
+    for D in (64, 128, 256, 384, 512):  # the same for single tokens, keys falling as well
+        for up in (True, False):
+            b = Batch(25, [1, 1, 1], [900, 17, 400], 8, 1, D, 16)
+            grow = torch.linspace(0.01, 3.0, 900, device="cuda")
+            grow = grow if up else grow.flip(0)
+            for s in range(3):
+                for p in range(-(-int(b.lens[s]) // 16)):
+                    n = min(16, int(b.lens[s]) - 16 * p)
+                    b.k[b.table[s, p], :n] *= grow[16 * p:16 * p + n, None, None].bfloat16()
+            b.check(w4, scale=0.5, step=True)
+
+
+def test_short_segments_whole(w4):
+    """Windows and tables so short that a block takes whole segments, more and fewer of them than blocks."""
+    rng = np.random.default_rng(8)
+    for B, D, Hkv, window in ((1, 256, 1, 512), (5, 128, 2, 300), (200, 64, 2, 100), (160, 256, 1, 40), (9, 512, 1, 100)):
+        lens = rng.integers(0, 900, B)
+        Batch(30 + B, np.ones(B, int), lens, 4 * Hkv, Hkv, D, 16).check(w4, window=window, step=True)
+    Batch(29, np.ones(40, int), rng.integers(0, 200, 40), 16, 2, 128, 64).check(w4, step=True)
 
 
 def test_binding_checks(w4):
