@@ -27,8 +27,8 @@
 // stream takes 7). A tile's adapters are shared by kTurns blocks, which take every kTurns-th (a tile
 // where one prompt ends and the next begins took a block two passes, and with it the
 // call; most tiles leave all turns but the first idle). Second kernel: y and b, 256
-// columns a block; y of all rows is asked for at once, and the partial sums are added and
-// split once per block, through shared memory.
+// columns a block; the partial sums are added and split once per block, through shared
+// memory, with y of the first 32 rows and b on their way.
 //
 // Bound by y and out (8 bytes per element) for prompts, by the adapters for mixed
 // batches, by latency for one token.
@@ -536,10 +536,10 @@ lora_down_kernel(const Args a)
 
 // out = y + b h. NS: steps of 32 across R. A warp has 32 columns of the tile's 64 rows.
 template <int NS>
-__global__ void __launch_bounds__(kThreads, NS <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, NS == 1 ? 3 : (NS == 2 ? 2 : 1))
 lora_up_kernel(const Args a)
 {
-    constexpr int TR = 64, RB = TR / 16, RU = NS == 1 ? 4 : 2; // row blocks; in flight
+    constexpr int TR = 64, RB = TR / 16, RU = 2;               // row blocks; in flight
     constexpr int HP = 32 * NS + 8;                            // elements between rows of h
     extern __shared__ __align__(16) __nv_bfloat16 hs_[];       // [3][TR][HP]
     __shared__ int s_id[TR];

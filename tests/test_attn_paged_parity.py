@@ -56,6 +56,8 @@ class Batch:
             self.k, self.v = pool(self.pages, page, Hkv, D), pool(self.pages, page, Hkv, D)
         elif layout == "heads":
             self.k, self.v = (pool(self.pages, Hkv, page, D).transpose(1, 2) for _ in range(2))
+        elif layout == "inner":  # a row of every page side by side
+            self.k, self.v = (pool(page, self.pages, Hkv, D).transpose(0, 1) for _ in range(2))
         else:
             kv = pool(self.pages, 2, page, Hkv, D)
             self.k, self.v = kv[:, 0], kv[:, 1]
@@ -96,10 +98,11 @@ def test_widths_and_pages(w4, D, page):
     Batch(D + page, [1, 1, 1, 1, 1], [1, 16, 17, 400, 129], 8, 2, D, page).check(w4, step=True)
 
 
-@pytest.mark.parametrize("layout", ["heads", "beside"])
+@pytest.mark.parametrize("layout", ["heads", "beside", "inner"])
 @pytest.mark.parametrize("D,page", [(128, 16), (256, 64), (512, 256)])
 def test_layouts_of_the_pool(w4, layout, D, page):
     Batch(3, [40, 1, 3], [300, 90, 3], 6, 2, D, page, layout).check(w4, window=150)
+    Batch(4, [1, 1, 1], [300, 90, 3], 6, 2, D, page, layout).check(w4, step=True)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (7, 1), (12, 4), (16, 2), (100, 1), (128, 1)])
@@ -276,6 +279,26 @@ def test_deterministic_streams_and_graphs(w4, step):
         torch.cuda.synchronize()
         np.testing.assert_array_equal(f64(out), other)
     assert w4.device_error() == 0
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_lengths_past_the_table_and_below_zero(w4, step):
+    """Positions stay what the length says; the keys end with the table."""
+    for D, window in ((128, 0), (256, 0), (512, 0), (128, 70)):
+        b = Batch(26, [1, 1, 1, 1], [64, 33, 20, 50], 8, 2, D, 16)
+        b.lens = np.array([2**31 - 1, 100, -3, 50])
+        b.table[0, 1] = -1
+        got = b.check(w4, window=window, step=step)
+        assert not got[2].any()
+        if window:
+            assert not got[0].any()  # its window lies past the table
+
+
+def test_most_sequences(w4):
+    rng = np.random.default_rng(9)
+    b = Batch(27, np.ones(4096, int), rng.integers(0, 40, 4096), 1, 1, 64, 16)
+    b.check(w4, step=True)
+    b.check(w4)
 
 
 def test_sharp_and_growing_scores(w4):

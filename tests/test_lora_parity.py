@@ -95,6 +95,13 @@ def test_shapes(w4, N, K):
     check(w4, y, x, a, b, np.arange(19) % 4 - 1, s)
 
 
+@pytest.mark.parametrize("N,K", [(24, 96), (40, 608), (520, 4128), (2048, 32)])
+def test_shapes_of_prompts(w4, N, K):
+    """Columns and summed elements that end within a step of the kernels."""
+    y, x, a, b, s = make(N + 1, 777, N, K, 24, 3)
+    check(w4, y, x, a, b, np.repeat([1, -1, 2, 0], [400, 7, 300, 70]), s)
+
+
 def test_many_adapters(w4):
     y, x, a, b, s = make(1, 300, 40, 64, 8, 500)
     ids = np.random.default_rng(2).integers(0, 500, 300)
@@ -145,6 +152,12 @@ def test_rows_do_not_reach_each_other(w4):
         got = w4.w4_lora(y, x, a2, b, dev(ids), scale=s)
         rest = torch.from_numpy(ids != 2).cuda()
         assert not torch.isfinite(got[~rest]).any() and torch.equal(got[rest], want[rest])
+        b2 = b.clone()
+        b2[2, 5:9] = float("nan")
+        got = w4.w4_lora(y, x, a, b2, dev(ids), scale=s)
+        assert torch.isnan(got[~rest][:, 5:9]).all() and torch.equal(got[rest], want[rest])
+        got[:, 5:9] = want[:, 5:9]
+        assert torch.equal(got, want)
 
 
 def test_rows_past_one_pass(w4):

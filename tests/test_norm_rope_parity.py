@@ -156,6 +156,9 @@ def store(w4, seed, lq, past, Hq, Hkv, D, R, page, dtype="float32", layout="rows
     elif layout == "heads":
         g = [Guard((pages, Hkv, page, D), torch.bfloat16) for _ in range(2)]
         kp, vp = (x.t.transpose(1, 2) for x in g)
+    elif layout == "inner":  # a row of every page side by side
+        g = [Guard((page, pages, Hkv, D), torch.bfloat16) for _ in range(2)]
+        kp, vp = (x.t.transpose(0, 1) for x in g)
     else:  # keys and values of a page side by side
         g = [Guard((pages, 2, page, Hkv, D), torch.bfloat16)]
         kp, vp = g[0].t[:, 0], g[0].t[:, 1]
@@ -193,7 +196,7 @@ def store(w4, seed, lq, past, Hq, Hkv, D, R, page, dtype="float32", layout="rows
 
 
 @pytest.mark.parametrize("page", [16, 64, 1024])
-@pytest.mark.parametrize("layout", ["rows", "heads", "beside"])
+@pytest.mark.parametrize("layout", ["rows", "heads", "beside", "inner"])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_store_layouts(w4, page, layout, dtype):
     store(w4, 1, [1, 40, 3, 17], [0, 5, 1000, 15], 8, 2, 128, 128, page, dtype, layout, status=True)
@@ -218,6 +221,21 @@ def test_store_without_a_page(w4):
     w4.w4_qkv_paged(q, k, v, kp, vp, dev([[1]]), dev([3]), None, cu_q=dev([0, 5]), status=st)
     assert int(st) == 1 and bool((kp[0] == 9).all()) and bool((kp[1, 3:] == 9).all())
     assert torch.equal(vp[1, :3], v[2:].bfloat16())
+
+
+def test_store_lengths_at_the_ends(w4):
+    """Lengths of 2^31 - 1 and below zero; 4096 sequences, some empty."""
+    import torch
+    q, k, v = rows(2, 2, 1, 128, 8, torch.float32)
+    kp = torch.full((2, 16, 1, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    vp, st = kp.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    f = freqs(128)
+    got = w4.w4_qkv_paged(q, k, v, kp, vp, dev([[0], [1]]), dev([2**31 - 1, -7]), dev(f, np.float32), status=st)
+    assert int(st) == 1 and bool((kp == 9).all()) and bool((vp == 9).all())
+    close(f64(got), f64(q), np.array([2**31 - 2, -1]), f, False)
+    rng = np.random.default_rng(3)
+    lq = rng.integers(0, 3, 4096)
+    store(w4, 7, lq.tolist(), rng.integers(0, 30, 4096).tolist(), 1, 1, 64, 64, 16, status=True)
 
 
 def test_store_far_in_a_large_pool(w4):
