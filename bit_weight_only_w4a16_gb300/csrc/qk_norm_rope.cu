@@ -106,7 +106,9 @@ qk_norm_rope_kernel(const NormRopeArgs a, const int hp, const int split)
     // This lane's chunks: offsets of their two halves within a head.
     int o0[CPL], o1[CPL];
     bool has[CPL], rot[CPL];
+    float freq[CPL][4];
     unsigned long long turn[CPL][4];
+    bool first = true;
     pdl_launch_dependents();
     pdl_wait();
 #pragma unroll
@@ -119,7 +121,7 @@ qk_norm_rope_kernel(const NormRopeArgs a, const int hp, const int split)
         o1[i] = half ? 4 * c + a.R / 2 : 8 * c + 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            turn[i][j] = rot[i] ? turn_of(__ldg(a.inv_freq + 4 * c + j)) : 0ull;
+            freq[i][j] = rot[i] ? __ldg(a.inv_freq + 4 * c + j) : 0.f;
     }
 
     const long long items = (long long)a.M * split;
@@ -187,6 +189,14 @@ qk_norm_rope_kernel(const NormRopeArgs a, const int hp, const int split)
                 *a.status = 1;
         } else {
             pos = __ldg(a.pos + m);
+        }
+        if (first) { // with the first loads on their way
+            first = false;
+#pragma unroll
+            for (int i = 0; i < CPL; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    turn[i][j] = turn_of(freq[i][j]);
         }
         float cs[CPL][4], sn[CPL][4];
 #pragma unroll
