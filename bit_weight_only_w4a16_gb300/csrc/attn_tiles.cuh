@@ -1237,9 +1237,17 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
                                     sts128(p + b * NEXT, make_uint4(0, 0, 0, 0));
                             } else if ((some >> rr) & 1u) {
                                 uint4 v[S::DV / 64];
+                                // Exponents of ones: the half's magnitude and 0x80 reach 0x8000.
+                                uint32_t odd = 0;
 #pragma unroll
                                 for (int b = 0; b < S::DV / 64; ++b)
                                     v[b] = lds128(p + b * NEXT);
+#pragma unroll
+                                for (int b = 0; b < S::DV / 64; ++b)
+                                    odd |= ((v[b].x & 0x7FFF7FFFu) + 0x00800080u) | ((v[b].y & 0x7FFF7FFFu) + 0x00800080u) |
+                                           ((v[b].z & 0x7FFF7FFFu) + 0x00800080u) | ((v[b].w & 0x7FFF7FFFu) + 0x00800080u);
+                                if (!(odd & 0x80008000u))
+                                    continue;
 #pragma unroll
                                 for (int b = 0; b < S::DV / 64; ++b) {
                                     uint32_t *e = reinterpret_cast<uint32_t *>(&v[b]);

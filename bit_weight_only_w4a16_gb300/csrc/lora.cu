@@ -86,13 +86,13 @@ __device__ __forceinline__ int find_tile(const Args &a, int t, bool none, Tile &
         const int m = tid + i * kThreads;
         lead[i] = false;
         if (i * kThreads < a.M) {
+            // Equal ones among the rows of the warps before, then within this one's.
             const int mine = s.ids[m];
-            const int end = min(m | 31, a.M - 1); // the warp's lanes end together
-            for (int j = 0; j <= end; j += 4) {
+            for (int j = 0; j < (m & ~31); j += 4) {
                 const int4 o = *reinterpret_cast<const int4 *>(s.ids + j);
-                rank[i] += (j < m && o.x == mine) + (j + 1 < m && o.y == mine) + (j + 2 < m && o.z == mine) +
-                           (j + 3 < m && o.w == mine);
+                rank[i] += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
             }
+            rank[i] += __popc(__match_any_sync(0xFFFFFFFFu, mine) & ((1u << lane) - 1u));
             lead[i] = mine >= (none ? -1 : 0) && rank[i] % 16 == 0;
         }
         votes[i] = __ballot_sync(0xFFFFFFFFu, lead[i]);
