@@ -136,12 +136,12 @@ struct Rows {
 
 // q, k, v (and for a tree the nodes' own kt, vt); a.* but the scratch is set.
 // tiles: row tiles of the call at most, over all heads and value slices.
-template <int D, Kind KIND>
+template <typename S, Kind KIND>
 cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Rows &kt, const Rows &vt,
                    long long tiles, bool may_cut, float *ws, int num_sms, cudaStream_t s)
 {
-    using S = Shape<D>;
-    static_assert(S::TQ == (D <= 128 ? 2 : 1) && S::NV == (D > 256 ? 2 : 1), "as in attn_tile_tokens, attn_slices");
+    constexpr int D = S::DIM;
+    static_assert(S::TQ <= (D <= 128 ? 2 : 1) && S::NV == (D > 256 ? 2 : 1), "as in attn_tile_tokens, attn_slices");
     Maps m;
     if (!encode_rows(&m.q, q.p, q.rows, a.Hq, D, q.ld, a.G, a.tpt) ||
         (KIND == kPaged
@@ -154,7 +154,7 @@ cudaError_t launch(Args a, const Rows &q, const Rows &k, const Rows &v, const Ro
         return cudaErrorInvalidValue;
     set_scratch(a, ws, num_sms);
 
-    auto kern = attn_kernel<D, KIND>;
+    auto kern = attn_kernel<D, KIND, S::TQ>;
     static std::atomic<unsigned long long> set{0};
     cudaError_t e = allow_smem(kern, S::SMEM, set);
     if (e != cudaSuccess)

@@ -20,12 +20,20 @@ cudaError_t run_attn_paged(const AttnPagedArgs &p, float *ws, int *err, int num_
         using S = decltype(shape);
         const long long tt = (long long)a.tpt * S::TQ;
         const long long tiles = (p.total_q / tt + p.B) * p.Hkv * S::NV;
-        const bool may_cut = a.most_k > attn::kKeys;
-        return attn::launch<S::DIM, attn::kPaged>(a, q, k, v, k, v, tiles, may_cut, ws, num_sms, s);
+        // Units of a row tile at most: its window and tokens, which may begin and end within a key tile.
+        const long long keys = a.window > 0 && a.window + tt < a.most_k ? a.window + tt : a.most_k;
+        const bool may_cut = (keys + attn::kKeys - 1) / attn::kKeys + 1 > attn::kWholeUnits;
+        return attn::launch<S, attn::kPaged>(a, q, k, v, k, v, tiles, may_cut, ws, num_sms, s);
     };
     switch (p.D) {
     case 64: return run(attn::Shape<64>{});
-    case 128: return run(attn::Shape<128>{});
+    case 128:
+        // Two row tiles share the keys where products are the bound; of chunks of up to four tiles on average
+        // most row tiles have no second one to share with, and one has twice the softmax threads (12 chunks, 24
+        // tokens on up to 18269: 67 and 79 us; 12 of 1411 tokens on up to 929: 34 and 39; 7 of 4000 on up to
+        // 9000: 301 and 250).
+        return p.total_q <= 4ll * p.B * a.tpt && (long long)p.B * p.Hkv < 1ll << 26 ? run(attn::Shape<128, 1>{})
+                                                                                     : run(attn::Shape<128>{});
     case 256: return run(attn::Shape<256>{});
     case 384: return run(attn::Shape<384>{});
     case 512: return run(attn::Shape<512>{});

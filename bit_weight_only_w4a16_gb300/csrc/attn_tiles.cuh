@@ -26,7 +26,7 @@
 // which a second kernel merges in key order (deterministic).
 //
 // Tensor memory (512 columns) holds two score tiles and the accumulators: two row
-// tiles share the keys at D <= 128; above, one row tile has two score tiles in
+// tiles share the keys at D <= 128 (a paged call's short chunks have one at D = 128); above, one row tile has two score tiles in
 // turn, and from D = 384 on the value width is cut into two slices, each with a CTA
 // of its own that forms the scores again (half as many operations more).
 //
@@ -78,14 +78,20 @@ constexpr int kPieces = 4;      // pieces in flight between the warps
 // for what lies a piece away (a whole row tile: units times 1 to 5 us; the largest keys
 // and values that fit the device take about 25 s). A short wait that gives up ends all others.
 constexpr int kWaitLimit = 1 << 15, kWaitPiece = 1 << 21;
+// A paged call whose row tiles have so many units or fewer cuts none of them: joining the parts takes
+// longer (a piece's partial sums are 128 KB, the merge 10 to 20 us). 3088 rows in 100 row tiles of 2.9 units
+// on average, 7 at most, D = 256: 22 us whole, 47 cut; 22 drawn batches of chunks together 0.8 times (4: 0.85,
+// 12: 0.83).
+constexpr int kWholeUnits = 8;
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
-template <int D>
+// RT: MMA row tiles per CTA.
+template <int D, int RT = (D <= 128 ? 2 : 1)>
 struct Shape {
     static constexpr int DIM = D;
     static constexpr int NV = D > 256 ? 2 : 1;       // slices of the value width (tensor memory holds 256 columns of O)
     static constexpr int DV = D / NV;                // width of a slice
-    static constexpr int TQ = D <= 128 ? 2 : 1;      // MMA row tiles per CTA
+    static constexpr int TQ = RT;
     static constexpr int QB = D / 64;                // blocks of a row tile's Q
     // One ring of stages in the order of use. 32 KiB where the ring then still
     // covers a copy's latency (about 1500 cycles): waiting for a stage and freeing
@@ -573,7 +579,7 @@ struct Shared {
     Piece piece[kPieces];
     float x[2][2][kRowsQ]; // the two threads of a row: maxima, sums ([unit parity][half][row])
     int xok[2][8];         // and whether their waits ended well ([parity][softmax warp])
-    int cut[2][4], tiles;
+    int cut[2][4], tiles, most; // most: units of the largest row tile
     int special[4];        // piece whose value rows had NaN or infinities
     // paged: unit's keys whose page is none of the pool, a bit for 16 keys. Keys of a unit
     // are copied at most 8 units ahead of the softmax (half the ring's slots, and two).
@@ -703,11 +709,19 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
         incl_r = block_scan<S::THREADS>(cost_r, sh.warp_sums, total_r);
     };
     long long W = 0;
+    int most = 0;
     for (int r0 = 0; r0 < R; r0 += S::THREADS) {
         round(r0);
         W += total_r;
+        most = max(most, n_r);
+    }
+    if (KIND == kPaged) {
+        // (sh.most is zero: the kernel's start, and a barrier since.)
+        atomicMax(&sh.most, __reduce_max_sync(0xFFFFFFFFu, most));
+        __syncthreads();
     }
     const long long all = W * HS;
+    const int few = (int)min((long long)kWholeUnits, all / gridDim.x + 1);
     long long at[2];
     int hs[2];
 #pragma unroll
@@ -732,10 +746,16 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             if (cost_r > 0 && hs[e] < HS && at[e] >= p && at[e] < p + cost_r) {
-                sh.cut[e][0] = hs[e] * R + r;
+                const int u = (int)max(0ll, at[e] - p - extra);
+                // A paged call's short row tiles stay whole: all of them, or those not longer than a run. The cut
+                // moves to the tile's nearer end (the next tile's place in its sequence is found where the
+                // run begins).
+                const bool whole = KIND == kPaged && n_r <= (sh.most <= kWholeUnits ? kWholeUnits : few);
+                const bool on = whole && 2 * u >= n_r;
+                sh.cut[e][0] = hs[e] * R + r + (on ? 1 : 0);
                 sh.cut[e][1] = s_r;
-                sh.cut[e][2] = r - sbase[s_r];
-                sh.cut[e][3] = (int)max(0ll, at[e] - p - extra);
+                sh.cut[e][2] = r - sbase[s_r] + (on ? 1 : 0);
+                sh.cut[e][3] = whole ? 0 : u;
             }
         before += total_r;
         if (max(at[0], at[1]) < before)
@@ -743,11 +763,11 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
     }
 }
 
-template <int D, Kind KIND>
-__global__ void __launch_bounds__(Shape<D>::THREADS, 1)
+template <int D, Kind KIND, int RT>
+__global__ void __launch_bounds__(Shape<D, RT>::THREADS, 1)
 attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
 {
-    using S = Shape<D>;
+    using S = Shape<D, RT>;
     constexpr bool TREE = KIND == kTree;
     // Stages of keys and values: [block of 64 dims][row][128 B], or for pages [group of 8
     // rows][block][row][128 B].
@@ -785,6 +805,7 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
             mbar_init(smem_addr(&bars.pc_empty[i]), 3 + 8);
         }
         sh.abort = 0;
+        sh.most = 0;
         for (int i = 0; i < 4; ++i)
             sh.special[i] = -1;
         fence_mbar_init();
@@ -1592,8 +1613,14 @@ attn_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps)
         uint32_t piece = 0;
         bool ok = true;
         Seq q = {};
-        if (tile < end || (tile == end && u < end_u))
+        if (tile < end || (tile == end && u < end_u)) {
             q = load_seq<KIND>(a, s);
+            while (KIND == kPaged && i * tt >= q.lq) { // ends: the run has a row tile
+                i = 0;
+                s = s + 1 < a.B ? s + 1 : 0;
+                q = load_seq<KIND>(a, s);
+            }
+        }
         while (ok && (tile < end || (tile == end && u < end_u))) {
             Piece w;
             w.hs = tile / sh.tiles;

@@ -301,6 +301,20 @@ def test_most_sequences(w4):
     b.check(w4)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_short_and_long_row_tiles(w4, D):
+    """Row tiles that stay whole beside some that are cut, more and fewer of them than blocks."""
+    rng = np.random.default_rng(D)
+    lq = rng.integers(0, 9, 60)
+    lq[7], lq[30], lq[31] = 300, 1, 150
+    lens = lq + rng.integers(0, 260, 60)
+    Batch(40, lq, lens, 4, 4, D, 16).check(w4)          # all short
+    lens[30], lens[31] = 4000, 1700
+    Batch(41, lq, lens, 4, 4, D, 16).check(w4)          # two long ones
+    Batch(42, lq, lens, 4, 4, D, 64).check(w4, window=300)
+    Batch(43, lq[28:33], lens[28:33], 8, 1, D, 32).check(w4)
+
+
 def test_sharp_and_growing_scores(w4):
     import torch
     for D in (128, 256):
