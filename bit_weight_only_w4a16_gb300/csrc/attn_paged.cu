@@ -22,7 +22,7 @@ cudaError_t run_attn_paged(const AttnPagedArgs &p, float *ws, int *err, int num_
         const long long tiles = (p.total_q / tt + p.B) * p.Hkv * S::NV;
         // Units of a row tile at most: its window and tokens, which may begin and end within a key tile.
         const long long keys = a.window > 0 && a.window + tt < a.most_k ? a.window + tt : a.most_k;
-        const bool may_cut = (keys + attn::kKeys - 1) / attn::kKeys + 1 > attn::kWholeUnits;
+        const bool may_cut = (keys + attn::kKeys - 1) / attn::kKeys + 1 > attn::whole_units(p.D);
         return attn::launch<S, attn::kPaged>(a, q, k, v, k, v, tiles, may_cut, ws, num_sms, s);
     };
     switch (p.D) {

@@ -175,8 +175,9 @@ step_kernel(const StepArgs p)
         all += total;
     }
     const long long tot = all * a.Hkv, segments = (long long)a.B * a.Hkv;
-    // Runs of tiles: one for each warp of a block at least. Or of segments.
-    const long long blocks = max(1ll, min((long long)gridDim.x, p.whole ? segments : tot / S::W));
+    // Runs of tiles: one for each warp of a block, or a segment's worth. Or of segments. (5 tokens of
+    // 4 positions at D = 512 in one block's run: 28 us.)
+    const long long blocks = min((long long)gridDim.x, p.whole ? segments : max(tot / S::W, segments));
     const long long per = p.whole ? segments : tot;
     const long long u0 = per * min((long long)blockIdx.x, blocks) / blocks;
     const long long u1 = per * min((long long)blockIdx.x + 1, blocks) / blocks;

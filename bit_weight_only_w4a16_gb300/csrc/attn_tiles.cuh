@@ -80,9 +80,8 @@ constexpr int kPieces = 4;      // pieces in flight between the warps
 constexpr int kWaitLimit = 1 << 15, kWaitPiece = 1 << 21;
 // A paged call whose row tiles have so many units or fewer cuts none of them: joining the parts takes
 // longer (a piece's partial sums are 128 KB, the merge 10 to 20 us). 3088 rows in 100 row tiles of 2.9 units
-// on average, 7 at most, D = 256: 22 us whole, 47 cut; 22 drawn batches of chunks together 0.8 times (4: 0.85,
-// 12: 0.83).
-constexpr int kWholeUnits = 8;
+// on average, 7 at most, D = 256: 22 us whole, 47 cut; 22 drawn batches of chunks together 0.78 times.
+constexpr int whole_units(int D) { return D <= 256 ? 12 : 8; } // a unit takes twice as long above
 constexpr int kMaxSeqs = 4096;  // sequences of a call (their tile prefix is staged in the ring's space)
 
 // RT: MMA row tiles per CTA.
@@ -721,7 +720,7 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
         __syncthreads();
     }
     const long long all = W * HS;
-    const int few = (int)min((long long)kWholeUnits, all / gridDim.x + 1);
+    const int few = (int)min((long long)whole_units(S::DIM), all / gridDim.x + 1);
     long long at[2];
     int hs[2];
 #pragma unroll
@@ -750,7 +749,7 @@ __device__ __forceinline__ void plan_run(const Args &a, Shared &sh, int *sbase, 
                 // A paged call's short row tiles stay whole: all of them, or those not longer than a run. The cut
                 // moves to the tile's nearer end (the next tile's place in its sequence is found where the
                 // run begins).
-                const bool whole = KIND == kPaged && n_r <= (sh.most <= kWholeUnits ? kWholeUnits : few);
+                const bool whole = KIND == kPaged && n_r <= (sh.most <= whole_units(S::DIM) ? whole_units(S::DIM) : few);
                 const bool on = whole && 2 * u >= n_r;
                 sh.cut[e][0] = hs[e] * R + r + (on ? 1 : 0);
                 sh.cut[e][1] = s_r;
