@@ -454,7 +454,8 @@ int w4_lora(float *out, const float *y, const uint16_t *x, const uint16_t *a, co
  *   D in {64, 128, 256, 384, 512}; R a multiple of 8 in 0..D (0: no rotation, inv_freq
  *   may be NULL); eps >= 0. 16-byte aligned pointers (int32 and inv_freq 4-byte), ld*
  *   multiples of 8.
- * Norm and turn in fp32, one rounding to bf16. The angle is exact to 2^-32 of a turn
+ * Norm and turn in fp32 (squares are added in fp32: elements up to about 10^18), one
+ * rounding to bf16. The angle is exact to 2^-32 of a turn
  * for the fp32 inv_freq at every position (whole turns are dropped in integers).
  */
 int w4_qk_norm_rope(uint16_t *q_out, uint16_t *k_out, const void *q, const void *k, const float *q_weight,
@@ -501,8 +502,11 @@ int w4_qkv_paged(uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages, const vo
  *   belongs to no sequence is not written.
  *
  *   out, q bf16 [total_q][Hq][D], ldq / ldo elements between rows; cu_q NULL: total_q = B.
- *   Hq / Hkv, D, scale, precision, masked values, tiles and scratch (no concurrent calls)
- *   as w4_attn_prompt.
+ *   Hq / Hkv, D, scale, masked values, tiles and scratch (no concurrent calls) as
+ *   w4_attn_prompt.
+ * Precision as w4_attn_prompt; single tokens (cu_q NULL, up to 8 heads on one, 16 at D <=
+ * 256) carry their weights as two bf16 parts (2^-16). A kept value that is infinite leaves
+ * infinity or NaN in its column of the rows that keep it.
  */
 int w4_attn_paged(uint16_t *out, const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
                   const int32_t *table, const int32_t *lens, const int32_t *cu_q, int B, int total_q, int Hq, int Hkv,

@@ -200,7 +200,7 @@ def store(w4, seed, lq, past, Hq, Hkv, D, R, page, dtype="float32", layout="rows
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_store_layouts(w4, page, layout, dtype):
     store(w4, 1, [1, 40, 3, 17], [0, 5, 1000, 15], 8, 2, 128, 128, page, dtype, layout, status=True)
-    store(w4, 2, [1, 1, 1], [0, 15, 16], 4, 1, 512, 256, page, dtype, layout, norm_v=False, step=True, status=True)
+    store(w4, 2, [1, 1, 1], [0, 15, 16], 3, 1, 512, 256, page, dtype, layout, norm_v=False, step=True, status=True)
 
 
 def test_store_empty_sequences_and_rows_behind(w4):
