@@ -1,6 +1,7 @@
 """Python binding of libw4a16.so, the W4A16 GEMV/GEMM library for GB300 (sm_103a).
 
-Argument marshalling only: every step of the computation runs in the CUDA
+Argument marshalling only (for the serving calls' usual case in native code, _binding,
+where that is built): every step of the computation runs in the CUDA
 kernels behind the C ABI declared in include/w4a16.h. Tensors must be CUDA
 tensors on the current device; bf16 data may be passed either as torch.bfloat16
 or as raw int16/uint16 bits. There is no CPU path: if the compiled library is
@@ -99,6 +100,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 _lib = load_library()
+
+
+def _load_binding():
+    """The serving calls' native checks (csrc/binding.cpp), or None."""
+    try:
+        from . import _binding
+    except ImportError:
+        return None
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                    (_lib.w4_lora, _lib.w4_qk_norm_rope, _lib.w4_qkv_paged, _lib.w4_attn_paged)))
+    return _binding
+
+
+_fast = _load_binding()
 
 
 def _check(rc: int, call: str):
@@ -523,8 +538,9 @@ def w4_kv_commit(k_cache, v_cache, k_tree, v_tree, path, count, pos, kpos=None, 
 
 
 # These calls serve single tokens of many requests, where the call's host time is most of
-# its time: what is usual is tested in one expression per tensor, and what is not goes
-# through the helpers above, which say what is wrong.
+# its time: the native binding makes the usual call (and answers None to anything else),
+# and here what is usual is tested in one expression per tensor. What is not goes through
+# the helpers above, which say what is wrong.
 _ROWS = _BITS16 | _F32
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -616,6 +632,10 @@ def w4_qk_norm_rope(q, k, pos, inv_freq, q_weight=None, k_weight=None, eps: floa
     pairs: neighbouring elements are turned together, else j and j + R / 2. q_out may
     be q, k_out k, where those are bf16.
     """
+    if _fast is not None:
+        r = _fast.rope(q, k, pos, inv_freq, q_weight, k_weight, eps, pairs, q_out, k_out, stream)
+        if r is not None:
+            return r
     M, Hq, D = shape = q.shape
     dt, dev = q.dtype, _device(q, "q")
     if dt not in _ROWS:
@@ -660,6 +680,11 @@ def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_
     its new tokens, which are the last; cu_q int32 [B + 1]: the sequences' first rows,
     or None: row b is sequence b's. A token without a page sets status (int32 [1]).
     """
+    if _fast is not None:
+        r = _fast.qkv(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q, q_weight, k_weight, v_weight, eps, pairs,
+                      q_out, status, stream)
+        if r is not None:
+            return r
     M, Hq, D = shape = q.shape
     dt, dev = q.dtype, _device(q, "q")
     if dt not in _ROWS:
@@ -695,6 +720,10 @@ def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, 
     w4_qkv_paged; window 0 = no window. Uses the library's split scratch: no other call
     that does may overlap in time.
     """
+    if _fast is not None:
+        r = _fast.attn(q, k_pages, v_pages, table, lens, cu_q, window, scale, out, stream)
+        if r is not None:
+            return r
     M, Hq, D = shape = q.shape
     Hkv = k_pages.shape[2]
     dev = _device(q, "q")
@@ -737,6 +766,10 @@ def w4_lora(y, x, a, b, ids, scale=None, out=None, status=None, stream=None):
     may be y. An id of L or more counts as none and sets status (int32 [1]). Uses the
     library's split scratch: no other call that does may overlap in time.
     """
+    if _fast is not None:
+        r = _fast.lora(y, x, a, b, ids, scale, out, status, stream)
+        if r is not None:
+            return r
     M, N = shape = y.shape
     L, R, K = a.shape
     if max(M, N, K, R, L) > _INT_MAX:

@@ -1,4 +1,5 @@
-"""Build libw4a16.so in-tree with nvcc for sm_103a (no cmake; parallel objects)."""
+"""Build libw4a16.so in-tree with nvcc for sm_103a (no cmake; parallel objects), and the
+serving calls' native binding _binding.so with g++ against the installed torch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,11 +7,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libw4a16.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,8 +45,36 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_binding(force: bool = False):
+    """_binding.so, or None where it cannot be built (the Python binding is complete
+    without it; only the host time of the serving calls is longer)."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (src, os.path.join(INCLUDE, "w4a16.h"))):
+        return BINDING
+    try:
+        import torch
+        base = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(_nvcc()))
+        tmp = BINDING + ".tmp"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I", os.path.join(base, "include"),
+               "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I",
+               sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L", os.path.join(base, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(tmp, BINDING)
+        return BINDING
+    except Exception as e:  # noqa: BLE001
+        print(f"the native binding was not built: {e}", file=sys.stderr)
+        return None
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and up_to_date():
+        build_binding()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -59,7 +91,9 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(2, min(8, os.cpu_count() or 2))) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -70,6 +104,5 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
                 extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else None))
