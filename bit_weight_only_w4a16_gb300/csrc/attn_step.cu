@@ -153,7 +153,7 @@ step_kernel(const StepArgs p)
     using S = StepShape<D, HT>;
     constexpr int THREADS = S::W * 32, KS = D / 16, CH = D / 8; // 16-byte pieces of a row
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_base, s_run[2], s_scan[S::W];
+    __shared__ long long s_base, s_run[4], s_scan[S::W];
     __shared__ int s_seq, s_h;
     const Args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
@@ -164,51 +164,69 @@ step_kernel(const StepArgs p)
     pdl_wait();
 
     // -------------------------------------------------- this block's run
-    // Tiles of all sequences (of one head), then the sequence in which the run begins.
-    long long all = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-        int lo, len, n = 0;
-        if (b0 + tid < a.B)
-            keys_of(a, b0 + tid, lo, len, n);
-        long long total;
-        run_sum<S::W>(n, s_scan, total);
-        all += total;
-    }
-    const long long tot = all * a.Hkv, segments = (long long)a.B * a.Hkv;
-    // Runs of tiles: one for each warp of a block, or a segment's worth. Or of segments. (5 tokens of
-    // 4 positions at D = 512 in one block's run: 28 us.)
-    const long long blocks = min((long long)gridDim.x, p.whole ? segments : max(tot / S::W, segments));
-    const long long per = p.whole ? segments : tot;
-    const long long u0 = per * min((long long)blockIdx.x, blocks) / blocks;
-    const long long u1 = per * min((long long)blockIdx.x + 1, blocks) / blocks;
-    if (tid < 2)
-        s_run[tid] = tot; // the end of the last run, until a sequence claims the place
-    long long before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-        int lo, len, n = 0;
-        if (b0 + tid < a.B)
-            keys_of(a, b0 + tid, lo, len, n);
-        long long total;
-        const long long incl = before + run_sum<S::W>(n, s_scan, total);
-        const long long first = (incl - n) * a.Hkv, seg0 = (long long)(b0 + tid) * a.Hkv; // of this sequence
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const long long u = e ? u1 : u0;
-            if (n > 0 && (p.whole ? u >= seg0 && u < seg0 + a.Hkv : u >= first && u < incl * a.Hkv)) {
-                const int h = (int)(p.whole ? u - seg0 : (u - first) / n);
-                const long long base = first + (long long)h * n;
-                s_run[e] = p.whole ? base : u;
-                if (e == 0) {
-                    s_seq = b0 + tid;
-                    s_h = h;
-                    s_base = base;
-                }
-            }
+    // Its tiles [x0, x1), of them the first's segment; for runs of whole segments counted from
+    // the run's own first tile, else from the call's.
+    // (Through shared memory, which leaves the registers to the sums.)
+    long long x0 = 0, x1 = 0, tot = 0, blocks = 1;
+    const long long segments = (long long)a.B * a.Hkv;
+    if (p.whole) {
+        blocks = min((long long)gridDim.x, segments);
+        const long long g0 = segments * min((long long)blockIdx.x, blocks) / blocks;
+        const long long g1 = segments * min((long long)blockIdx.x + 1, blocks) / blocks;
+        if (tid == 0) {
+            s_seq = (int)(g0 / a.Hkv);
+            s_h = (int)(g0 % a.Hkv);
+            s_base = 0;
         }
-        before += total;
+        for (long long b = g0 / a.Hkv; b * a.Hkv < g1 && g0 < g1; ++b) {
+            int lo, len, n;
+            keys_of(a, (int)b, lo, len, n);
+            x1 += n * (min(g1, (b + 1) * a.Hkv) - max(g0, b * a.Hkv));
+        }
+    } else {
+        // Tiles of all sequences (of one head), then the sequence in which the run begins.
+        long long all = 0;
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            int lo, len, n = 0;
+            if (b0 + tid < a.B)
+                keys_of(a, b0 + tid, lo, len, n);
+            long long total;
+            run_sum<S::W>(n, s_scan, total);
+            all += total;
+        }
+        tot = all * a.Hkv;
+        // Runs of a tile for each warp of a block, or a segment's worth, at least. (5 tokens of 4
+        // positions at D = 512 in one block's run: 28 us.)
+        blocks = min((long long)gridDim.x, max(tot / S::W, segments));
+        x0 = tot * min((long long)blockIdx.x, blocks) / blocks;
+        x1 = tot * min((long long)blockIdx.x + 1, blocks) / blocks;
+        long long before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            int lo, len, n = 0;
+            if (b0 + tid < a.B)
+                keys_of(a, b0 + tid, lo, len, n);
+            long long total;
+            const long long incl = before + run_sum<S::W>(n, s_scan, total);
+            const long long first = (incl - n) * a.Hkv; // of this sequence
+            if (n > 0 && x0 >= first && x0 < incl * a.Hkv) {
+                s_seq = b0 + tid;
+                s_h = (int)((x0 - first) / n);
+                s_base = first + (long long)s_h * n;
+            }
+            before += total;
+            if (before * a.Hkv > x0)
+                break;
+        }
+    }
+    if (tid == 0) {
+        s_run[0] = x0;
+        s_run[1] = x1;
+        s_run[2] = tot;
+        s_run[3] = blocks;
     }
     __syncthreads();
-    const long long x0 = s_run[0], x1 = s_run[1];
+    x0 = s_run[0];
+    x1 = s_run[1];
     int begins = 0, begins_b = 0, begins_h = 0; // parts of the cut segment that this run begins, if any
     if (x0 < x1) {
         Walk c;
@@ -496,7 +514,7 @@ step_kernel(const StepArgs p)
             }
             if (!whole && first) {
                 // The block that has the segment's last tile: the largest one whose run begins at or before it.
-                begins = (int)(((c.base + c.n) * blocks - 1) / tot) - (int)blockIdx.x + 1;
+                begins = (int)(((c.base + c.n) * s_run[3] - 1) / s_run[2]) - (int)blockIdx.x + 1;
                 begins_b = c.b;
                 begins_h = c.h;
             }
