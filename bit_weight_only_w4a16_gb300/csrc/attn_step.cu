@@ -25,7 +25,8 @@
 // runs, one per block; a block's warps take turns and join their sums at a segment's end.
 // A segment that was cut leaves partial sums, which a second kernel joins in a fixed order.
 // Where a window or a short table keeps segments to a few tiles a warp, runs are whole
-// segments and the second kernel is left out.
+// segments and the second kernel is left out; with fewer segments than SMs a cluster of
+// blocks has each, whose sums are joined through distributed shared memory.
 #include "attn_launch.cuh"
 
 namespace w4 {
@@ -56,6 +57,7 @@ struct StepArgs {
     const uint16_t *q, *k;
     long long ldq;
     int whole; // runs of whole segments
+    int cs;    // blocks of a cluster, which has one segment (whole; else 1)
 };
 
 // A run's place: a segment and its kept keys.
@@ -86,6 +88,16 @@ __device__ __forceinline__ void step_to(const Args &a, Walk &w, long long x)
             w.t0 = w.lo / kTile;
         }
     }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
 }
 
 // Inclusive sum over a block of W warps; `total`: all of them. 64 bits: 32 sequences of
@@ -170,9 +182,10 @@ step_kernel(const StepArgs p)
     long long x0 = 0, x1 = 0, tot = 0, blocks = 1;
     const long long segments = (long long)a.B * a.Hkv;
     if (p.whole) {
-        blocks = min((long long)gridDim.x, segments);
-        const long long g0 = segments * min((long long)blockIdx.x, blocks) / blocks;
-        const long long g1 = segments * min((long long)blockIdx.x + 1, blocks) / blocks;
+        const long long block = blockIdx.x / p.cs; // with clusters there are as many as segments
+        blocks = min((long long)gridDim.x / p.cs, segments);
+        const long long g0 = segments * min(block, blocks) / blocks;
+        const long long g1 = segments * min(block + 1, blocks) / blocks;
         if (tid == 0) {
             s_seq = (int)(g0 / a.Hkv);
             s_h = (int)(g0 % a.Hkv);
@@ -236,7 +249,8 @@ step_kernel(const StepArgs p)
         keys_of(a, c.b, c.lo, c.len, c.n);
         c.t0 = c.lo / kTile;
         Walk f = c; // what is copied next
-        long long xf = x0 + w;
+        const int mine = (int)(blockIdx.x % p.cs) * S::W + w, hop = S::W * p.cs; // this warp's tiles
+        long long xf = x0 + mine;
 
         // The next tile's page, a tile ahead of its copies.
         auto page_of = [&]() {
@@ -278,7 +292,7 @@ step_kernel(const StepArgs p)
                 at = (size_t)(have ? pg : 0) * a.page_stride +
                      (size_t)(key & ((1 << a.page_log2) - 1)) * a.row_stride + (size_t)f.h * a.head_stride;
                 rows(p.k, slot);
-                xf += S::W;
+                xf += hop;
                 pg = page_of();
             } else {
                 asm volatile("cp.async.commit_group;" ::: "memory");
@@ -305,7 +319,7 @@ step_kernel(const StepArgs p)
         };
 
         int slot = 0;
-        long long x = x0 + w;
+        long long x = x0 + mine;
         for (long long xs = x0; xs < x1;) { // segments
             step_to(a, c, xs);
             const long long end = min(x1, c.base + c.n);
@@ -332,7 +346,7 @@ step_kernel(const StepArgs p)
                     o[t][s][0] = o[t][s][1] = o[t][s][2] = o[t][s][3] = 0.f;
             }
 #pragma unroll 1
-            for (; x < end; x += S::W) {
+            for (; x < end; x += hop) {
                 ahead(true, slot);
                 const uint32_t kb = ring + slot * S::HALF;
                 slot = slot == S::ST - 1 ? 0 : slot + 1;
@@ -432,11 +446,11 @@ step_kernel(const StepArgs p)
                     l[t][i] += __shfl_xor_sync(0xFFFFFFFFu, l[t][i], 16);
                 }
             const int u = w & (S::W / 2 - 1);
-            float *mine = join + (size_t)(u * S::HEADS + 2 * tq) * S::HS + g;
+            float *own = join + (size_t)(u * S::HEADS + 2 * tq) * S::HS + g;
             auto leave = [&]() {
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
-                    float *to = mine + (size_t)8 * t * S::HS;
+                    float *to = own + (size_t)8 * t * S::HS;
 #pragma unroll
                     for (int s = 0; s < KS; ++s) {
                         to[16 * s] = o[t][s][0];
@@ -456,7 +470,7 @@ step_kernel(const StepArgs p)
             if (w < S::W / 2) {
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
-                    const float *from = mine + (size_t)8 * t * S::HS;
+                    const float *from = own + (size_t)8 * t * S::HS;
                     float fa[2], fb[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -500,7 +514,12 @@ step_kernel(const StepArgs p)
                     y.z = fmaf(fu, z.z, y.z);
                     y.w = fmaf(fu, z.w, y.w);
                 }
-                if (whole) {
+                if (p.cs > 1) {
+                    // The ring is done with: a cluster's block has one segment.
+                    *reinterpret_cast<float4 *>(smem + ((size_t)h * D + 4 * d4) * 4) = y;
+                    if (d4 == 0)
+                        reinterpret_cast<float2 *>(smem + (size_t)S::HEADS * D * 4)[h] = make_float2(M, L);
+                } else if (whole) {
                     const float inv = L == 0.f ? 0.f : 1.f / L; // nothing kept: zeros
                     uint2 b;
                     b.x = pack2(y.x * inv, y.y * inv);
@@ -511,6 +530,33 @@ step_kernel(const StepArgs p)
                     if (d4 == 0)
                         *reinterpret_cast<float2 *>(a.ws_ml + ((size_t)part * 256 + h) * 2) = make_float2(M, L);
                 }
+            }
+            if (p.cs > 1) {
+                cluster_sync();
+                const uint32_t sums = smem_addr(smem), mls = sums + S::HEADS * D * 4;
+                for (int e = (int)(blockIdx.x % p.cs) * THREADS + tid; e < a.G * (D / 4); e += THREADS * p.cs) {
+                    const int h = e / (D / 4), d4 = e - h * (D / 4);
+                    float M = -INFINITY, L = 0.f;
+                    for (int k = 0; k < p.cs; ++k)
+                        M = fmaxf(M, ld_cluster_f32(map_rank(mls + 8 * h, k)));
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < p.cs; ++k) {
+                        const uint32_t ml = map_rank(mls + 8 * h, k);
+                        const float m = ld_cluster_f32(ml), f = m == -INFINITY ? 0.f : ex2(m - M);
+                        const float4 z = ld_cluster_f32x4(map_rank(sums + (h * D + 4 * d4) * 4, k));
+                        L = fmaf(f, ld_cluster_f32(ml + 4), L);
+                        y.x = fmaf(f, z.x, y.x);
+                        y.y = fmaf(f, z.y, y.y);
+                        y.z = fmaf(f, z.z, y.z);
+                        y.w = fmaf(f, z.w, y.w);
+                    }
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    uint2 b;
+                    b.x = pack2(y.x * inv, y.y * inv);
+                    b.y = pack2(y.z * inv, y.w * inv);
+                    *reinterpret_cast<uint2 *>(a.out + (size_t)c.b * a.ldo + (size_t)(c.h * a.G + h) * D + 4 * d4) = b;
+                }
+                cluster_sync(); // this block's sums have been read
             }
             if (!whole && first) {
                 // The block that has the segment's last tile: the largest one whose run begins at or before it.
@@ -640,32 +686,44 @@ cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t
     StepArgs p = p0;
     set_scratch(p.a, ws, num_sms);
     // Keys of a segment at most, in tiles (a window may begin and end within one). Windows of 512, 8 heads,
-    // D = 256 (5 tiles a warp): 3 tokens 10.4 us whole and 9.8 cut and joined (but one launch, where calls
-    // are bound by those), 61 on two heads of 128 8.3 and 14.4, 152 tokens 11.5 and 27. At D = 512 a tile is
-    // 2 us for a warp: 5 of them 14.6 and 10.7.
+    // D = 256, one block a segment (5 tiles a warp): 3 tokens 10.4 us whole and 9.8 cut and joined, 61 on two
+    // heads of 128 8.3 and 14.4, 152 tokens 11.5 and 27. At D = 512 a tile takes a warp twice as long.
     const long long keys = p.a.window > 0 && p.a.window < p.a.most_k ? p.a.window : p.a.most_k;
-    p.whole = (keys + kTile - 1) / kTile + 1 <= (D <= 256 ? 6 : 2) * S::W;
+    const long long tiles = (keys + kTile - 1) / kTile + 1, segments = (long long)p.a.B * p.a.Hkv;
+    // Clusters while they take no more than three quarters of the SMs (the rest of a GPC may not hold one) and
+    // every warp may have a tile: 3 tokens 8.7 us in clusters of 4, 10.4 in single blocks; one 8.3 and 10.3;
+    // 2 of 6 heads on 2 of 384 on tables of 256 keys 7.5 and 14.3 (cut); one on a table of 3000 10.9 and 10.2 (cut).
+    p.cs = 1;
+    while (p.cs < 8 && segments * p.cs * 2 <= num_sms * 3 / 4 && (long long)S::W * p.cs * 2 <= tiles)
+        p.cs *= 2;
+    p.whole = tiles <= (D <= 256 ? 6ll : 3ll) * S::W * p.cs;
+    if (!p.whole)
+        p.cs = 1;
     static std::atomic<unsigned long long> set{0};
     cudaError_t e = allow_smem(step_kernel<D, HT>, S::SMEM, set);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms);
+    cfg.gridDim = dim3((unsigned)(p.cs > 1 ? segments * p.cs : num_sms));
     cfg.blockDim = dim3(S::W * 32);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.cs > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, step_kernel<D, HT>, p);
-    const long long segments = (long long)p.a.B * p.a.Hkv;
     if (e != cudaSuccess || p.whole)
         return e;
     if (num_sms > kJoinThreads) // a thread for each block's record and part
         return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(segments < num_sms ? segments : num_sms), (unsigned)(p.a.G * ((D + 127) / 128)));
+    cfg.numAttrs = 1;
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, step_join_kernel, p.a, num_sms);
