@@ -348,6 +348,69 @@ def test_short_segments_whole(w4):
     Batch(29, np.ones(40, int), rng.integers(0, 200, 40), 16, 2, 128, 64).check(w4, step=True)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (64, 16, 1), (128, 16, 2), (256, 8, 1), (256, 11, 1), (384, 6, 2), (512, 8, 1)])
+def test_few_short_segments_shared_by_blocks(w4, D, Hq, Hkv):
+    """Few sequences on a window or a short table: 2, 4 and 8 blocks have a segment, some of them without a
+    tile or without a kept key, and every one's sums are joined."""
+    rng = np.random.default_rng(D + Hq)
+    for B, keys, window in ((1, 2000, 512), (1, 500, 0), (3, 1000, 300), (3, 300, 0), (9, 260, 0), (9, 900, 200), (20, 700, 257)):
+        lens = rng.integers(1, keys + 1, B)
+        lens[0] = keys
+        if B > 1:
+            lens[1], lens[2] = 0, 1
+        b = Batch(50 + B, np.ones(B, int), lens, Hq, Hkv, D, 32, extra_cols=1)
+        b.check(w4, window=window, step=True)
+        n = -(-keys // 32)
+        first = max(0, keys - window) // 32 if window else 0
+        b.table[0, first + (n - first) // 2:] = -1    # half of the kept keys have no page
+        if B > 3:
+            b.table[3:5] = b.pages                    # and two sequences none at all
+        got = b.check(w4, window=window, step=True)
+        assert B <= 3 or not got[3:5].any()
+
+
+def test_short_segments_one_after_another(w4):
+    """Calls of every form of the single tokens in one captured chain, each on the last one's output: a block's
+    sums are not written over while another reads them."""
+    import torch
+    calls = [Batch(60 + i, np.ones(B, int), np.full(B, keys), 8, 1, D, 16)
+             for i, (B, keys, D) in enumerate([(3, 512, 256), (1, 512, 256), (3, 5000, 256), (9, 200, 256), (3, 256, 256)])]
+    dt = [(dev(b.table), dev(b.lens)) for b in calls]
+    outs = [torch.empty_like(b.q) for b in calls]
+
+    def chain(stream=None):
+        for i, b in enumerate(calls):
+            if i:  # the last output's first row takes the place of a query
+                b.q[:1].copy_(outs[i - 1][:1])
+            w4.w4_attn_paged(b.q, b.k, b.v, *dt[i], scale=1 / 16, out=outs[i], stream=stream)
+
+    for i, b in enumerate(calls):
+        if i:
+            b.q[:1].copy_(outs[i - 1][:1])
+        w4.w4_attn_paged(b.q, b.k, b.v, *dt[i], scale=1 / 16, out=outs[i])
+        torch.cuda.synchronize()
+    want = [f64(o) for o in outs]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain(s)
+        s.synchronize()
+        for o, x in zip(outs, want):
+            np.testing.assert_array_equal(f64(o), x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                chain(s)
+        for o in outs:
+            o.zero_()
+        for _ in range(20):
+            g.replay()
+        s.synchronize()
+    for o, x in zip(outs, want):
+        np.testing.assert_array_equal(f64(o), x)
+    assert w4.device_error() == 0
+
+
 def test_binding_checks(w4):
     import torch
     q = torch.zeros(4, 8, 256, dtype=torch.bfloat16, device="cuda")
