@@ -102,6 +102,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 _lib = load_library()
 
 
+def _check(rc: int, call: str):
+    if rc != W4_OK:
+        detail = _lib.w4_last_cuda_error().decode() if rc == 4 else ""
+        raise W4Error(rc, call, detail)
+
+
 def _load_binding():
     """The serving calls' native checks (csrc/binding.cpp), or None."""
     try:
@@ -109,17 +115,11 @@ def _load_binding():
     except ImportError:
         return None
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                    (_lib.w4_lora, _lib.w4_qk_norm_rope, _lib.w4_qkv_paged, _lib.w4_attn_paged)))
+                    (_lib.w4_lora, _lib.w4_qk_norm_rope, _lib.w4_qkv_paged, _lib.w4_attn_paged)), _check)
     return _binding
 
 
 _fast = _load_binding()
-
-
-def _check(rc: int, call: str):
-    if rc != W4_OK:
-        detail = _lib.w4_last_cuda_error().decode() if rc == 4 else ""
-        raise W4Error(rc, call, detail)
 
 
 def _ptr(t):

@@ -683,6 +683,8 @@ template <int D, int HT>
 cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t s)
 {
     using S = StepShape<D, HT>;
+    if (num_sms > kJoinThreads) // the join has a thread for each block's record and part
+        return cudaErrorInvalidValue;
     StepArgs p = p0;
     set_scratch(p.a, ws, num_sms);
     // Keys of a segment at most, in tiles (a window may begin and end within one). Windows of 512, 8 heads,
@@ -720,8 +722,6 @@ cudaError_t launch_step(const StepArgs &p0, float *ws, int num_sms, cudaStream_t
     e = cudaLaunchKernelEx(&cfg, step_kernel<D, HT>, p);
     if (e != cudaSuccess || p.whole)
         return e;
-    if (num_sms > kJoinThreads) // a thread for each block's record and part
-        return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(segments < num_sms ? segments : num_sms), (unsigned)(p.a.G * ((D + 127) / 128)));
     cfg.numAttrs = 1;
     cfg.blockDim = dim3(kJoinThreads);

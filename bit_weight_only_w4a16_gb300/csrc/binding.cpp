@@ -6,9 +6,10 @@
 // took 17 us: 9 of checks, 3 of argument conversion, the rest the launch.
 //
 // Every function returns None for whatever is not plainly right - another type, a shape
-// that does not fit, a subclass of torch.Tensor, an error of the C call (which then launched
-// nothing) - and the Python code, which is complete by itself, makes the call or raises
-// what is wrong with it.
+// that does not fit, a subclass of torch.Tensor, arguments that the C call refuses (it then
+// launched nothing) - and the Python code, which is complete by itself, makes the call or
+// raises what is wrong with it. Any other error of the C call is raised here: a part of
+// the call may have been launched, in place, and is not made a second time.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -36,6 +37,21 @@ inline void need(bool ok)
 {
     if (!ok)
         throw Unusual();
+}
+
+// Thrown where the C call failed; the Python function that raises it.
+struct Failed {
+    int status;
+    const char *call;
+};
+PyObject *p_check;
+
+inline void done(int status, const char *call)
+{
+    if (status == W4_ERR_INVALID_ARG || status == W4_ERR_UNSUPPORTED || status == W4_ERR_MISALIGNED)
+        throw Unusual();
+    if (status != W4_OK)
+        throw Failed{status, call};
 }
 
 // A plain tensor (not a subclass) in memory.
@@ -214,10 +230,11 @@ PyObject *lora(PyObject *const *a)
     const int m = to_int(M), n = to_int(N), k = to_int(K), r = to_int(R), l = to_int(L);
     const at::Tensor out = output(a[6], {M, N}, y, at::kFloat);
     const int64_t ldo = matrix(out, c, at::kFloat, M, N);
-    need(p_lora(static_cast<float *>(out.data_ptr()), static_cast<const float *>(y.const_data_ptr()),
+    done(p_lora(static_cast<float *>(out.data_ptr()), static_cast<const float *>(y.const_data_ptr()),
                 static_cast<const uint16_t *>(x.const_data_ptr()), static_cast<const uint16_t *>(la.const_data_ptr()),
                 static_cast<const uint16_t *>(lb.const_data_ptr()), ids, scale, m, n, k, r, l, ldo, ldy, ldx, status,
-                c.stream) == W4_OK);
+                c.stream),
+         "w4_lora");
     return give(a[6], out);
 }
 
@@ -272,9 +289,10 @@ PyObject *rope(PyObject *const *a)
     }
     const at::Tensor qo = output(a[8], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldqo = rows_of(qo, c, at::kBFloat16, M, Hq, D);
-    need(p_rope(static_cast<uint16_t *>(qo.data_ptr()), kp ? static_cast<uint16_t *>(ko.data_ptr()) : nullptr,
+    done(p_rope(static_cast<uint16_t *>(qo.data_ptr()), kp ? static_cast<uint16_t *>(ko.data_ptr()) : nullptr,
                 q.const_data_ptr(), kp, qw, kw, f, pos, m, hq, (int)Hkv, d, R, ldq, ldk, ldqo, ldko, f32, pairs, eps,
-                c.stream) == W4_OK);
+                c.stream),
+         "w4_qk_norm_rope");
     PyObject *first = give(a[8], qo);
     PyObject *second = Py_None;
     if (kp)
@@ -310,9 +328,10 @@ PyObject *qkv(PyObject *const *a)
     const int m = to_int(M), hq = to_int(Hq), hkv = to_int(Hkv), d = to_int(D);
     const at::Tensor qo = output(a[14], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldqo = rows_of(qo, c, at::kBFloat16, M, Hq, D);
-    need(p_qkv(static_cast<uint16_t *>(qo.data_ptr()), p.k, p.v, q.const_data_ptr(), k.const_data_ptr(),
+    done(p_qkv(static_cast<uint16_t *>(qo.data_ptr()), p.k, p.v, q.const_data_ptr(), k.const_data_ptr(),
                v.const_data_ptr(), qw, kw, vw, f, b.table, b.lens, b.cu, b.B, m, hq, hkv, d, R, p.pages, p.page, b.n, ldq,
-               ldk, ldv, ldqo, p.ps, p.rs, p.hs, f32, pairs, eps, status, c.stream) == W4_OK);
+               ldk, ldv, ldqo, p.ps, p.rs, p.hs, f32, pairs, eps, status, c.stream),
+         "w4_qkv_paged");
     return give(a[14], qo);
 }
 
@@ -334,9 +353,10 @@ PyObject *attn(PyObject *const *a)
     const int m = to_int(M), hq = to_int(Hq), hkv = to_int(Hkv), d = to_int(D);
     const at::Tensor out = output(a[8], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldo = rows_of(out, c, at::kBFloat16, M, Hq, D);
-    need(p_attn(static_cast<uint16_t *>(out.data_ptr()), static_cast<const uint16_t *>(q.const_data_ptr()), p.k, p.v,
+    done(p_attn(static_cast<uint16_t *>(out.data_ptr()), static_cast<const uint16_t *>(q.const_data_ptr()), p.k, p.v,
                 b.table, b.lens, b.cu, b.B, m, hq, hkv, d, p.pages, p.page, b.n, ldq, ldo, p.ps, p.rs, p.hs, window, scale,
-                c.stream) == W4_OK);
+                c.stream),
+         "w4_attn_paged");
     return give(a[8], out);
 }
 
@@ -347,6 +367,14 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
         try {
             return F(args);
         } catch (const Unusual &) {
+        } catch (const Failed &f) {
+            PyErr_Clear();
+            PyObject *r = PyObject_CallFunction(p_check, "is", f.status, f.call);
+            if (r) { // it raises
+                Py_DECREF(r);
+                PyErr_SetString(PyExc_RuntimeError, f.call);
+            }
+            return nullptr;
         } catch (...) { // the Python code meets it again and says what it is
         }
         PyErr_Clear();
@@ -354,11 +382,12 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
-// The library's functions, by address.
+// The library's functions, by address, and at the first time the Python function that raises
+// their errors (status, name).
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+    if (n != 5 && !(n == 4 && p_check)) {
+        PyErr_SetString(PyExc_TypeError, "bind takes four addresses and a function");
         return nullptr;
     }
     void *p[4];
@@ -371,6 +400,11 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n)
     p_rope = reinterpret_cast<decltype(p_rope)>(p[1]);
     p_qkv = reinterpret_cast<decltype(p_qkv)>(p[2]);
     p_attn = reinterpret_cast<decltype(p_attn)>(p[3]);
+    if (n == 5) {
+        Py_INCREF(args[4]);
+        Py_XDECREF(p_check);
+        p_check = args[4];
+    }
     Py_RETURN_NONE;
 }
 

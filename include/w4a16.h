@@ -19,7 +19,9 @@
  *     stream). Calls only enqueue work on `stream` and return; nothing is
  *     complete until the caller synchronizes that stream.
  *   - Arguments are validated on the host before anything is launched. A call
- *     that returns an error launched nothing.
+ *     that returns an error other than W4_ERR_CUDA launched nothing. After W4_ERR_CUDA
+ *     a part of the call may have been launched: its outputs are not valid, and a call
+ *     in place is not to be made again on them.
  *   - Results are bitwise deterministic run to run (no floating-point atomics).
  *   - All calls are safe to capture in a CUDA graph once the library has been
  *     initialised on the device (w4_init, or any earlier call on that device).
