@@ -46,8 +46,15 @@ struct Failed {
 };
 PyObject *p_check;
 
-inline void done(int status, const char *call)
+// Makes the call. Other Python threads run meanwhile: a launch may wait for room in its
+// stream's queue, whose work may wait for a host function that needs the interpreter.
+template <typename F, typename... A>
+void make(const char *call, F f, A... args)
 {
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = f(args...);
+    Py_END_ALLOW_THREADS
     if (status == W4_ERR_INVALID_ARG || status == W4_ERR_UNSUPPORTED || status == W4_ERR_MISALIGNED)
         throw Unusual();
     if (status != W4_OK)
@@ -230,11 +237,10 @@ PyObject *lora(PyObject *const *a)
     const int m = to_int(M), n = to_int(N), k = to_int(K), r = to_int(R), l = to_int(L);
     const at::Tensor out = output(a[6], {M, N}, y, at::kFloat);
     const int64_t ldo = matrix(out, c, at::kFloat, M, N);
-    done(p_lora(static_cast<float *>(out.data_ptr()), static_cast<const float *>(y.const_data_ptr()),
-                static_cast<const uint16_t *>(x.const_data_ptr()), static_cast<const uint16_t *>(la.const_data_ptr()),
-                static_cast<const uint16_t *>(lb.const_data_ptr()), ids, scale, m, n, k, r, l, ldo, ldy, ldx, status,
-                c.stream),
-         "w4_lora");
+    make("w4_lora", p_lora, static_cast<float *>(out.data_ptr()), static_cast<const float *>(y.const_data_ptr()),
+         static_cast<const uint16_t *>(x.const_data_ptr()), static_cast<const uint16_t *>(la.const_data_ptr()),
+         static_cast<const uint16_t *>(lb.const_data_ptr()), ids, scale, m, n, k, r, l, ldo, ldy, ldx, status,
+         c.stream);
     return give(a[6], out);
 }
 
@@ -289,10 +295,9 @@ PyObject *rope(PyObject *const *a)
     }
     const at::Tensor qo = output(a[8], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldqo = rows_of(qo, c, at::kBFloat16, M, Hq, D);
-    done(p_rope(static_cast<uint16_t *>(qo.data_ptr()), kp ? static_cast<uint16_t *>(ko.data_ptr()) : nullptr,
-                q.const_data_ptr(), kp, qw, kw, f, pos, m, hq, (int)Hkv, d, R, ldq, ldk, ldqo, ldko, f32, pairs, eps,
-                c.stream),
-         "w4_qk_norm_rope");
+    make("w4_qk_norm_rope", p_rope, static_cast<uint16_t *>(qo.data_ptr()),
+         kp ? static_cast<uint16_t *>(ko.data_ptr()) : nullptr, q.const_data_ptr(), kp, qw, kw, f, pos, m, hq,
+         (int)Hkv, d, R, ldq, ldk, ldqo, ldko, f32, pairs, eps, c.stream);
     PyObject *first = give(a[8], qo);
     PyObject *second = Py_None;
     if (kp)
@@ -328,10 +333,9 @@ PyObject *qkv(PyObject *const *a)
     const int m = to_int(M), hq = to_int(Hq), hkv = to_int(Hkv), d = to_int(D);
     const at::Tensor qo = output(a[14], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldqo = rows_of(qo, c, at::kBFloat16, M, Hq, D);
-    done(p_qkv(static_cast<uint16_t *>(qo.data_ptr()), p.k, p.v, q.const_data_ptr(), k.const_data_ptr(),
-               v.const_data_ptr(), qw, kw, vw, f, b.table, b.lens, b.cu, b.B, m, hq, hkv, d, R, p.pages, p.page, b.n, ldq,
-               ldk, ldv, ldqo, p.ps, p.rs, p.hs, f32, pairs, eps, status, c.stream),
-         "w4_qkv_paged");
+    make("w4_qkv_paged", p_qkv, static_cast<uint16_t *>(qo.data_ptr()), p.k, p.v, q.const_data_ptr(),
+         k.const_data_ptr(), v.const_data_ptr(), qw, kw, vw, f, b.table, b.lens, b.cu, b.B, m, hq, hkv, d, R, p.pages,
+         p.page, b.n, ldq, ldk, ldv, ldqo, p.ps, p.rs, p.hs, f32, pairs, eps, status, c.stream);
     return give(a[14], qo);
 }
 
@@ -353,10 +357,9 @@ PyObject *attn(PyObject *const *a)
     const int m = to_int(M), hq = to_int(Hq), hkv = to_int(Hkv), d = to_int(D);
     const at::Tensor out = output(a[8], {M, Hq, D}, q, at::kBFloat16);
     const int64_t ldo = rows_of(out, c, at::kBFloat16, M, Hq, D);
-    done(p_attn(static_cast<uint16_t *>(out.data_ptr()), static_cast<const uint16_t *>(q.const_data_ptr()), p.k, p.v,
-                b.table, b.lens, b.cu, b.B, m, hq, hkv, d, p.pages, p.page, b.n, ldq, ldo, p.ps, p.rs, p.hs, window, scale,
-                c.stream),
-         "w4_attn_paged");
+    make("w4_attn_paged", p_attn, static_cast<uint16_t *>(out.data_ptr()),
+         static_cast<const uint16_t *>(q.const_data_ptr()), p.k, p.v, b.table, b.lens, b.cu, b.B, m, hq, hkv, d,
+         p.pages, p.page, b.n, ldq, ldo, p.ps, p.rs, p.hs, window, scale, c.stream);
     return give(a[8], out);
 }
 
