@@ -5,7 +5,10 @@
 //   out[m][n] = y[m][n] + sum_r b[i][n][r] h[m][r]
 // h goes to the second product as three bf16 parts, each the rounding of what those
 // before it leave (within 2^-25 of h, as fp32 is): y and out are fp32, and two parts
-// (2^-17) were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32.
+// (2^-17) were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32. b h
+// is summed apart and added to y once: products added to y in the tensor core lose up to a
+// step of y each (6 at R <= 32, 24 at 128: errors of 1.8, 3.6 and 2.5 10^-7 of out for 1 row
+// at R = 16, 61 at 64 and 4001 at 32, which are 0.5, 0.9 and 1.9 now, at the same times).
 //
 // In both forms the second product's operands come straight from global memory: within
 // 32 elements of the summed dimension a thread holds 8 consecutive ones (both operands in
@@ -360,6 +363,12 @@ lora_group_kernel(const Args a, const int groups)
     if (!EARLY && n0 < p.N)
         ask(n0);
     for (; n0 < p.N; n0 += step) {
+        float d[4][4]; // b h, added to y once
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                d[j][i] = 0.f;
         if (id >= 0) {
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
@@ -373,15 +382,14 @@ lora_group_kernel(const Args a, const int groups)
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int t = 2; t >= 0; --t) // small parts first
-                        mma32(c[j], h[t][0], h[t][1], b[k][j]);
+                        mma32(d[j], h[t][0], h[t][1], b[k][j]);
             }
         }
-        float d[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                d[j][i] = c[j][i];
+                d[j][i] = id >= 0 ? c[j][i] + d[j][i] : c[j][i]; // (without an adapter y's bits, -0 too)
         const int at = n0 + 4 * tq;
         const bool in0 = at < p.N, in1 = at + 16 < p.N;
         if (n0 + step < p.N)
@@ -631,12 +639,12 @@ lora_up_kernel(const Args a)
                     load_b<NS>(b, p, mine, n0);
                     have = mine;
                 }
-                float d[4][4];
+                float d[4][4]; // b h, added to y once
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        d[j][k] = c[u][j][k];
+                        d[j][k] = 0.f;
 #pragma unroll
                 for (int k = 0; k < NS; ++k) {
                     uint4 h[3][2];
@@ -657,7 +665,7 @@ lora_up_kernel(const Args a)
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        c[u][j][k] = (k < 2 ? ok0 : ok1) ? d[j][k] : c[u][j][k];
+                        c[u][j][k] = (k < 2 ? ok0 : ok1) ? c[u][j][k] + d[j][k] : c[u][j][k];
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q)

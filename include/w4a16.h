@@ -429,7 +429,9 @@ int w4_kv_commit(uint16_t *k_cache, uint16_t *v_cache, int32_t *kpos, const uint
  *   R a multiple of 8 in 8..128 (adapters of lower rank have rows of zeros), K a multiple
  *   of 32, N of 8 and at most 2^23; M, L >= 1; ldx a multiple of 8, ldo and ldy of 4.
  *   16-byte aligned pointers, ids, scale and status 4-byte.
- * Sums in fp32; a x is carried to the second product as three bf16 parts (2^-25). Any
+ * Sums in fp32, the adapter's added to y once (one rounding of out); a x is carried to the
+ * second product as three bf16 parts (2^-24). Finite x, a and b, with a x below 3.3 10^38: an
+ * infinity leaves NaN or infinities in the rows that meet it. Any
  * order of ids is served; past 512 rows those of one request should lie together (a
  * tile of 64 rows takes its adapters in turn). Uses the library's split scratch:
  * calls that need it must not run concurrently on different streams.
