@@ -6,6 +6,8 @@ whose caches share one pool of pages, with low-rank adapters beside the projecti
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 from .draft import attend
@@ -19,6 +21,20 @@ def norm(x, weight, eps):
     return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
 
 
+_TWO_PI = Fraction("6.283185307179586476925286766559005768394338798750211641949889184615632812572417997256")
+_BITS = 160
+
+
+def angle(pos, inv_freq):
+    """pos [M] * inv_freq [h] (fp32) without its whole turns, from -pi to pi. A frequency is a whole number of
+    2^-160 turns (off by half of one), so whole turns of its multiples drop out exactly."""
+    one = 1 << _BITS
+    f = np.array([round(Fraction(float(x)) * one / _TWO_PI) for x in np.asarray(inv_freq, np.float32)], object)
+    t = np.array([int(p) for p in np.asarray(pos)], object)[:, None] * f[None, :]
+    t = (t + one // 2) % one - one // 2
+    return 2 * np.pi * (t / one).astype(np.float64)
+
+
 def turn(u, pos, inv_freq, pairs):
     """(turned, size) of heads u [M][H][D] at positions pos [M]: size = |a| + |b| of the
     pair that an element belongs to, |u| where it is not turned."""
@@ -27,11 +43,8 @@ def turn(u, pos, inv_freq, pairs):
     if inv_freq is None or len(inv_freq) == 0:
         return out, size
     h = len(inv_freq)
-    f = np.asarray(inv_freq, np.float32).astype(np.float64)
-    # Whole turns leave no rounding behind in extended precision (64-bit significands).
-    t = np.asarray(pos, np.longdouble)[:, None] * f.astype(np.longdouble)[None, :]
-    t = np.remainder(t, 2 * np.longdouble("3.14159265358979323846264338327950288"))
-    c, s = np.cos(t).astype(np.float64)[:, None], np.sin(t).astype(np.float64)[:, None]
+    t = angle(pos, inv_freq)
+    c, s = np.cos(t)[:, None], np.sin(t)[:, None]
     i = np.arange(h) * (2 if pairs else 1)
     j = i + (1 if pairs else h)
     a, b = u[..., i], u[..., j]
