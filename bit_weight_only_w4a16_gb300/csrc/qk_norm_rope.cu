@@ -14,9 +14,11 @@
 //
 // The angle. pos * freq_j in fp32 would be off by 2^-24 of itself: 0.008 radians at
 // position 131072. Turns are counted in integers instead: freq_j / 2 pi is formed as a
-// 64-bit fraction of a turn (the fp32 frequency's 24-bit significand times 2^66 / 2 pi,
-// shifted), and the 64-bit product with the position drops whole turns by itself.
-// Its upper 32 bits are the angle, within 2^-32 of a turn for every position.
+// 64-bit fraction of a turn (the fp32 frequency's 24-bit significand times 96 bits of
+// 1 / 2 pi, shifted; 64 bits of it left 2^-17 of a turn at frequencies near 2^24), and the
+// 64-bit product with the position drops whole turns by itself. Its upper 32 bits are the
+// angle, within 2^-31 of a turn for every position and frequency below 2^24; in half turns
+// as fp32 it is within 2^-26 of a turn, fp32's own step near a half turn.
 //
 // Work. A group of D / 8 lanes (32 at most) has a token and some of its heads; a lane holds
 // both halves of four pairs (8 elements, two 16-byte loads of fp32), so the turn needs no
@@ -37,16 +39,18 @@ namespace {
 constexpr int kThreads = 256;
 
 // Fraction of a turn that freq radians are, in units of 2^-64 (whole turns drop out).
-// freq = m 2^e with a 24-bit m; 2^66 / (2 pi) in 64 bits is 0xA2F9836E4E44152A
-// (the leading bits of 2 / pi), so the fraction is m * that, shifted by e - 2.
+// freq = m 2^e with a 24-bit m; 2^66 / (2 pi) is 0xA2F9836E4E441529.FC2757D1 (the leading
+// bits of 2 / pi), so the fraction is m * that, shifted by e - 2.
 __device__ __forceinline__ unsigned long long turn_of(float freq)
 {
     const uint32_t b = __float_as_uint(freq);
     const int ex = (int)((b >> 23) & 0xFFu);
-    const unsigned long long m = (b & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
+    const uint32_t m = (b & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
     const int s = 2 - ((ex ? ex : 1) - 150); // right shift of the 128-bit product
-    const unsigned long long c = 0xA2F9836E4E44152Aull;
-    const unsigned long long lo = m * c, hi = __umul64hi(m, c);
+    // In words of 32 bits, none of whose sums overflows; what is below the point loses its last word.
+    const unsigned long long p0 = (unsigned long long)m * 0x4E441529u + __umulhi(m, 0xFC2757D1u);
+    const unsigned long long p1 = (unsigned long long)m * 0xA2F9836Eu + (p0 >> 32);
+    const unsigned long long lo = (p1 << 32) | (uint32_t)p0, hi = p1 >> 32;
     unsigned long long f;
     if (s <= 0)
         f = s > -64 ? lo << -s : 0ull;

@@ -459,8 +459,8 @@ int w4_lora(float *out, const float *y, const uint16_t *x, const uint16_t *a, co
  *   may be NULL); eps >= 0. 16-byte aligned pointers (int32 and inv_freq 4-byte), ld*
  *   multiples of 8.
  * Norm and turn in fp32 (squares are added in fp32: elements up to about 10^18), one
- * rounding to bf16. The angle is exact to 2^-32 of a turn
- * for the fp32 inv_freq at every position (whole turns are dropped in integers).
+ * rounding to bf16. The angle is within 2^-26 of a turn for the fp32 inv_freq at every
+ * position (whole turns are dropped in integers, to 2^-31; then fp32).
  */
 int w4_qk_norm_rope(uint16_t *q_out, uint16_t *k_out, const void *q, const void *k, const float *q_weight,
                     const float *k_weight, const float *inv_freq, const int32_t *pos, int M, int Hq, int Hkv, int D,
