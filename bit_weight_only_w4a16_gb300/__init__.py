@@ -13,9 +13,12 @@ first, zero point 8), scales bf16 [N][K/32], x bf16 [M][K], y fp32 [M][N].
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
+
+from . import build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a16.so")
@@ -109,9 +112,14 @@ def _check(rc: int, call: str):
 
 
 def _load_binding():
-    """The serving calls' native checks (csrc/binding.cpp), or None."""
+    """The serving calls' native checks (csrc/binding.cpp), built for this torch and this Python, or None."""
+    path = build.binding_path()
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
     try:
-        from . import _binding
+        _binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_binding)
     except ImportError:
         return None
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in

@@ -1,5 +1,5 @@
 """Build libw4a16.so in-tree with nvcc for sm_103a (no cmake; parallel objects), and the
-serving calls' native binding _binding.so with g++ against the installed torch."""
+serving calls' native binding with g++ against the installed torch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,7 +14,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libw4a16.so")
-BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,18 +44,31 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_path() -> str:
+    """The native binding for this torch and this Python: it uses the layout of their objects, so one that
+    was built for others has another name and is neither current nor loaded."""
+    import torch
+    git = (torch.version.git_version or "")[:10]
+    return os.path.join(HERE, f"_binding.{torch.__version__}.{git}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def binding_current() -> bool:
+    path = binding_path()
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in
+                                        (os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "w4a16.h")))
+
+
 def build_binding(force: bool = False):
-    """_binding.so, or None where it cannot be built (the Python binding is complete
-    without it; only the host time of the serving calls is longer)."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (src, os.path.join(INCLUDE, "w4a16.h"))):
-        return BINDING
+    """The native binding's path, or None where it cannot be built (the Python binding is
+    complete without it; only the host time of the serving calls is longer)."""
     try:
         import torch
+        if not force and binding_current():
+            return binding_path()
+        src, path = os.path.join(CSRC, "binding.cpp"), binding_path()
         base = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(_nvcc()))
-        tmp = BINDING + ".tmp"
+        tmp = path + ".tmp"
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I", os.path.join(base, "include"),
                "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I",
                sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
@@ -65,8 +77,8 @@ def build_binding(force: bool = False):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr[-2000:])
-        os.replace(tmp, BINDING)
-        return BINDING
+        os.replace(tmp, path)
+        return path
     except Exception as e:  # noqa: BLE001
         print(f"the native binding was not built: {e}", file=sys.stderr)
         return None
