@@ -4,8 +4,8 @@
 //   h[m][r] = scale[i] sum_k a[i][r][k] x[m][k]            r < R <= 128
 //   out[m][n] = y[m][n] + sum_r b[i][n][r] h[m][r]
 // h goes to the second product as three bf16 parts, each the rounding of what those
-// before it leave (within 2^-25 of h, as fp32 is): y and out are fp32, and two parts
-// (2^-17) were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32. b h
+// before it leave (within 2^-24 of h, as fp32 is): y and out are fp32, and two parts
+// (2^-16) were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32. b h
 // is summed apart and added to y once: products added to y in the tensor core lose up to a
 // step of y each (6 at R <= 32, 24 at 128: errors of 1.8, 3.6 and 2.5 10^-7 of out for 1 row
 // at R = 16, 61 at 64 and 4001 at 32, which are 0.5, 0.9 and 1.9 now, at the same times).
@@ -780,7 +780,7 @@ cudaError_t run_lora(const LoraArgs &p, float *ws, size_t ws_floats, int num_sms
     int parts = 1;
     while (parts < 8 && all * parts * 2 <= 2ll * num_sms && parts * 512 < p.K)
         parts *= 2;
-    // Rows whose partial sums fit the scratch go in one pass (82000 at R = 128).
+    // Rows whose partial sums fit the scratch go in one pass (79040 at R = 128 on 152 SMs).
     const long long most = (long long)(ws_floats / ((size_t)p.R * parts)) / 64 * 64;
     for (long long m0 = 0; m0 < p.M; m0 += most) {
         Args a = {};
