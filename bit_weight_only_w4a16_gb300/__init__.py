@@ -686,7 +686,8 @@ def w4_qkv_paged(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q=None, q_
     k_pages, v_pages bf16 [pages][page][Hkv][D] (strided views alike); table int32
     [B][n]: the pages of each sequence in order; lens int32 [B]: positions of each with
     its new tokens, which are the last; cu_q int32 [B + 1]: the sequences' first rows,
-    or None: row b is sequence b's. A token without a page sets status (int32 [1]).
+    or None: row b is sequence b's. A token without a page sets status (int32 [1]). Rows
+    of no sequence (a padded batch's last) are not written: in a new q_out they hold anything.
     """
     if _fast is not None:
         r = _fast.qkv(q, k, v, k_pages, v_pages, table, lens, inv_freq, cu_q, q_weight, k_weight, v_weight, eps, pairs,
@@ -725,8 +726,8 @@ def w4_attn_paged(q, k_pages, v_pages, table, lens, cu_q=None, window: int = 0, 
     sequence when cu_q is None) over a paged cache that holds their keys already.
 
     q bf16 [total_q][Hq][D] (rows may be strided); pages, table, lens and cu_q as
-    w4_qkv_paged; window 0 = no window. Uses the library's split scratch: no other call
-    that does may overlap in time.
+    w4_qkv_paged; window 0 = no window. Rows of no sequence are not written. Uses the
+    library's split scratch: no other call that does may overlap in time.
     """
     if _fast is not None:
         r = _fast.attn(q, k_pages, v_pages, table, lens, cu_q, window, scale, out, stream)

@@ -7,7 +7,7 @@
 //
 // Mathematics as in attn_tiles.cuh: out = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m), with m
 // moved only when the maximum has grown by more than 2^8. A weight goes to the value
-// product as two bf16 parts (within 2^-17 of it). Sums are fp32.
+// product as two bf16 parts (within 2^-16 of it). Sums are fp32.
 //
 // Why not the tiles of attn_tiles.cuh: a row tile there has 128 rows, of which one token
 // with its G heads fills G, and its scores, weights and product follow one another

@@ -509,7 +509,9 @@ int w4_qkv_paged(uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages, const vo
  *   Hq / Hkv, D, scale, masked values, tiles and scratch (no concurrent calls) as
  *   w4_attn_prompt.
  * Precision as w4_attn_prompt; single tokens (cu_q NULL, up to 8 heads on one, 16 at D <=
- * 256) carry their weights as two bf16 parts (2^-16). A kept value that is infinite leaves
+ * 256) carry their weights as two bf16 parts (2^-16), the same token in a packed call (cu_q) as one
+ * (2^-8). What is launched for single tokens follows from table_pages and window, not from lens: a
+ * table much wider than the lengths costs one or two us. A kept value that is infinite leaves
  * infinity or NaN in its column of the rows that keep it.
  */
 int w4_attn_paged(uint16_t *out, const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
