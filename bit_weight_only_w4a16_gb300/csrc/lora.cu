@@ -6,9 +6,10 @@
 // h goes to the second product as three bf16 parts, each the rounding of what those
 // before it leave (within 2^-24 of h, as fp32 is): y and out are fp32, and two parts
 // (2^-16) were their largest error (10^-6 of out where the sums' is 10^-7). Sums are fp32. b h
-// is summed apart and added to y once: products added to y in the tensor core lose up to a
-// step of y each (6 at R <= 32, 24 at 128: errors of 1.8, 3.6 and 2.5 10^-7 of out for 1 row
-// at R = 16, 61 at 64 and 4001 at 32, which are 0.5, 0.9 and 1.9 now, at the same times).
+// is summed apart, small parts of all R first, and added to y once: the tensor core cuts each
+// sum to a step of its own size. Errors of out for 1 row at R = 16, 61 at 64 and 4001 at 32,
+// in 10^-7: products added to y 1.8, 3.6, 2.5; apart 0.4, 0.9, 2.0; small parts first 0.4, 0.6,
+// 2.0 (at R = 128 2.1 -> 0.8 of 37 rows), at the same times; a plain fp32 sum 0.3, 1.4, 2.1.
 //
 // In both forms the second product's operands come straight from global memory: within
 // 32 elements of the summed dimension a thread holds 8 consecutive ones (both operands in
@@ -371,19 +372,17 @@ lora_group_kernel(const Args a, const int groups)
                 d[j][i] = 0.f;
         if (id >= 0) {
 #pragma unroll
-            for (int k = 0; k < NS; ++k) {
-                uint4 h[3][2];
+            for (int t = 2; t >= 0; --t) // all small parts first
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
+                for (int k = 0; k < NS; ++k) {
+                    uint4 h[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
-                        h[t][q] = lds128(smem_addr(hs + (size_t)(t * 16 + g + 8 * q) * HP + 32 * k + 8 * tq));
+                        h[q] = lds128(smem_addr(hs + (size_t)(t * 16 + g + 8 * q) * HP + 32 * k + 8 * tq));
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int t = 2; t >= 0; --t) // small parts first
-                        mma32(d[j], h[t][0], h[t][1], b[k][j]);
-            }
+                    for (int j = 0; j < 4; ++j)
+                        mma32(d[j], h[0], h[1], b[k][j]);
+                }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -549,6 +548,7 @@ lora_up_kernel(const Args a)
 {
     constexpr int TR = 64, RB = TR / 16, RU = 2;               // row blocks; in flight
     constexpr int HP = 32 * NS + 8;                            // elements between rows of h
+    constexpr int AT = NS == 1 ? 3 : 1;                        // parts of h read together (one at a time: 29.7 us for 28.7)
     extern __shared__ __align__(16) __nv_bfloat16 hs_[];       // [3][TR][HP]
     __shared__ int s_id[TR];
     const LoraArgs &p = a.p;
@@ -646,19 +646,22 @@ lora_up_kernel(const Args a)
                     for (int k = 0; k < 4; ++k)
                         d[j][k] = 0.f;
 #pragma unroll
-                for (int k = 0; k < NS; ++k) {
-                    uint4 h[3][2];
+                for (int t0 = 2; t0 >= 0; t0 -= AT) // all small parts first
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)
+                    for (int k = 0; k < NS; ++k) {
+                        uint4 h[AT][2];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            h[t][q] = lds128(smem_addr(hs_ + (size_t)(t * TR + i + 8 * q + g) * HP + 32 * k + 8 * tq));
+                        for (int t = 0; t < AT; ++t)
 #pragma unroll
-                    for (int t = 2; t >= 0; --t) // small parts first
+                            for (int q = 0; q < 2; ++q)
+                                h[t][q] = lds128(
+                                    smem_addr(hs_ + (size_t)((t0 - t) * TR + i + 8 * q + g) * HP + 32 * k + 8 * tq));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma32(d[j], h[t][0], h[t][1], b[k][j]);
-                }
+                        for (int t = 0; t < AT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma32(d[j], h[t][0], h[t][1], b[k][j]);
+                    }
                 // Rows of other adapters stay as they were.
                 const bool ok0 = (its >> (from + g)) & 1, ok1 = (its >> (from + g + 8)) & 1;
 #pragma unroll
