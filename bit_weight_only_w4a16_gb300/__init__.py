@@ -7,6 +7,11 @@ tensors on the current device; bf16 data may be passed either as torch.bfloat16
 or as raw int16/uint16 bits. There is no CPU path: if the compiled library is
 missing, importing the binding raises.
 
+A call runs on `stream` (the current one where none is given). An output that it
+makes is memory of the current stream: with another `stream`, let that wait for the
+current one before the call, and the current one for it before the output is used
+or dropped.
+
 Weight format: qweight uint32 [N][K/8] (8 codes per word along K, low nibble
 first, zero point 8), scales bf16 [N][K/32], x bf16 [M][K], y fp32 [M][N].
 """
